@@ -340,6 +340,143 @@ int idx_topk_decode_paged_noalloc(const uint8_t *q, const float *q_scale, const 
                                   int32_t page_size, int32_t num_pages, int32_t K, int32_t *out_idx,
                                   void *stream);
 
+/*
+ * ------------------------------------------------------------------------
+ * Operators around the indexer: the attention that consumes its lists, the
+ * caches it reads, and the e4m3 operands it takes.  The conventions above hold
+ * for them too, with these differences: their 16-bit tensors are bfloat16 or
+ * half (`dtype`), and input strides are given in numbers, non-negative
+ * multiples of 8, with unit stride along the last dimension; base pointers of
+ * 16-bit tensors are 16-byte aligned.
+ *
+ * A latent row is 512 latent numbers, shared by all heads as key and as value,
+ * followed by 64 rotary numbers that are key only.
+ */
+#define IDX_TOPK_LATENT 512
+#define IDX_TOPK_ROPE 64
+#define IDX_TOPK_NOPE 128   /* expanded form: per-head key width beside the rotary part */
+#define IDX_TOPK_VALUE 128  /* expanded form: per-head value width                      */
+#define IDX_TOPK_MAX_ATTN_HEADS 128
+#define IDX_TOPK_MAX_STEPS 16
+
+#define IDX_TOPK_BF16 0
+#define IDX_TOPK_F16 1
+
+/* Bytes of workspace idx_topk_latent_selected needs (0 for arguments it rejects). */
+size_t idx_topk_latent_selected_workspace(int32_t T, int32_t H, int32_t K);
+
+/*
+ * Latent attention over listed slots (absorbed form).  For every token t and head h
+ *   x[i]   = scale * q[t,h,:] . cache[slots[t,i],:]           (576 numbers)
+ *   o[t,h] = sum_i softmax_i(x) * cache[slots[t,i], 0:512],   lse[t,h] = log sum_i exp(x[i])
+ * over the entries of row t of `slots` that lie in [0, num_slots); others (the -1 padding of
+ * idx_topk_prefill and idx_topk_decode_paged, anywhere in the row) are skipped and nothing is
+ * read for them.  A slot that is listed twice counts twice.  A row without entries gives o = 0
+ * and lse = -inf.
+ *   q         [T][H][576], strides q_token, q_head
+ *   cache     [num_slots][576] contiguous; any number of slots (64-bit offsets)
+ *   slots     [T][K] int32, K in 1..2048
+ *   H         1..128
+ *   scale     finite and > 0
+ *   out       [T][H][512] in `dtype`, 16-byte aligned
+ *   lse       [T][H] float or NULL
+ * Sums and softmax statistics are FP32; the softmax weights are rounded to `dtype` for the
+ * matrix cores.  The result does not depend on timing (no atomics on numbers).
+ */
+int idx_topk_latent_selected(const void *q, int64_t q_token, int64_t q_head, const void *cache,
+                             int64_t num_slots, const int32_t *slots, int32_t K, int32_t T, int32_t H,
+                             float scale, int32_t dtype, void *out, float *lse, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace idx_topk_latent_paged needs (0 for arguments it rejects). */
+size_t idx_topk_latent_paged_workspace(int32_t B, int32_t S, int32_t H, int32_t max_pages);
+
+/*
+ * Latent attention over whole paged sequences (absorbed form): the S last tokens of each of B
+ * sequences (S = 1: one decode step; more: speculated tokens), step j of sequence b seeing the
+ * keys at logical positions below seq_lens[b] - S + 1 + j.
+ *   q          [B][S][H][576], strides q_seq, q_token, q_head;  S in 1..16, H in 1..128
+ *   cache      [num_pages][64][576] contiguous
+ *   page_table [B][max_pages] int32 physical page ids
+ *   seq_lens   [B] int32 (device), S's own tokens included; a length outside
+ *              [0, max_pages * 64] is taken as 0
+ *   out        [B][S][H][512], lse [B][S][H] float or NULL
+ * Keys in pages whose id lies outside [0, num_pages) are skipped, as are cache slots past a
+ * sequence's length (they may hold anything).  A step that sees no key gives o = 0 and
+ * lse = -inf.
+ */
+int idx_topk_latent_paged(const void *q, int64_t q_seq, int64_t q_token, int64_t q_head,
+                          const void *cache, int32_t num_pages, const int32_t *page_table,
+                          int32_t max_pages, const int32_t *seq_lens, int32_t B, int32_t S, int32_t H,
+                          float scale, int32_t dtype, void *out, float *lse, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace idx_topk_latent_expanded needs (0 for arguments it rejects). */
+size_t idx_topk_latent_expanded_workspace(int32_t Tq, int32_t B, int32_t max_q, int32_t max_k, int32_t H);
+
+/*
+ * Latent attention, expanded form: per-head keys and values have been computed from the latent
+ * rows (kv), the rotary part of the keys is shared by the heads.  B packed prompts: prompt b
+ * has the query tokens cu_q[b] .. cu_q[b+1] and the keys cu_k[b] .. cu_k[b+1].
+ *   x[i,j] = scale * (q[i,h,0:128] . kv[j,h,0:128] + q[i,h,128:192] . k_rope[j,:])
+ *   o[i,h] = sum_j softmax_j(x) kv[j,h,128:256]
+ * causal != 0: query i of Lq sees keys j <= i + Lk - Lq of Lk (the prompt's last tokens are the
+ * queries); causal = 0: all keys.  A query that sees no key gives o = 0 and lse = -inf.
+ *   q         [Tq][H][192], strides q_token, q_head
+ *   kv        [Tk][H][256] (key part, then value), strides kv_token, kv_head
+ *   k_rope    [Tk][64], stride rope_token
+ *   cu_q      [B+1] int32 device, cu_k [B+1] int32 device: running token counts.  A prompt whose
+ *             range is not within [0, Tq] or [0, Tk] is skipped (its output is not written)
+ *   max_q     at least the longest prompt's query tokens (queries past it are not computed),
+ *   max_k     about the longest prompt's keys (only sizes the launch); B at most 65535
+ *   out       [Tq][H][128], lse [Tq][H] float or NULL
+ * A key's numbers must be finite if any query of its prompt sees it.
+ */
+int idx_topk_latent_expanded(const void *q, int64_t q_token, int64_t q_head, const void *kv,
+                             int64_t kv_token, int64_t kv_head, const void *k_rope, int64_t rope_token,
+                             const int32_t *cu_q, const int32_t *cu_k, int32_t B, int32_t Tq, int32_t Tk,
+                             int32_t max_q, int32_t max_k, int32_t H, float scale, int32_t causal,
+                             int32_t dtype, void *out, float *lse, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, quantised to e4m3:
+ *   h = x + residual,  y = h * rsqrt(mean(h^2) + eps) * weight      (FP32, per row)
+ *   scale = max|y| / 448 over each group of a row (1 where the group is all zero),
+ *   codes = nearest e4m3fn of y / scale (ties to even)
+ * With rows of 128 numbers and group 0 the outputs are q and q_scale (or k and k_scale) of
+ * idx_topk_prefill and idx_topk_decode_paged.
+ *   x         [rows][width], row stride x_stride
+ *   residual  NULL or [rows][width], row stride residual_stride
+ *   weight    NULL (all ones) or [width] in `dtype`
+ *   width     1..16384; group 0 (one scale a row) or 128 (width a multiple of 128)
+ *   codes     [rows][width] uint8, scales [rows][width / group] float (group 0: [rows])
+ *   residual_out  NULL or [rows][width] in `dtype`: h rounded once; may be `residual` or `x`
+ *             itself where that one's row stride is `width`
+ * Here strides may be any non-negative number and pointers aligned to their type only; rows
+ * that are 16-byte aligned with a width that is a multiple of 8 take the fast path.
+ * Inputs must be finite.  No workspace.
+ */
+int idx_topk_norm_quant(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                        const void *weight, float eps, int32_t rows, int32_t width, int32_t group,
+                        int32_t dtype, uint8_t *codes, float *scales, void *residual_out, void *stream);
+
+/*
+ * Append tokens to the caches: for every token t with slots[t] in [0, num_slots)
+ *   latent_cache[slots[t],:] = latents[t,:]
+ *   k_scale[slots[t]] = max|index_keys[t,:]| / 448 (1 for an all-zero key),
+ *   k_cache[slots[t],:] = nearest e4m3fn of index_keys[t,:] / k_scale[slots[t]]
+ * Tokens with other slots (-1: padding) are not stored.  The slots of one call must be distinct
+ * (two tokens of one slot leave a mixture there).
+ *   latents     [T][576] stride latent_token, latent_cache [num_slots][576]; both NULL: not stored
+ *   index_keys  [T][128] stride key_token, k_cache [num_slots][128] uint8, k_scale [num_slots];
+ *               all NULL: not stored
+ */
+int idx_topk_cache_append(const void *latents, int64_t latent_token, const void *index_keys,
+                          int64_t key_token, const int32_t *slots, int32_t T, int32_t dtype,
+                          void *latent_cache, uint8_t *k_cache, float *k_scale, int64_t num_slots,
+                          void *stream);
+
 /* Copy the counters of the last call that used `workspace` into *out.
  * Synchronises `stream`.  For tests and diagnosis, not for hot loops. */
 int idx_topk_read_stats(const void *workspace, idx_topk_stats *out, void *stream);

@@ -396,6 +396,246 @@ def decode_paged(q8, q_scale, k_cache, k_scale, w, page_table, seq_lens, K: int,
     return out
 
 
+# ------------------------------------------------------- operators around the indexer
+
+LATENT, ROPE, NOPE, VALUE = 512, 64, 128, 128
+LATENT_ROW = LATENT + ROPE
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+_i64, _f32 = ctypes.c_int64, ctypes.c_float
+_lib.idx_topk_latent_selected_workspace.restype = _sz
+_lib.idx_topk_latent_selected_workspace.argtypes = [_i32, _i32, _i32]
+_lib.idx_topk_latent_selected.restype = ctypes.c_int
+_lib.idx_topk_latent_selected.argtypes = [_vp, _i64, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _f32, _i32, _vp, _vp, _vp,
+                                          _sz, _vp]
+_lib.idx_topk_latent_paged_workspace.restype = _sz
+_lib.idx_topk_latent_paged_workspace.argtypes = [_i32, _i32, _i32, _i32]
+_lib.idx_topk_latent_paged.restype = ctypes.c_int
+_lib.idx_topk_latent_paged.argtypes = [_vp, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _f32, _i32,
+                                       _vp, _vp, _vp, _sz, _vp]
+_lib.idx_topk_latent_expanded_workspace.restype = _sz
+_lib.idx_topk_latent_expanded_workspace.argtypes = [_i32, _i32, _i32, _i32, _i32]
+_lib.idx_topk_latent_expanded.restype = ctypes.c_int
+_lib.idx_topk_latent_expanded.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32,
+                                          _i32, _i32, _f32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]
+_lib.idx_topk_norm_quant.restype = ctypes.c_int
+_lib.idx_topk_norm_quant.argtypes = [_vp, _i64, _vp, _i64, _vp, _f32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp]
+_lib.idx_topk_cache_append.restype = ctypes.c_int
+_lib.idx_topk_cache_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i64, _vp]
+
+
+def latent_selected_workspace_bytes(T: int, H: int, K: int) -> int:
+    return int(_lib.idx_topk_latent_selected_workspace(T, H, K))
+
+
+def latent_paged_workspace_bytes(B: int, S: int, H: int, max_pages: int) -> int:
+    return int(_lib.idx_topk_latent_paged_workspace(B, S, H, max_pages))
+
+
+def latent_expanded_workspace_bytes(Tq: int, B: int, max_q: int, max_k: int, H: int) -> int:
+    return int(_lib.idx_topk_latent_expanded_workspace(Tq, B, max_q, max_k, H))
+
+
+def _dtype16(t: torch.Tensor) -> int:
+    if t.dtype not in _DTYPES:
+        raise ValueError("expected bfloat16 or float16, got %s" % t.dtype)
+    return _DTYPES[t.dtype]
+
+
+def _rows16(t: torch.Tensor, dtype, *shape):
+    """Pointer of a strided 16-bit input whose last dimension is contiguous;
+    `shape` gives its trailing sizes (None: any)."""
+    if not t.is_cuda:
+        raise ValueError("expected a device tensor")
+    if t.dtype != dtype:
+        raise ValueError("expected dtype %s, got %s" % (dtype, t.dtype))
+    if t.dim() != len(shape) or any(n is not None and t.shape[i] != n for i, n in enumerate(shape)):
+        raise ValueError("expected shape %s, got %s" % (list(shape), list(t.shape)))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("expected unit stride along the last dimension")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _stride(t: torch.Tensor, dim: int) -> int:
+    """Stride in numbers; a dimension of one has none that matters."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, device):
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("expected an output of shape %s, got %s" % (list(shape), list(t.shape)))
+    _ptr(t, dtype)
+    return t
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("expected all tensors on %s, got one on %s" % (dev, t.device))
+
+
+def _cache_rows(cache: torch.Tensor, width: int, dtype):
+    if cache.shape[-1] != width:
+        raise ValueError("expected a cache of rows of %d, got shape %s" % (width, list(cache.shape)))
+    return _ptr(cache, dtype), cache.numel() // width
+
+
+def latent_selected(q, cache, slots, scale: float, out=None, lse=None, workspace=None, stream=None):
+    """Latent attention over listed slots; see idx_topk_latent_selected in
+    include/idx_topk.h.
+
+    q [T,H,576] bf16 or f16 (strided), cache [...,576] contiguous, slots [T,K]
+    int32 (the output of prefill or decode_paged: -1 entries are skipped).
+    Returns (out [T,H,512], lse [T,H] f32).
+    """
+    dt = _dtype16(q)
+    q_ptr = _rows16(q, q.dtype, None, None, LATENT_ROW)
+    T, H = int(q.shape[0]), int(q.shape[1])
+    if slots.dim() != 2 or slots.shape[0] != T:
+        raise ValueError("expected slots of shape [%d, K], got %s" % (T, list(slots.shape)))
+    K = int(slots.shape[1])
+    dev = q.device
+    cache_ptr, num_slots = _cache_rows(cache, LATENT_ROW, q.dtype)
+    out = _out(out, (T, H, LATENT), q.dtype, dev)
+    lse = _out(lse, (T, H), torch.float32, dev)
+    _same_device(dev, cache, slots, out, lse, workspace)
+    if workspace is None:
+        workspace = alloc_workspace(latent_selected_workspace_bytes(T, H, K), dev)
+    _check(_lib.idx_topk_latent_selected(q_ptr, _stride(q, 0), _stride(q, 1), cache_ptr, num_slots, _ptr(slots, torch.int32),
+                                         K, T, H, float(scale), dt, _ptr(out), _ptr(lse), _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out, lse
+
+
+def latent_paged(q, cache, page_table, seq_lens, scale: float, out=None, lse=None, workspace=None, stream=None):
+    """Latent attention over whole paged sequences; see idx_topk_latent_paged.
+
+    q [B,S,H,576] (strided; S tokens at the end of each sequence), cache
+    [P,64,576], page_table [B,max_pages] int32, seq_lens [B] int32 (device).
+    Returns (out [B,S,H,512], lse [B,S,H] f32).
+    """
+    dt = _dtype16(q)
+    q_ptr = _rows16(q, q.dtype, None, None, None, LATENT_ROW)
+    B, S, H = (int(n) for n in q.shape[:3])
+    if cache.dim() != 3 or cache.shape[1] != PAGE:
+        raise ValueError("expected a cache of shape [pages, 64, 576], got %s" % list(cache.shape))
+    if page_table.dim() != 2 or page_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("expected page_table [%d, max_pages] and seq_lens [%d]" % (B, B))
+    dev = q.device
+    cache_ptr, num_slots = _cache_rows(cache, LATENT_ROW, q.dtype)
+    max_pages = int(page_table.shape[1])
+    out = _out(out, (B, S, H, LATENT), q.dtype, dev)
+    lse = _out(lse, (B, S, H), torch.float32, dev)
+    _same_device(dev, cache, page_table, seq_lens, out, lse, workspace)
+    if workspace is None:
+        workspace = alloc_workspace(latent_paged_workspace_bytes(B, S, H, max_pages), dev)
+    _check(_lib.idx_topk_latent_paged(q_ptr, _stride(q, 0), _stride(q, 1), _stride(q, 2), cache_ptr, num_slots // PAGE,
+                                      _ptr(page_table, torch.int32), max_pages, _ptr(seq_lens, torch.int32), B, S, H,
+                                      float(scale), dt, _ptr(out), _ptr(lse), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out, lse
+
+
+def latent_expanded(q, kv, k_rope, cu_q, cu_k, max_q: int, max_k: int, scale: float, causal: bool = True, out=None,
+                    lse=None, workspace=None, stream=None):
+    """Causal attention over packed prompts with expanded keys and values; see
+    idx_topk_latent_expanded.
+
+    q [Tq,H,192], kv [Tk,H,256] (128 key numbers, then 128 value numbers),
+    k_rope [Tk,64], all strided; cu_q, cu_k [B+1] int32 (device) running token
+    counts, max_q and max_k the longest prompt's query tokens and keys.
+    Returns (out [Tq,H,128], lse [Tq,H] f32).
+    """
+    dt = _dtype16(q)
+    Tq, H, Tk = int(q.shape[0]), int(q.shape[1]), int(kv.shape[0])
+    q_ptr = _rows16(q, q.dtype, None, None, NOPE + ROPE)
+    kv_ptr = _rows16(kv, q.dtype, None, H, NOPE + VALUE)
+    rope_ptr = _rows16(k_rope, q.dtype, Tk, ROPE)
+    if cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.shape[0] < 1:
+        raise ValueError("expected cu_q and cu_k of shape [B+1]")
+    B = int(cu_q.shape[0]) - 1
+    dev = q.device
+    out = _out(out, (Tq, H, VALUE), q.dtype, dev)
+    lse = _out(lse, (Tq, H), torch.float32, dev)
+    _same_device(dev, kv, k_rope, cu_q, cu_k, out, lse, workspace)
+    if workspace is None:
+        workspace = alloc_workspace(latent_expanded_workspace_bytes(Tq, B, max_q, max_k, H), dev)
+    _check(_lib.idx_topk_latent_expanded(q_ptr, _stride(q, 0), _stride(q, 1), kv_ptr, _stride(kv, 0), _stride(kv, 1), rope_ptr,
+                                         _stride(k_rope, 0), _ptr(cu_q, torch.int32), _ptr(cu_k, torch.int32), B, Tq, Tk,
+                                         int(max_q), int(max_k), H, float(scale), 1 if causal else 0, dt, _ptr(out),
+                                         _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                         _stream(stream)))
+    return out, lse
+
+
+def norm_quant(x, weight, eps: float, residual=None, group: int = 0, codes=None, scales=None, residual_out=None,
+               stream=None):
+    """Root-mean-square norm of x + residual to e4m3 codes and scales; see
+    idx_topk_norm_quant.
+
+    x, residual [R,W] bf16 or f16 (strided rows) and weight [W] or None; group 0 (one
+    scale a row) or 128.  Returns (codes [R,W] float8_e4m3fn, scales [R,W/group]
+    f32, x + residual or None): the last one is residual_out, or with a
+    residual and no residual_out a new tensor.
+    """
+    dt = _dtype16(x)
+    x_ptr = _rows16(x, x.dtype, None, None)
+    R, W = int(x.shape[0]), int(x.shape[1])
+    dev = x.device
+    res_ptr = None if residual is None else _rows16(residual, x.dtype, R, W)
+    if weight is not None and tuple(weight.shape) != (W,):
+        raise ValueError("expected a weight of shape [%d], got %s" % (W, list(weight.shape)))
+    groups = W // group if group > 0 else 1
+    codes = _out(codes, (R, W), torch.float8_e4m3fn, dev)
+    scales = _out(scales, (R, groups), torch.float32, dev)
+    if residual is not None or residual_out is not None:
+        residual_out = _out(residual_out, (R, W), x.dtype, dev)
+    _same_device(dev, residual, weight, codes, scales, residual_out)
+    _check(_lib.idx_topk_norm_quant(x_ptr, _stride(x, 0), res_ptr, 0 if residual is None else _stride(residual, 0),
+                                    _ptr(weight, x.dtype), float(eps), R, W, int(group), dt, _ptr(codes), _ptr(scales),
+                                    _ptr(residual_out), _stream(stream)))
+    return codes, scales, residual_out
+
+
+def cache_append(latents, index_keys, slots, latent_cache, k_cache, k_scale, stream=None):
+    """Store new tokens in the caches; see idx_topk_cache_append.
+
+    latents [T,576] and index_keys [T,128] bf16 or f16 (strided rows), slots [T]
+    int32 (-1: not stored), latent_cache [...,576], k_cache [...,128] uint8 or
+    float8_e4m3fn, k_scale [...] f32.  latents with latent_cache, or index_keys
+    with k_cache and k_scale, may be None together.
+    """
+    one = latents if latents is not None else index_keys
+    if one is None:
+        raise ValueError("expected latents, index_keys or both")
+    dt, dev, T = _dtype16(one), one.device, int(one.shape[0])
+    if (latents is None) != (latent_cache is None) or len({index_keys is None, k_cache is None, k_scale is None}) != 1:
+        raise ValueError("latents come with latent_cache, index_keys with k_cache and k_scale")
+    if tuple(slots.shape) != (T,):
+        raise ValueError("expected slots of shape [%d], got %s" % (T, list(slots.shape)))
+    lat_ptr = key_ptr = cache_ptr = kc_ptr = ks_ptr = None
+    num = []
+    if latents is not None:
+        lat_ptr = _rows16(latents, one.dtype, T, LATENT_ROW)
+        cache_ptr, n = _cache_rows(latent_cache, LATENT_ROW, one.dtype)
+        num.append(n)
+    if index_keys is not None:
+        key_ptr = _rows16(index_keys, one.dtype, T, DIM)
+        kc = k_cache.view(torch.uint8) if k_cache.dtype == torch.float8_e4m3fn else k_cache
+        kc_ptr, n = _cache_rows(kc, DIM, torch.uint8)
+        ks_ptr = _ptr(k_scale, torch.float32)
+        num += [n, k_scale.numel()]
+    if len(set(num)) != 1:
+        raise ValueError("the caches hold different numbers of slots: %s" % num)
+    _same_device(dev, latents, index_keys, slots, latent_cache, k_cache, k_scale)
+    _check(_lib.idx_topk_cache_append(lat_ptr, 0 if latents is None else _stride(latents, 0), key_ptr,
+                                      0 if index_keys is None else _stride(index_keys, 0), _ptr(slots, torch.int32), T, dt,
+                                      cache_ptr, kc_ptr, ks_ptr, num[0], _stream(stream)))
+
+
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 

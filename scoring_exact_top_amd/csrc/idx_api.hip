@@ -4,6 +4,8 @@
 
 #include "idx_internal.hpp"
 #include "idx_decode.hpp"
+#include "idx_latent.hpp"
+#include "idx_norm.hpp"
 #include "idx_rows.hpp"
 #include "idx_scan.hpp"
 
@@ -239,6 +241,61 @@ extern "C" int idx_topk_decode_paged_noalloc(const uint8_t* q, const float* q_sc
                                              void* stream) {
   return decode_paged_noalloc(q, q_scale, k_cache, k_scale, w, page_table, seq_lens, B, max_pages, page_size,
                               num_pages, K, out_idx, static_cast<hipStream_t>(stream));
+}
+
+extern "C" size_t idx_topk_latent_selected_workspace(int32_t T, int32_t H, int32_t K) {
+  return latent_selected_workspace_bytes(T, H, K);
+}
+
+extern "C" int idx_topk_latent_selected(const void* q, int64_t q_token, int64_t q_head, const void* cache,
+                                        int64_t num_slots, const int32_t* slots, int32_t K, int32_t T, int32_t H,
+                                        float scale, int32_t dtype, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  return latent_selected(q, q_token, q_head, cache, num_slots, slots, K, T, H, scale, dtype, out, lse, workspace,
+                         workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+extern "C" size_t idx_topk_latent_paged_workspace(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
+  return latent_paged_workspace_bytes(B, S, H, max_pages);
+}
+
+extern "C" int idx_topk_latent_paged(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, const void* cache,
+                                     int32_t num_pages, const int32_t* page_table, int32_t max_pages,
+                                     const int32_t* seq_lens, int32_t B, int32_t S, int32_t H, float scale,
+                                     int32_t dtype, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  return latent_paged(q, q_seq, q_token, q_head, cache, num_pages, page_table, max_pages, seq_lens, B, S, H, scale,
+                      dtype, out, lse, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+extern "C" size_t idx_topk_latent_expanded_workspace(int32_t Tq, int32_t B, int32_t max_q, int32_t max_k, int32_t H) {
+  return latent_expanded_workspace_bytes(Tq, B, max_q, max_k, H);
+}
+
+extern "C" int idx_topk_latent_expanded(const void* q, int64_t q_token, int64_t q_head, const void* kv,
+                                        int64_t kv_token, int64_t kv_head, const void* k_rope, int64_t rope_token,
+                                        const int32_t* cu_q, const int32_t* cu_k, int32_t B, int32_t Tq, int32_t Tk,
+                                        int32_t max_q, int32_t max_k, int32_t H, float scale, int32_t causal,
+                                        int32_t dtype, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  return latent_expanded(q, q_token, q_head, kv, kv_token, kv_head, k_rope, rope_token, cu_q, cu_k, B, Tq, Tk, max_q,
+                         max_k, H, scale, causal, dtype, out, lse, workspace, workspace_bytes,
+                         static_cast<hipStream_t>(stream));
+}
+
+extern "C" int idx_topk_norm_quant(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                   const void* weight, float eps, int32_t rows, int32_t width, int32_t group,
+                                   int32_t dtype, uint8_t* codes, float* scales, void* residual_out, void* stream) {
+  return norm_quant(x, x_stride, residual, residual_stride, weight, eps, rows, width, group, dtype, codes, scales,
+                    residual_out, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int idx_topk_cache_append(const void* latents, int64_t latent_token, const void* index_keys,
+                                     int64_t key_token, const int32_t* slots, int32_t T, int32_t dtype,
+                                     void* latent_cache, uint8_t* k_cache, float* k_scale, int64_t num_slots,
+                                     void* stream) {
+  return cache_append(latents, latent_token, index_keys, key_token, slots, T, dtype, latent_cache, k_cache, k_scale,
+                      num_slots, static_cast<hipStream_t>(stream));
 }
 
 extern "C" int idx_topk_read_stats(const void* workspace, idx_topk_stats* out, void* stream) {

@@ -1,0 +1,167 @@
+// Building blocks of the attention kernels (gfx950).
+//
+// Attention of a row (one query vector) over keys i with logits
+// x_i = scale * q.k_i is o = sum_i exp(x_i) v_i / sum_i exp(x_i), computed in
+// one pass over the keys with a running reference m (any m at which nothing
+// overflows gives the same quotient):
+//
+//   p_i = 2^(x_i log2(e) - m),  l = sum p_i,  o' = sum p_i v_i,
+//   o = o' / l,  log(sum exp) = (m + log2 l) ln 2,
+//
+// and o', l are multiplied by 2^(m_old - m_new) where m moves.
+//
+// A wave owns 32 rows.  Both products are v_mfma_f32_32x32x16 with the keys
+// (or the values' columns) as the 32 rows of A and the 32 attention rows as
+// the columns of B:
+//
+//   logits^T [32 keys x 32 rows] = K [32 x d] . Q^T [d x 32]
+//   o'^T     [32 columns x 32 rows] += V^T [32 x keys] . P^T [keys x 32]
+//
+// In a 32x32 result, lane l = 32h + c holds column c, and its register r holds
+// row (r & 3) + 8 (r >> 2) + 4h.  So every lane holds one attention row's
+// statistics (c), its maximum and sum need one exchange between the two wave
+// halves, and o' is rescaled by a factor that is the lane's own.  The B
+// operand of the second product wants 8 keys of a row in each lane: with key
+// (j & 3) + 8 (j >> 2) + 4h of a 16-key step as the operand's k index 8h + j
+// they are exactly the 8 logits that the lane holds, in order, so P goes from
+// one product to the next without leaving its registers; the A operand then
+// takes the keys in that order too, 4 at a time through the transposing
+// ds_read_b64_tr_b16 (a 16-lane group reads 4 keys x 16 columns row by row
+// and each lane receives one column's 4 keys).
+//
+// P is rounded to the inputs' 16-bit type for the matrix core: its relative
+// rounding error (2^-8 at most for bfloat16, 2^-11 for half) is that of the output's
+// own rounding.  Logits, maxima, sums and o' stay in FP32; l sums the FP32 p.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace idxk {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int w4i __attribute__((ext_vector_type(4)));
+
+// c += A B with c in VGPRs.  The compiler gives the results of all MFMAs of a
+// kernel to one register file; where o' takes the whole accumulator file (256
+// registers: 512 columns of 32 rows), the logits must stay out of it.  The
+// two leading wait states cover a VALU write of an operand; sources that come
+// from loads are waited for by the compiler, and mfma_v_done() ends a chain.
+#define IDX_MFMA_V(NAME, FIRST, NEXT)                                                       \
+  static __device__ __forceinline__ void NAME(v16f& c, v8 a, v8 b, bool first) {            \
+    if (first) asm(FIRST : "=&v"(c) : "v"(a), "v"(b));                                      \
+    else asm(NEXT : "+v"(c) : "v"(a), "v"(b));                                              \
+  }
+
+// A 16-pass MFMA's result may be read by VALU instructions 18 wait states later.
+__device__ __forceinline__ void mfma_v_done(v16f& c) { asm volatile("s_nop 15\n\ts_nop 7" : "+v"(c)); }
+
+struct TBf16 {
+  typedef __bf16 elem;
+  typedef __bf16 v8 __attribute__((ext_vector_type(8)));
+  typedef __bf16 v4 __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  IDX_MFMA_V(mfma_v, "s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0",
+             "s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0")
+};
+
+struct TF16 {
+  typedef _Float16 elem;
+  typedef _Float16 v8 __attribute__((ext_vector_type(8)));
+  typedef _Float16 v4 __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  IDX_MFMA_V(mfma_v, "s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, 0",
+             "s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0")
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// o' and l are rescaled only where a row's maximum passes its reference by
+// this many octaves: p stays below 2^8, far from any type's limit, and
+// rescaling o' (all its registers) becomes rare.  The quotient is the same.
+constexpr float kRescaleOctaves = 8.f;
+
+template <class V>
+__device__ __forceinline__ V lds_read(const char* p) {
+  return *reinterpret_cast<const V*>(p);
+}
+
+// 4 keys (rows of LDS) of one value column: see above.
+template <class T>
+__device__ __forceinline__ typename T::v4 lds_read_tr(const char* p) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  const v4s r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (__attribute__((address_space(3))) v4s*)(__attribute__((address_space(3))) char*)p);
+  typename T::v4 o;
+  __builtin_memcpy(&o, &r, sizeof o);
+  return o;
+}
+
+template <class T>
+__device__ __forceinline__ typename T::v8 cat(typename T::v4 a, typename T::v4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The value of the other half of the wave (lane l ^ 32).
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+
+// Key of a 32-key tile whose logit is in register r of wave half h.
+__device__ __forceinline__ constexpr int key_of(int r, int h) { return (r & 3) + 8 * (r >> 2) + 4 * h; }
+
+// A row's statistics: m in octaves (-inf before the first live key), l.
+struct RowStat {
+  float m, l;
+};
+
+// The largest logit of each row in a tile (FP32, unscaled; -inf where masked)
+// in octaves, c = scale * log2(e) > 0.  All 64 lanes take part.
+__device__ __forceinline__ float tile_max(const v16f& x, float c) {
+  float mx = x[0];
+#pragma unroll
+  for (int r = 1; r < 16; ++r) mx = fmaxf(mx, x[r]);
+  return fmaxf(mx, other_half(mx)) * c;
+}
+
+// Whether some row of the wave has to move its reference for a tile of
+// maximum mx (the first live keys move it from -inf).
+__device__ __forceinline__ bool must_move(const RowStat& st, float mx) { return __any(mx > st.m + kRescaleOctaves); }
+
+// Moves the references to cover mx; returns the factor of o'.
+__device__ __forceinline__ float move_reference(RowStat& st, float mx) {
+  const float m = fmaxf(st.m, mx);
+  const float alpha = st.m == m ? 1.f : __builtin_amdgcn_exp2f(st.m - m);  // 0 where m was -inf
+  st.m = m;
+  st.l *= alpha;
+  return alpha;
+}
+
+// A tile's logits to p, in place.
+__device__ __forceinline__ void softmax_tile(v16f& x, RowStat& st, float c) {
+  const float m = st.m == -INFINITY ? 0.f : st.m;  // a row without a live key yet: p = 0
+  float l = 0.f;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -m));
+    l += x[r];
+  }
+  st.l += l;  // this half's keys; the halves are added at the end
+}
+
+// p of the 16-key step s (0 or 1) of a tile as the second product's B operand.
+template <class T>
+__device__ __forceinline__ typename T::v8 p_operand(const v16f& p, int s) {
+  typename T::v8 o;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = (typename T::elem)p[8 * s + j];
+  return o;
+}
+
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+}
+
+}  // namespace idxk
