@@ -142,13 +142,13 @@ __device__ __forceinline__ float move_reference(RowStat& st, float mx) {
 // A tile's logits to p, in place.
 __device__ __forceinline__ void softmax_tile(v16f& x, RowStat& st, float c) {
   const float m = st.m == -INFINITY ? 0.f : st.m;  // a row without a live key yet: p = 0
-  float l = 0.f;
+  float l[4] = {};
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
     x[r] = __builtin_amdgcn_exp2f(fmaf(x[r], c, -m));
-    l += x[r];
+    l[r & 3] += x[r];
   }
-  st.l += l;  // this half's keys; the halves are added at the end
+  st.l += (l[0] + l[1]) + (l[2] + l[3]);  // this half's keys; the halves are added at the end
 }
 
 // p of the 16-key step s (0 or 1) of a tile as the second product's B operand.

@@ -8,7 +8,11 @@
 // heads 121 operations a byte.
 //
 // A workgroup takes one token (or sequence) and up to 128 rows (heads, or steps x heads), 32 a
-// wave; all its waves share each 32-key tile in LDS (idx_attn.hpp has the arithmetic).
+// wave; its waves share each 32-key tile in LDS (idx_attn.hpp has the arithmetic), read from
+// memory straight into LDS while earlier tiles are worked on.  With 64 rows or fewer the waves
+// form two key groups that take every other tile and are joined at the end.  Where tokens or
+// sequences alone leave compute units idle, the keys are split over workgroups, whose partial
+// results a second kernel joins.
 #include "idx_attn.hpp"
 #include "idx_latent.hpp"
 
@@ -20,20 +24,27 @@ constexpr int kLatSteps = kLatent / 16;   // ... of which in the latent part
 constexpr int kCols = kLatent / 32;       // 32-column blocks of the values
 constexpr int kRopeOff = kTileKeys * kLatent * 2;             // rotary part of a tile, behind the latent parts
 constexpr int kTileBytes = kTileKeys * kLatRow * 2;
+constexpr int kBuffers = 4;               // tiles in LDS: 144 of the 160 KiB
 constexpr int kMaxList = IDX_TOPK_KMAX;
+constexpr int kPlanBatch = 1024;          // larger batches take one workgroup a sequence
+constexpr int kUnits = 256;               // compute units: one workgroup each
 
 struct LatArgs {
   const char* q;
   int64_t q_seq, q_token, q_head;  // in numbers
   const char* cache;
   int64_t num_slots;
-  const int32_t* list;             // slots [T][K], or page ids [B][K]
+  const int32_t* list;             // slots [B][K], or page ids [B][K]
   const int32_t* lens;             // paged: [B]
   int32_t K, B, S, H;
   int32_t row_blocks;
+  int32_t parts;                   // listed: workgroups a token's list is split over; paged: workgroups in all
   float c;                         // scale * log2(e)
   char* out;
   float* lse;
+  float* part_o;                   // [part * row_blocks + block][32 HG][512]
+  float2* part_ml;                 // [part * row_blocks + block][32 HG]
+  int2* plan;                      // paged: [B] first part and number of parts
 };
 
 // A row of zeros for keys that a tile does not have: they are masked, and
@@ -47,33 +58,204 @@ __device__ const uint4 kZeroRow[kLatRow * 2 / 16] = {};
 __device__ __forceinline__ int lat_swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 __device__ __forceinline__ int rope_swz(int r) { return (r >> 1) & 7; }
 
-// 16 bytes a lane from memory to 1 KiB of LDS (lane order), without registers.
-__device__ __forceinline__ void dma16(const char* src, char* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+// Workgroup `wg` of a paged call: its sequence, which of the sequence's parts
+// it takes and how many there are.  A sequence gets parts in proportion to its
+// pages, at least one and none under kMinPages; every workgroup (its first
+// wave) works the plan out from the lengths.
+struct Part {
+  int b, part, parts, first;
+};
+constexpr int kMinPages = 2;
+
+__device__ __forceinline__ int wave_incl_scan(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  return x;
 }
 
-template <class T, int HG, bool PAGED>
-__global__ __launch_bounds__(64 * HG) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_latent(LatArgs A) {
-  __shared__ __attribute__((aligned(1024))) char s_tile[kTileBytes];
-  __shared__ int32_t s_list[PAGED ? 1 : kMaxList];
-  const int tid = threadIdx.x, lane = tid & 63, hg = __builtin_amdgcn_readfirstlane(tid >> 6);
+__device__ __forceinline__ int seq_len(const LatArgs& A, int b) {
+  const int n = A.lens[b];
+  return n < 0 || (int64_t)n > (int64_t)A.K * IDX_TOPK_PAGE ? 0 : n;
+}
+
+__device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
+  if (A.parts == A.B) return Part{wg, 0, 1, wg};
+  int64_t total = 0;
+  for (int b0 = 0; b0 < A.B; b0 += 64) {
+    const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    total += __shfl(wave_incl_scan(n, lane), 63, 64);
+  }
+  // sum of max(1, ceil(n / unit)) <= total / unit + B <= parts
+  int unit = (int)((total + (A.parts - A.B) - 1) / (A.parts - A.B));
+  unit = unit < kMinPages ? kMinPages : unit;
+  int base = 0;
+  for (int b0 = 0; b0 < A.B; b0 += 64) {
+    const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    const int parts = b0 + lane < A.B ? max(1, (n + unit - 1) / unit) : 0;
+    const int end = base + wave_incl_scan(parts, lane);
+    const uint64_t mine = __ballot(wg >= end - parts && wg < end);
+    if (mine) {
+      const int at = __ffsll((unsigned long long)mine) - 1;
+      const int n_at = __shfl(parts, at, 64), first = __shfl(end, at, 64) - n_at;
+      return Part{b0 + at, wg - first, n_at, first};
+    }
+    base = __shfl(end, 63, 64);
+  }
+  return Part{-1, 0, 0, 0};  // a spare workgroup
+}
+
+// 64 lanes x 16 bytes from src + off (a lane's) to 1 KiB of LDS in lane order,
+// without registers.  The compiler does not see the write: the tile waits
+// below order it.
+__device__ __forceinline__ void dma_row(const char* src, int off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(src));
+}
+__device__ __forceinline__ void dma_lanes(const char* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src));
+}
+// All but the last N of this wave's loads to LDS are done.
+template <int N>
+__device__ __forceinline__ void dma_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Every wave is here, and has its LDS reads back.
+__device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// HG row groups of 32 (one wave each) x KG key groups: wave (kg, hg) walks
+// the tiles kg, kg + KG, ... of the workgroup's range for its 32 rows.
+template <class T, int HG, int KG, bool PAGED>
+__global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_latent(LatArgs A) {
+  constexpr int kRing = kBuffers / KG;           // tiles of a key group in LDS
+  constexpr int kRows = kTileKeys / HG;          // rows of a tile that one wave loads
+  constexpr int kLoads = kRows + 4 / HG;         // its loads to LDS a tile
+  __shared__ __attribute__((aligned(1024))) char s_tile[kBuffers * kTileBytes];
+  __shared__ int32_t s_list[PAGED ? 4 : kMaxList + kTileKeys];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int hg = wave % HG, kg = wave / HG;
   const int h = lane >> 5, col = lane & 31;
-  const int b = blockIdx.x / A.row_blocks, rb = blockIdx.x % A.row_blocks;
+  // workgroups of one chiplet (every eighth) take neighbouring work
+  const int total = gridDim.x, per = total >> 3, extra = total & 7, x8 = blockIdx.x & 7, i8 = blockIdx.x >> 3;
+  const int work = x8 * per + min(x8, extra) + i8;
+  const int wg = work / A.row_blocks, rb = work % A.row_blocks;
+
+  Part part;
+  int len, tile0, tile1;  // keys of the sequence or list, this workgroup's tiles
+  if (PAGED) {
+    if (wave == 0) {
+      part = plan_part(A, wg, lane);
+      if (lane == 0) {
+        s_list[0] = part.b; s_list[1] = part.part; s_list[2] = part.parts; s_list[3] = part.first;
+        if (rb == 0 && part.b >= 0 && part.part == 0) A.plan[part.b] = make_int2(part.first, part.parts);
+      }
+    }
+    __syncthreads();
+    part.b = __builtin_amdgcn_readfirstlane(s_list[0]);
+    part.part = __builtin_amdgcn_readfirstlane(s_list[1]);
+    part.parts = __builtin_amdgcn_readfirstlane(s_list[2]);
+    if (part.b < 0) return;
+    len = __builtin_amdgcn_readfirstlane(seq_len(A, part.b));
+    const int pages = (len + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE;
+    tile0 = 2 * (int)((int64_t)pages * part.part / part.parts);
+    tile1 = min(2 * (int)((int64_t)pages * (part.part + 1) / part.parts), (len + kTileKeys - 1) / kTileKeys);
+  } else {
+    part.b = wg / A.parts; part.part = wg % A.parts; part.parts = A.parts;
+    len = A.K;
+    const int tiles = (len + kTileKeys - 1) / kTileKeys;
+    tile0 = tiles * part.part / A.parts;
+    tile1 = tiles * (part.part + 1) / A.parts;
+    // this range's slots, -1 for what is not to be read
+    for (int i = tid; i < (tile1 - tile0) * kTileKeys + kTileKeys; i += 64 * HG * KG) {
+      const int at = tile0 * kTileKeys + i;
+      const int s = at < min(len, tile1 * kTileKeys) ? A.list[(int64_t)part.b * A.K + at] : -1;
+      s_list[i] = s >= 0 && s < A.num_slots ? s : -1;
+    }
+  }
+  const int b = part.b;
   const int row = (rb * HG + hg) * 32 + col;
   const bool have = row < A.S * A.H;
   const int step = have ? row / A.H : 0, head = have ? row % A.H : 0;
+  int limit = PAGED ? len - A.S + 1 + step : len;  // this lane's row sees keys below
+  const int limit_min = PAGED ? len - A.S + 1 : len;     // every row does
 
-  int len = A.K, limit;  // keys of the walk; this lane's row sees keys below `limit`
-  if (PAGED) {
-    len = A.lens[b];
-    if (len < 0 || (int64_t)len > (int64_t)A.K * IDX_TOPK_PAGE) len = 0;
-    limit = len - A.S + 1 + step;
-  } else {
-    limit = len;
-    for (int i = tid; i < len; i += 64 * HG) s_list[i] = A.list[(int64_t)b * A.K + i];
-  }
+  if (!PAGED) __syncthreads();
 
+  v16f o[kCols];
+#pragma unroll
+  for (int d = 0; d < kCols; ++d) o[d] = v16f{};
+  RowStat st{-INFINITY, 0.f};
+  // this lane's LDS byte offsets in a tile: its key's row (first product; step
+  // s at chunk 2s + h), and its two rows of the transposing reads (second)
+  const int tr = 4 * h + ((lane & 15) >> 2), tc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+  int kaddr = col * (kLatent * 2) + ((h ^ lat_swz(col)) << 4), raddr = kRopeOff + col * (kRope * 2) + ((h ^ rope_swz(col)) << 4);
+  int vaddr0 = tr * (kLatent * 2) + ((tc ^ lat_swz(tr)) << 4) + (lane & 1) * 8;
+  int vaddr1 = (tr + 8) * (kLatent * 2) + ((tc ^ lat_swz(tr + 8)) << 4) + (lane & 1) * 8;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)s_tile;
+
+  int lane_r = lane;
+  const int mine = tile0 + kg;                                // this key group's first tile
+  const int steps = tile1 > tile0 ? (tile1 - tile0 + KG - 1) / KG : 0;  // the same for all key groups: barriers
+
+  // Slot of key `col` of step i's tile (-1: none).
+  const auto slot_of = [&](int i) -> int { return s_list[(i * KG + kg) * kTileKeys + (lane_r & 31)]; };
+  // Physical page of step i's tile, -1: none (a tile lies in one page).
+  const auto page_of = [&](int i) -> int {
+    const int key = (mine + i * KG) * kTileKeys;
+    if (key >= len) return -1;
+    // a scalar load: vector loads would queue behind the tile loads
+    const int pg = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)A.list)[(int64_t)b * A.K + key / IDX_TOPK_PAGE];
+    return pg >= 0 && (int64_t)pg * IDX_TOPK_PAGE < A.num_slots ? pg : -1;
+  };
+  // Starts this wave's share of step i's tile.
+  const auto load = [&](int i) {
+    const uint32_t dst = lds0 + (kg * kRing + i % kRing) * kTileBytes;
+    const char* const zero = reinterpret_cast<const char*>(kZeroRow);
+    const int key0 = (mine + i * KG) * kTileKeys;
+    int slots = 0, live = 0;
+    const char* page = zero;
+    int l16 = lane_r;  // 16 lane, made here as the offsets of the products below
+    asm volatile("" : "+v"(l16));
+    l16 = (l16 ^ (HG == 1 ? 0 : lat_swz(hg * kRows))) << 4;
+    if (PAGED) {
+      const int pg = __builtin_amdgcn_readfirstlane(page_of(i));
+      live = pg < 0 ? 0 : min(kTileKeys, len - key0);
+      if (pg >= 0) page = A.cache + ((int64_t)pg * IDX_TOPK_PAGE + key0 % IDX_TOPK_PAGE) * (kLatRow * 2);
+    } else {
+      slots = slot_of(i);
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int r = hg * kRows + j;
+      const char* src;
+      if (PAGED) {
+        src = r < live ? page + r * (kLatRow * 2) : zero;
+      } else {
+        const int s = __builtin_amdgcn_readlane(slots, r);
+        const int64_t at = (int64_t)s * (kLatRow * 2);
+        src = A.cache + (s >= 0 ? at : zero - A.cache);
+      }
+      dma_row(src, l16 ^ (lat_swz(j) << 4), dst + r * (kLatent * 2));
+    }
+#pragma unroll
+    for (int j = 0; j < 4 / HG; ++j) {
+      const int l = l16 >> 4 ^ (HG == 1 ? 0 : lat_swz(hg * kRows));
+      const int r = 8 * (hg * (4 / HG) + j) + (l >> 3);
+      const char* src;
+      if (PAGED) {
+        src = r < live ? page + r * (kLatRow * 2) : zero;
+      } else {
+        const int s = s_list[(i * KG + kg) * kTileKeys + r];
+        src = s >= 0 ? A.cache + (int64_t)s * (kLatRow * 2) : zero;
+      }
+      dma_lanes(src + kLatent * 2 + (((l & 7) ^ rope_swz(r)) << 4), dst + kRopeOff + (hg * (4 / HG) + j) * 1024);
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < kRing; ++i)
+    if (i < steps) load(i);
   typename T::v8 q[kSteps];
   {
     const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + step * A.q_token +
@@ -84,85 +266,68 @@ __global__ __launch_bounds__(64 * HG) __attribute__((amdgpu_waves_per_eu(1, 1)))
       else q[s] = typename T::v8{};
     }
   }
-  v16f o[kCols];
-#pragma unroll
-  for (int d = 0; d < kCols; ++d) o[d] = v16f{};
-  RowStat st{-INFINITY, 0.f};
-  // this lane's LDS byte offsets: its key's row (first product; step s at
-  // chunk 2s + h), and its two rows of the transposing reads (second)
-  const int tr = 4 * h + ((lane & 15) >> 2), tc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-  int kaddr = col * (kLatent * 2) + ((h ^ lat_swz(col)) << 4), raddr = col * (kRope * 2) + ((h ^ rope_swz(col)) << 4);
-  int vaddr0 = tr * (kLatent * 2) + ((tc ^ lat_swz(tr)) << 4) + (lane & 1) * 8;
-  int vaddr1 = (tr + 8) * (kLatent * 2) + ((tc ^ lat_swz(tr + 8)) << 4) + (lane & 1) * 8;
 
-  // Loads the tile at k0 and computes its logits, masked.
-  const auto logits = [&](int k0) {
-    __syncthreads();  // the last tile is read (first: the list is there)
-    // slots of the tile's keys: lane i (and i + 32) key i
-    int64_t slot = -1;
-    if (k0 + col < len) {
-      if (PAGED) {
-        const int key = k0 + col;
-        const int pg = A.list[(int64_t)b * A.K + key / IDX_TOPK_PAGE];
-        slot = pg < 0 ? -1 : (int64_t)pg * IDX_TOPK_PAGE + key % IDX_TOPK_PAGE;
-      } else {
-        slot = s_list[k0 + col];
-      }
-      if (slot >= A.num_slots) slot = -1;
-    }
-    const uint32_t live = (uint32_t)__ballot(slot >= 0);
-    const char* src = slot >= 0 ? A.cache + slot * (kLatRow * 2) : reinterpret_cast<const char*>(kZeroRow);
-    for (int r = hg * (kTileKeys / HG); r < (hg + 1) * (kTileKeys / HG); ++r) {
-      const int64_t p = __shfl((long long)(intptr_t)src, r, 64);
-      dma16(reinterpret_cast<const char*>(p) + ((lane ^ lat_swz(r)) << 4), s_tile + r * (kLatent * 2));
-    }
-    for (int j = hg * (4 / HG); j < (hg + 1) * (4 / HG); ++j) {
-      const int r = 8 * j + (lane >> 3);
-      const int64_t p = __shfl((long long)(intptr_t)src, r, 64);
-      dma16(reinterpret_cast<const char*>(p) + kLatent * 2 + (((lane & 7) ^ rope_swz(r)) << 4), s_tile + kRopeOff + j * 1024);
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-
-    asm volatile("" : "+v"(kaddr), "+v"(raddr), "+v"(vaddr0), "+v"(vaddr1));  // the offsets below are made here, not kept in registers
+  // Waits for step i's tile and computes its logits, masked.
+  const auto logits = [&](int i) {
+    if (i + kRing <= steps) dma_wait<(kRing - 1) * kLoads>();
+    else dma_wait<0>();
+    tile_barrier();
+    const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
+    int ka = kaddr, ra = raddr;
+    asm volatile("" : "+v"(ka), "+v"(ra));  // the offsets below are made here, not kept in registers
     v16f x;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const char* p = s_tile + (kaddr ^ (j << 5));
+      const char* p = tile + (ka ^ (j << 5));
 #pragma unroll
       for (int u = 0; u < kLatSteps / 8; ++u) T::mfma_v(x, lds_read<typename T::v8>(p + 256 * u), q[8 * u + j], j + u == 0);
     }
 #pragma unroll
-    for (int j = 0; j < kRope / 16; ++j)
-      T::mfma_v(x, lds_read<typename T::v8>(s_tile + kRopeOff + (raddr ^ (j << 5))), q[kLatSteps + j], false);
+    for (int j = 0; j < kRope / 16; ++j) T::mfma_v(x, lds_read<typename T::v8>(tile + (ra ^ (j << 5))), q[kLatSteps + j], false);
     mfma_v_done(x);
-    if (live != ~0u || k0 + kTileKeys > limit) {
+    const int key0 = (mine + i * KG) * kTileKeys;
+    uint32_t live;
+    if (PAGED) live = __builtin_amdgcn_readfirstlane(page_of(i)) < 0 ? 0u : ~0u;
+    else live = (uint32_t)__ballot(slot_of(i) >= 0);
+    if (live != ~0u || key0 + kTileKeys > limit_min) {
+      int h4 = lane_r >> 5 << 2;
+      asm volatile("" : "+v"(h4));
+      const uint32_t live_h = live >> h4;
+      const int limit_h = limit - key0 - h4;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int k = key_of(r, h);
-        if (!(live >> k & 1) || k0 + k >= limit) x[r] = -INFINITY;
-      }
+      for (int r = 0; r < 16; ++r)
+        if (!(live_h >> key_of(r, 0) & 1) || key_of(r, 0) >= limit_h) x[r] = -INFINITY;
     }
     return x;
   };
 
-  // The inner loop never touches o' but by MFMA: it leaves to the outer one
-  // where a reference moves.
-  int k0 = 0;
-  if (len > 0) {
+  // o' fills the accumulator registers, and q most of the others.  The inner
+  // loop touches o' with MFMAs only and leaves to the outer one where a
+  // reference moves (rare).  Rescaling takes o' through the other registers, q
+  // to memory and back; the touch behind it makes the compiler wait for that
+  // there, not in the inner loop, where its waits would drain the tile loads in
+  // flight at every step.
+  if (steps > 0) {
+    int i = 0;
     v16f x = logits(0);
     float mx = tile_max(x, A.c);
     for (;;) {
       const float alpha = move_reference(st, mx);
 #pragma unroll
       for (int d = 0; d < kCols; ++d) o[d] *= alpha;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) asm volatile("" : "+v"(q[s]));
+      asm volatile("" : "+v"(x), "+v"(kaddr), "+v"(raddr), "+v"(vaddr0), "+v"(vaddr1), "+v"(lane_r), "+v"(limit), "+v"(st.m), "+v"(st.l));
       for (;;) {
         softmax_tile(x, st, A.c);
         const typename T::v8 p0 = p_operand<T>(x, 0), p1 = p_operand<T>(x, 1);
+        const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
+        int va0 = vaddr0, va1 = vaddr1;
+        asm volatile("" : "+v"(va0), "+v"(va1));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const char* pa = s_tile + (vaddr0 ^ (j << 6));
-          const char* pb = s_tile + (vaddr1 ^ (j << 6));
+          const char* pa = tile + (va0 ^ (j << 6));
+          const char* pb = tile + (va1 ^ (j << 6));
 #pragma unroll
           for (int u = 0; u < kCols / 4; ++u) {
             const int d = 4 * u + j;
@@ -171,20 +336,66 @@ __global__ __launch_bounds__(64 * HG) __attribute__((amdgpu_waves_per_eu(1, 1)))
                            p1, o[d]);
           }
         }
-        k0 += kTileKeys;
-        if (k0 >= len) break;
-        x = logits(k0);
+        tile_barrier();  // the tile is read: its buffer takes the next load
+        if (i + kRing < steps) load(i + kRing);
+        ++i;
+        if (i >= steps) break;
+        x = logits(i);
         mx = tile_max(x, A.c);
         if (must_move(st, mx)) break;
       }
-      if (k0 >= len) break;
+      if (i >= steps) break;
     }
   }
+  float l = st.l + other_half(st.l), m = st.m;
 
-  const float l = st.l + other_half(st.l);
+  // key groups are joined through LDS (nothing is in flight there any more):
+  // group 1 hands over m, l and o', 16 bytes a lane at a time
+  if (KG == 2) {
+    char* const buf = s_tile + hg * (kCols * 16 * 256 + 512);
+    if (kg == 1) {
+#pragma unroll
+      for (int d = 0; d < kCols; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float4 v = make_float4(o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]);
+          *reinterpret_cast<float4*>(buf + 512 + ((d * 4 + g) * 64 + lane) * 16) = v;
+        }
+      *reinterpret_cast<float2*>(buf + lane * 8) = make_float2(m, l);
+    }
+    __syncthreads();
+    if (kg == 1) return;
+    const float2 ml = *reinterpret_cast<const float2*>(buf + lane * 8);
+    const float top = fmaxf(m, ml.x);
+    const float f0 = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top), f1 = ml.x == top ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);
+    l = l * f0 + ml.y * f1;
+    m = top;
+#pragma unroll
+    for (int d = 0; d < kCols; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 v = *reinterpret_cast<const float4*>(buf + 512 + ((d * 4 + g) * 64 + lane) * 16);
+        o[d][4 * g] = o[d][4 * g] * f0 + v.x * f1;
+        o[d][4 * g + 1] = o[d][4 * g + 1] * f0 + v.y * f1;
+        o[d][4 * g + 2] = o[d][4 * g + 2] * f0 + v.z * f1;
+        o[d][4 * g + 3] = o[d][4 * g + 3] * f0 + v.w * f1;
+      }
+  }
   if (!have) return;
+  if (part.parts > 1) {
+    const int64_t at = (int64_t)(wg * A.row_blocks + rb) * (32 * HG) + hg * 32 + col;
+    float* po = A.part_o + at * kLatent;
+#pragma unroll
+    for (int d = 0; d < kCols; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4*>(po + 32 * d + 8 * g + 4 * h) =
+            make_float4(o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]);
+    if (h == 0) A.part_ml[at] = make_float2(m, l);
+    return;
+  }
   const int64_t at = ((int64_t)b * A.S + step) * A.H + head;
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   typename T::elem* out = reinterpret_cast<typename T::elem*>(A.out) + at * kLatent;
 #pragma unroll
   for (int d = 0; d < kCols; ++d)
@@ -192,26 +403,118 @@ __global__ __launch_bounds__(64 * HG) __attribute__((amdgpu_waves_per_eu(1, 1)))
     for (int g = 0; g < 4; ++g) {
       typename T::v4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = (typename T::elem)(l == 0.f ? 0.f : o[d][4 * g + j] * inv);
+      for (int j = 0; j < 4; ++j) v[j] = (typename T::elem)(o[d][4 * g + j] * inv);
       *reinterpret_cast<typename T::v4*>(out + 32 * d + 8 * g + 4 * h) = v;
     }
-  if (A.lse && h == 0) A.lse[at] = row_lse(st.m, l);
+  if (A.lse && h == 0) A.lse[at] = row_lse(m, l);
+}
+
+// Joins the parts of a row: o = sum_p 2^(m_p - m) o'_p / sum_p 2^(m_p - m) l_p.
+// Two rows a workgroup, four columns a thread.
+template <class T>
+__global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int block_rows, bool paged) {
+  const int rows = A.S * A.H;
+  const int64_t at = (int64_t)blockIdx.x * 2 + (threadIdx.x >> 7);
+  const int b = (int)(at / rows), row = (int)(at % rows), c = (threadIdx.x & 127) * 4;
+  if (b >= A.B) return;
+  int first = b * A.parts, n = A.parts;
+  if (paged) {
+    const int2 p = A.plan[b];
+    first = p.x; n = p.y;
+    if (n == 1) return;  // written by the walk
+  }
+  const int64_t at0 = ((int64_t)first * A.row_blocks + row / block_rows) * block_rows + row % block_rows;
+  const int64_t stride = (int64_t)A.row_blocks * block_rows;
+  float m = -INFINITY;
+  for (int p = 0; p < n; ++p) m = fmaxf(m, A.part_ml[at0 + p * stride].x);
+  const float m0 = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < n; ++p) {
+    const float2 ml = A.part_ml[at0 + p * stride];
+    const float4 v = *reinterpret_cast<const float4*>(A.part_o + (at0 + p * stride) * kLatent + c);
+    const float f = __builtin_amdgcn_exp2f(ml.x - m0);
+    l = fmaf(ml.y, f, l);
+    o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  typename T::v4 v;
+  v[0] = (typename T::elem)(o.x * inv); v[1] = (typename T::elem)(o.y * inv);
+  v[2] = (typename T::elem)(o.z * inv); v[3] = (typename T::elem)(o.w * inv);
+  *reinterpret_cast<typename T::v4*>(reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + c) = v;
+  if (A.lse && c == 0) A.lse[at] = row_lse(m, l);
 }
 
 // ------------------------------------------------------------------ host
 
 static inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+static inline size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// How a call is cut: 32 * hg rows a workgroup, `parts` as in LatArgs.
+struct LatGeom {
+  int hg, row_blocks, parts;
+  int64_t cells;  // partial results of 32 * hg rows each (0: none)
+  size_t o, ml, plan, total;
+};
+
+static LatGeom layout(LatGeom g, int64_t B) {
+  const size_t rows = (size_t)(g.cells * 32 * g.hg);
+  size_t at = 0;
+  g.o = at; at = a256(at + rows * kLatent * 4);
+  g.ml = at; at = a256(at + rows * 8);
+  g.plan = at; at = a256(at + (size_t)B * 8);
+  g.total = at < 256 ? 256 : at;
+  return g;
+}
+
+static LatGeom listed_geom(int32_t T, int32_t H, int32_t K) {
+  LatGeom g{};
+  g.hg = H <= 32 ? 1 : H <= 64 ? 2 : 4;
+  g.row_blocks = (H + 32 * g.hg - 1) / (32 * g.hg);
+  // lists are split where the tokens alone leave compute units idle; a part
+  // keeps at least two tiles
+  const int64_t groups = (int64_t)T * g.row_blocks;
+  int64_t parts = groups > 0 ? kUnits / groups : 1;
+  const int most = (K + 2 * kTileKeys - 1) / (2 * kTileKeys);
+  if (parts > most) parts = most;
+  g.parts = parts < 1 ? 1 : (int)parts;
+  g.cells = g.parts > 1 ? groups * g.parts : 0;
+  return layout(g, 0);
+}
+
+static LatGeom paged_geom(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
+  LatGeom g{};
+  const int rows = S * H;
+  g.hg = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
+  g.row_blocks = (rows + 32 * g.hg - 1) / (32 * g.hg);
+  int64_t parts = B;
+  if (B <= kPlanBatch && max_pages > kMinPages) {
+    parts = kUnits / g.row_blocks;
+    if (parts < 2 * (int64_t)B) parts = 2 * (int64_t)B;
+    const int64_t most = (int64_t)B * ((max_pages + kMinPages - 1) / kMinPages) + B;
+    if (parts > most) parts = most;
+  }
+  g.parts = (int)parts;
+  g.cells = parts > B ? parts * g.row_blocks : 0;
+  return layout(g, B);
+}
 
 template <class T, bool PAGED>
-static int launch(LatArgs A, hipStream_t stream) {
-  const int rows = A.S * A.H;
-  const int hg = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
-  A.row_blocks = (rows + 32 * hg - 1) / (32 * hg);
-  const int64_t grid = (int64_t)A.B * A.row_blocks;
-  if (grid > 0x7fffffffLL) return IDX_EUNSUPPORTED;
-  if (hg == 1) k_latent<T, 1, PAGED><<<dim3((uint32_t)grid), dim3(64), 0, stream>>>(A);
-  else if (hg == 2) k_latent<T, 2, PAGED><<<dim3((uint32_t)grid), dim3(128), 0, stream>>>(A);
-  else k_latent<T, 4, PAGED><<<dim3((uint32_t)grid), dim3(256), 0, stream>>>(A);
+static int launch(LatArgs A, const LatGeom& g, char* ws, hipStream_t stream) {
+  A.row_blocks = g.row_blocks;
+  A.parts = g.parts;
+  A.part_o = reinterpret_cast<float*>(ws + g.o);
+  A.part_ml = reinterpret_cast<float2*>(ws + g.ml);
+  A.plan = reinterpret_cast<int2*>(ws + g.plan);
+  const int64_t grid = (int64_t)(PAGED ? 1 : A.B) * g.parts * g.row_blocks;
+  const int64_t join = ((int64_t)A.B * A.S * A.H + 1) / 2;
+  if (grid > 0x7fffffffLL || join > 0x7fffffffLL) return IDX_EUNSUPPORTED;
+  const dim3 n((uint32_t)grid);
+  if (g.hg == 1) k_latent<T, 1, 2, PAGED><<<n, dim3(128), 0, stream>>>(A);
+  else if (g.hg == 2) k_latent<T, 2, 2, PAGED><<<n, dim3(256), 0, stream>>>(A);
+  else k_latent<T, 4, 1, PAGED><<<n, dim3(256), 0, stream>>>(A);
+  if (g.cells) k_latent_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, 32 * g.hg, PAGED);
   return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
 
@@ -230,7 +533,7 @@ static int check_common(const void* q, const void* cache, const int32_t* list, i
 
 size_t latent_selected_workspace_bytes(int32_t T, int32_t H, int32_t K) {
   if (T < 0 || H < 1 || H > kMaxHeads || K < 1 || K > IDX_TOPK_KMAX) return 0;
-  return 256;
+  return listed_geom(T, H, K).total;
 }
 
 int latent_selected(const void* q, int64_t q_token, int64_t q_head, const void* cache, int64_t num_slots,
@@ -240,17 +543,18 @@ int latent_selected(const void* q, int64_t q_token, int64_t q_head, const void* 
   const int rc = check_common(q, cache, slots, T, H, scale, dtype, out, lse);
   if (rc != IDX_OK || T == 0) return rc;
   if (!slots || (!cache && num_slots > 0)) return IDX_EINVAL;
-  const size_t need = latent_selected_workspace_bytes(T, H, K);
-  if (!workspace || workspace_bytes < need) return IDX_EWORKSPACE;
+  const LatGeom g = listed_geom(T, H, K);
+  if (!workspace || workspace_bytes < g.total) return IDX_EWORKSPACE;
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   LatArgs A{static_cast<const char*>(q), q_token, 0, q_head, static_cast<const char*>(cache), num_slots, slots,
-            nullptr, K, T, 1, H, 0, scale * kLog2e, static_cast<char*>(out), lse};
-  return dtype == IDX_TOPK_BF16 ? launch<TBf16, false>(A, stream) : launch<TF16, false>(A, stream);
+            nullptr, K, T, 1, H, 0, 0, scale * kLog2e, static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
+  char* const ws = static_cast<char*>(workspace);
+  return dtype == IDX_TOPK_BF16 ? launch<TBf16, false>(A, g, ws, stream) : launch<TF16, false>(A, g, ws, stream);
 }
 
 size_t latent_paged_workspace_bytes(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
   if (B < 0 || S < 1 || S > IDX_TOPK_MAX_STEPS || H < 1 || H > kMaxHeads || max_pages < 0) return 0;
-  return 256;
+  return paged_geom(B, S, H, max_pages).total;
 }
 
 int latent_paged(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, const void* cache,
@@ -264,13 +568,14 @@ int latent_paged(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, 
   const int rc = check_common(q, cache, page_table, B, H, scale, dtype, out, lse);
   if (rc != IDX_OK || B == 0) return rc;
   if (!seq_lens || (!page_table && max_pages > 0) || (!cache && num_pages > 0)) return IDX_EINVAL;
-  const size_t need = latent_paged_workspace_bytes(B, S, H, max_pages);
-  if (!workspace || workspace_bytes < need) return IDX_EWORKSPACE;
+  const LatGeom g = paged_geom(B, S, H, max_pages);
+  if (!workspace || workspace_bytes < g.total) return IDX_EWORKSPACE;
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   LatArgs A{static_cast<const char*>(q), q_seq, q_token, q_head, static_cast<const char*>(cache),
-            (int64_t)num_pages * IDX_TOPK_PAGE, page_table, seq_lens, max_pages, B, S, H, 0, scale * kLog2e,
-            static_cast<char*>(out), lse};
-  return dtype == IDX_TOPK_BF16 ? launch<TBf16, true>(A, stream) : launch<TF16, true>(A, stream);
+            (int64_t)num_pages * IDX_TOPK_PAGE, page_table, seq_lens, max_pages, B, S, H, 0, 0, scale * kLog2e,
+            static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
+  char* const ws = static_cast<char*>(workspace);
+  return dtype == IDX_TOPK_BF16 ? launch<TBf16, true>(A, g, ws, stream) : launch<TF16, true>(A, g, ws, stream);
 }
 
 }  // namespace idxk
