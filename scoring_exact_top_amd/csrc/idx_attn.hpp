@@ -164,4 +164,21 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
 }
 
+// 64 lanes x 16 bytes from src + off (a lane's) to 1 KiB of LDS in lane order,
+// without registers.  The compiler does not see the write: the tile waits
+// below order it.
+__device__ __forceinline__ void dma_row(const char* src, int off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(src));
+}
+__device__ __forceinline__ void dma_lanes(const char* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src));
+}
+// All but the last N of this wave's loads to LDS are done.
+template <int N>
+__device__ __forceinline__ void dma_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Every wave is here, and has its LDS reads back.
+__device__ __forceinline__ void tile_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 }  // namespace idxk
