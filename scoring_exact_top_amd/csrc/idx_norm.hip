@@ -35,6 +35,21 @@ __device__ __forceinline__ float wave_max(float x) {
   return x;
 }
 
+// The scale of a group whose largest magnitude is top: 1 for an all-zero group
+// (and for one so small that its scale would round to 0).
+__device__ __forceinline__ float scale_of(float top) {
+  const float s = top / kE4m3Max;
+  return s > 0.f ? s : 1.f;
+}
+
+// value / scale as value * up * inv: one division a group.  `up` lifts scales
+// whose reciprocal would overflow (a power of two: exact).
+struct Scaler {
+  float up, inv;
+  __device__ __forceinline__ explicit Scaler(float scale) : up(scale < 0x1p-100f ? 0x1p60f : 1.f), inv(1.f / (scale * up)) {}
+  __device__ __forceinline__ float operator()(float v) const { return v * up * inv; }
+};
+
 // One row a workgroup, element by element, h computed again in each pass:
 // any width, stride and alignment.
 template <class E>
@@ -67,10 +82,9 @@ __global__ __launch_bounds__(256) void k_norm_any(NormArgs A) {
     __syncthreads();
     top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
     __syncthreads();
-    const float scale = top > 0.f ? top / kE4m3Max : 1.f;
-    for (int i = g0 + tid; i < g0 + step; i += 256) {
-      A.codes[row * A.width + i] = (uint8_t)e4m3x2_enc(value(i) / scale, 0.f);
-    }
+    const float scale = scale_of(top);
+    const Scaler to(scale);
+    for (int i = g0 + tid; i < g0 + step; i += 256) A.codes[row * A.width + i] = (uint8_t)e4m3x2_enc(to(value(i)), 0.f);
     if (tid == 0) A.scales[row * (A.width / step) + g] = scale;
   }
   if (A.residual_out) {
@@ -79,6 +93,134 @@ __global__ __launch_bounds__(256) void k_norm_any(NormArgs A) {
     __syncthreads();
     for (int i = tid; i < A.width; i += 256) out[i] = (E)hidden(i);
   }
+}
+
+// Rows that are 16-byte aligned, 8 numbers a load: TPR threads a row (16, 64
+// or 256), NC chunks of 8 a thread, h kept in registers between the passes, so
+// that every byte is moved once.  A group of 128 columns is 16 neighbouring
+// chunks: its maximum needs four exchanges within 16 lanes.
+template <class E, int TPR, int NC>
+__global__ __launch_bounds__(256) void k_norm_rows(NormArgs A) {
+  typedef E v8 __attribute__((ext_vector_type(8)));
+  __shared__ float s_red[2][4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t row = (int64_t)blockIdx.x * (256 / TPR) + tid / TPR;
+  const int at = tid % TPR;  // this thread's first chunk
+  const int chunks = A.width >> 3;
+  const bool live = row < A.rows;
+  const E* x = static_cast<const E*>(A.x) + row * A.x_stride;
+  const E* res = A.residual ? static_cast<const E*>(A.residual) + row * A.residual_stride : nullptr;
+  const v8* w = static_cast<const v8*>(A.weight);
+
+  float h[NC][8];
+  {
+    v8 xv[NC], rv[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int i = at + c * TPR;
+      const bool in = live && i < chunks;
+      xv[c] = in ? *reinterpret_cast<const v8*>(x + 8 * i) : v8{};
+      rv[c] = in && res ? *reinterpret_cast<const v8*>(res + 8 * i) : v8{};
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[c][j] = res ? (float)xv[c][j] + (float)rv[c][j] : (float)xv[c][j];
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    float t = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = fmaf(h[c][j], h[c][j], t);
+    ss += t;
+  }
+#pragma unroll
+  for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1) ss += __shfl_xor(ss, d, 64);
+  if (TPR == 256) {
+    if (lane == 0) s_red[0][wave] = ss;
+    __syncthreads();
+    ss = (s_red[0][0] + s_red[0][1]) + (s_red[0][2] + s_red[0][3]);
+  }
+  if (A.residual_out) {
+    v8* out = reinterpret_cast<v8*>(static_cast<E*>(A.residual_out) + row * A.width);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int i = at + c * TPR;
+      v8 v;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (E)h[c][j];
+      if (live && i < chunks) out[i] = v;
+    }
+  }
+  const float rstd = 1.f / sqrtf(ss / (float)A.width + A.eps);
+  float top[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = at + c * TPR;
+    v8 wv = {};
+    if (w && i < chunks) wv = w[i];
+    top[c] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      h[c][j] = h[c][j] * rstd * (w ? (float)wv[j] : 1.f);
+      top[c] = fmaxf(top[c], fabsf(h[c][j]));
+    }
+  }
+  if (A.group) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) top[c] = fmaxf(top[c], __shfl_xor(top[c], d, 64));
+  } else {
+    float t = top[0];
+#pragma unroll
+    for (int c = 1; c < NC; ++c) t = fmaxf(t, top[c]);
+#pragma unroll
+    for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1) t = fmaxf(t, __shfl_xor(t, d, 64));
+    if (TPR == 256) {
+      if (lane == 0) s_red[1][wave] = t;
+      __syncthreads();
+      t = fmaxf(fmaxf(s_red[1][0], s_red[1][1]), fmaxf(s_red[1][2], s_red[1][3]));
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) top[c] = t;
+  }
+  if (!live) return;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = at + c * TPR;
+    if (i >= chunks) break;
+    const float scale = scale_of(top[c]);
+    const Scaler to(scale);
+    uint2 v;
+    v.x = e4m3x2_enc(to(h[c][0]), to(h[c][1])) | e4m3x2_enc(to(h[c][2]), to(h[c][3])) << 16;
+    v.y = e4m3x2_enc(to(h[c][4]), to(h[c][5])) | e4m3x2_enc(to(h[c][6]), to(h[c][7])) << 16;
+    *reinterpret_cast<uint2*>(A.codes + row * A.width + 8 * i) = v;
+    if (A.group) {
+      if ((i & 15) == 0) A.scales[row * (A.width / kGroup) + (i >> 4)] = scale;
+    } else if (i == 0) {
+      A.scales[row] = scale;
+    }
+  }
+}
+
+template <class E>
+static void launch_norm(const NormArgs& A, hipStream_t stream) {
+  const bool wide = (A.width & 7) == 0 && (((uintptr_t)A.x | (uintptr_t)A.residual | (uintptr_t)A.weight |
+                    (uintptr_t)A.residual_out) & 15u) == 0 && ((uintptr_t)A.codes & 7u) == 0 &&
+                    (A.rows == 1 || (A.x_stride & 7) == 0) && (!A.residual || A.rows == 1 || (A.residual_stride & 7) == 0);
+  const int chunks = A.width >> 3;
+  const auto grid = [&](int tpr) { return dim3((uint32_t)(((int64_t)A.rows * tpr + 255) / 256)); };
+  if (!wide) k_norm_any<E><<<dim3(A.rows), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 16) k_norm_rows<E, 16, 1><<<grid(16), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 64) k_norm_rows<E, 64, 1><<<grid(64), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 128) k_norm_rows<E, 64, 2><<<grid(64), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 256) k_norm_rows<E, 256, 1><<<grid(256), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 512) k_norm_rows<E, 256, 2><<<grid(256), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 768) k_norm_rows<E, 256, 3><<<grid(256), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 1024) k_norm_rows<E, 256, 4><<<grid(256), dim3(256), 0, stream>>>(A);
+  else k_norm_rows<E, 256, 8><<<grid(256), dim3(256), 0, stream>>>(A);
 }
 
 struct AppendArgs {
@@ -113,8 +255,9 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs A) {
     const E* k = reinterpret_cast<const E*>(A.keys) + t * A.key_token + 2 * lane;
     const float a = (float)k[0], b = (float)k[1];
     const float top = wave_max(fmaxf(fabsf(a), fabsf(b)));
-    const float scale = top > 0.f ? top / kE4m3Max : 1.f;
-    reinterpret_cast<uint16_t*>(A.k_cache + slot * kD)[lane] = (uint16_t)e4m3x2_enc(a / scale, b / scale);
+    const float scale = scale_of(top);
+    const Scaler to(scale);
+    reinterpret_cast<uint16_t*>(A.k_cache + slot * kD)[lane] = (uint16_t)e4m3x2_enc(to(a), to(b));
     if (lane == 0) A.k_scale[slot] = scale;
   }
 }
@@ -138,8 +281,8 @@ int norm_quant(const void* x, int64_t x_stride, const void* residual, int64_t re
   if (rows > 1 && residual_out && ((residual_out == x && x_stride != width) || (residual_out == residual && residual_stride != width)))
     return IDX_EINVAL;
   const NormArgs A{x, x_stride, residual, residual_stride, weight, eps, rows, width, group, codes, scales, residual_out};
-  if (dtype == IDX_TOPK_BF16) k_norm_any<__bf16><<<dim3(rows), dim3(256), 0, stream>>>(A);
-  else k_norm_any<_Float16><<<dim3(rows), dim3(256), 0, stream>>>(A);
+  if (dtype == IDX_TOPK_BF16) launch_norm<__bf16>(A, stream);
+  else launch_norm<_Float16>(A, stream);
   return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
 

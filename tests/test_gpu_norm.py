@@ -80,6 +80,22 @@ def test_norm_zero_rows_and_groups():
     assert torch.isfinite(scales).all() and (codes[1].float() == 448).all()
 
 
+def test_norm_tiny_values():
+    """Rows so small that their scales' reciprocals pass FP32's range, and ones whose scales would be 0: codes of the
+    definition, no NaN, positive scales."""
+    import scoring_exact_top_amd as lib
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    x[0] = torch.linspace(-1, 1, 256).to(torch.bfloat16) * 2.0 ** -118
+    x[1, 7], x[2, 9], x[3] = 2.0 ** -125, 2.0 ** -133, 1.0
+    w = torch.full((256,), 2.0 ** -6, dtype=torch.bfloat16)
+    codes, scales, _ = lib.norm_quant(x.cuda(), w.cuda(), 1.0)
+    assert torch.isfinite(codes.float()).all() and (scales > 0).all()
+    _, y = _norm(x, None, w, 1.0)
+    # FP32 keeps multiples of 2^-149: the first row's values (2^-124) and scale (2^-133) hold 16 bits of them
+    _check_codes(codes[:1].cpu(), scales[:1, 0], y[:1], 2.0 ** -15, "tiny")
+    assert float(codes[1, 7].float()) == 448 and int((codes[1].float() != 0).sum()) == 1
+
+
 def test_norm_strides_in_place_and_streams():
     """Rows of wider tensors (aligned and not), the residual updated in place, and a stream of its own."""
     import scoring_exact_top_amd as lib
