@@ -56,6 +56,8 @@ typedef int w4i __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void mfma_v_done(v16f& c) { asm volatile("s_nop 15\n\ts_nop 7" : "+v"(c)); }
 
 struct TBf16 {
+  // octaves that p may pass 1 by: o' and l stay far inside FP32's 2^127
+  static constexpr float kHeadroom = 64.f;
   typedef __bf16 elem;
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
   typedef __bf16 v4 __attribute__((ext_vector_type(4)));
@@ -67,6 +69,7 @@ struct TBf16 {
 };
 
 struct TF16 {
+  static constexpr float kHeadroom = 15.f;  // half ends below 2^16
   typedef _Float16 elem;
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
   typedef _Float16 v4 __attribute__((ext_vector_type(4)));
@@ -106,8 +109,18 @@ __device__ __forceinline__ typename T::v8 cat(typename T::v4 a, typename T::v4 b
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// The value of the other half of the wave (lane l ^ 32).
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+// The value of the other half of the wave (lane l ^ 32): the swap exchanges
+// the upper half of one register with the lower half of another.
+__device__ __forceinline__ float other_half(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// Maximum over a lane and the lane l ^ 32.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 
 // Key of a 32-key tile whose logit is in register r of wave half h.
 __device__ __forceinline__ constexpr int key_of(int r, int h) { return (r & 3) + 8 * (r >> 2) + 4 * h; }
@@ -123,7 +136,7 @@ __device__ __forceinline__ float tile_max(const v16f& x, float c) {
   float mx = x[0];
 #pragma unroll
   for (int r = 1; r < 16; ++r) mx = fmaxf(mx, x[r]);
-  return fmaxf(mx, other_half(mx)) * c;
+  return max_halves(mx) * c;
 }
 
 // Whether some row of the wave has to move its reference for a tile of

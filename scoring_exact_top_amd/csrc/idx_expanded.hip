@@ -76,7 +76,7 @@ __global__ __launch_bounds__(64 * kXWaves, 2) void k_expanded(ExpArgs A) {
   const int koff0 = kr * (int)A.kv_token * 2 + (((lane & 15) ^ row_swz(kr)) << 4);
   const int koff1 = (kr + 4) * (int)A.kv_token * 2 + (((lane & 15) ^ row_swz(kr + 4)) << 4);
   const int roff = rr * (int)A.rope_token * 2 + (((lane & 7) ^ rot_swz(rr)) << 4);
-  const auto load = [&](int t) {
+  const auto load = [&](int t) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + t % kXRing * kXBytes + wave * 2048;
     const uint32_t rdst = lds0 + t % kXRing * kXBytes + kXRope + wave * 1024;
     const char* kt = kv + (int64_t)t * kXTile * A.kv_token * 2;

@@ -42,8 +42,8 @@ struct LatArgs {
   float c;                         // scale * log2(e)
   char* out;
   float* lse;
-  float* part_o;                   // [part * row_blocks + block][32 HG][512]
-  float2* part_ml;                 // [part * row_blocks + block][32 HG]
+  float* part_o;                   // [(part * row_blocks + block) * HG + group] cells of 32 rows x 512 columns
+  float2* part_ml;                 // ... of 32 rows
   int2* plan;                      // paged: [B] first part and number of parts
 };
 
@@ -115,6 +115,7 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
   constexpr int kRows = kTileKeys / HG;          // rows of a tile that one wave loads
   constexpr int kLoads = kRows + 4 / HG;         // its loads to LDS a tile
   __shared__ __attribute__((aligned(1024))) char s_tile[kBuffers * kTileBytes];
+  __shared__ int32_t s_again;
   __shared__ int32_t s_list[PAGED ? 4 : kMaxList + kTileKeys];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hg = wave % HG, kg = wave / HG;
@@ -166,8 +167,6 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
   if (!PAGED) __syncthreads();
 
   v16f o[kCols];
-#pragma unroll
-  for (int d = 0; d < kCols; ++d) o[d] = v16f{};
   RowStat st{-INFINITY, 0.f};
   // this lane's LDS byte offsets in a tile: its key's row (first product; step
   // s at chunk 2s + h), and its two rows of the transposing reads (second)
@@ -178,13 +177,14 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)s_tile;
 
   int lane_r = lane;
-  const int mine = tile0 + kg;                                // this key group's first tile
-  const int steps = tile1 > tile0 ? (tile1 - tile0 + KG - 1) / KG : 0;  // the same for all key groups: barriers
+  const int mine = __builtin_amdgcn_readfirstlane(tile0) + kg;  // this key group's first tile
+  // the same for all key groups: barriers
+  const int steps = __builtin_amdgcn_readfirstlane(tile1 > tile0 ? (tile1 - tile0 + KG - 1) / KG : 0);
 
   // Slot of key `col` of step i's tile (-1: none).
-  const auto slot_of = [&](int i) -> int { return s_list[(i * KG + kg) * kTileKeys + (lane_r & 31)]; };
+  const auto slot_of = [&](int i) __attribute__((always_inline)) -> int { return s_list[(i * KG + kg) * kTileKeys + (lane_r & 31)]; };
   // Physical page of step i's tile, -1: none (a tile lies in one page).
-  const auto page_of = [&](int i) -> int {
+  const auto page_of = [&](int i) __attribute__((always_inline)) -> int {
     const int key = (mine + i * KG) * kTileKeys;
     if (key >= len) return -1;
     // a scalar load: vector loads would queue behind the tile loads
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     return pg >= 0 && (int64_t)pg * IDX_TOPK_PAGE < A.num_slots ? pg : -1;
   };
   // Starts this wave's share of step i's tile.
-  const auto load = [&](int i) {
+  const auto load = [&](int i) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + (kg * kRing + i % kRing) * kTileBytes;
     const char* const zero = reinterpret_cast<const char*>(kZeroRow);
     const int key0 = (mine + i * KG) * kTileKeys;
@@ -236,37 +236,45 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     }
   };
 
-#pragma unroll
-  for (int i = 0; i < kRing; ++i)
-    if (i < steps) load(i);
-  typename T::v8 q[kSteps];
+  const auto load_first = [&]() __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int i = 0; i < min(kRing, steps); ++i) load(i);
+  };
+  load_first();
+  typename T::v8 q[kSteps];  // a row past the last repeats the first: its results are dropped
   {
     const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + step * A.q_token +
                                 head * A.q_head + 8 * h;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      if (have) q[s] = *reinterpret_cast<const typename T::v8*>(p + 16 * s);
-      else q[s] = typename T::v8{};
-    }
+    for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 16 * s);
   }
 
   // Waits for step i's tile and computes its logits, masked.
-  const auto logits = [&](int i) {
+  const auto logits = [&](int i) __attribute__((always_inline)) {
     if (i + kRing <= steps) dma_wait<(kRing - 1) * kLoads>();
     else dma_wait<0>();
     tile_barrier();
     const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
     int ka = kaddr, ra = raddr;
     asm volatile("" : "+v"(ka), "+v"(ra));  // the offsets below are made here, not kept in registers
+    // products of four steps on one set of operands while the next set is read
+    typename T::v8 k[2][4];
+    const auto read = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        k[g & 1][u] = g < kLatSteps / 4 ? lds_read<typename T::v8>(tile + (ka ^ (g << 5)) + 256 * u)
+                                        : lds_read<typename T::v8>(tile + (ra ^ (u << 5)));
+    };
     v16f x;
+    read(0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const char* p = tile + (ka ^ (j << 5));
+    for (int g = 0; g < kSteps / 4; ++g) {
+      if (g + 1 < kSteps / 4) read(g + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int u = 0; u < kLatSteps / 8; ++u) T::mfma_v(x, lds_read<typename T::v8>(p + 256 * u), q[8 * u + j], j + u == 0);
+      for (int u = 0; u < 4; ++u) T::mfma_v(x, k[g & 1][u], q[g < kLatSteps / 4 ? 8 * u + g : kLatSteps + u], g + u == 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int j = 0; j < kRope / 16; ++j) T::mfma_v(x, lds_read<typename T::v8>(tile + (ra ^ (j << 5))), q[kLatSteps + j], false);
     mfma_v_done(x);
     const int key0 = (mine + i * KG) * kTileKeys;
     uint32_t live;
@@ -284,51 +292,66 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     return x;
   };
 
-  // o' fills the accumulator registers, and q most of the others.  The inner
-  // loop touches o' with MFMAs only and leaves to the outer one where a
-  // reference moves (rare).  Rescaling takes o' through the other registers, q
-  // to memory and back; the touch behind it makes the compiler wait for that
-  // there, not in the inner loop, where its waits would drain the tile loads in
-  // flight at every step.
-  if (steps > 0) {
-    int i = 0;
-    v16f x = logits(0);
-    float mx = tile_max(x, A.c);
-    for (;;) {
-      const float alpha = move_reference(st, mx);
+  // o' fills the accumulator registers and q most of the others, so rescaling
+  // o' where a row's maximum grows would take all of it through registers
+  // that are not there.  The reference stays at the row's first live tile's
+  // maximum instead: p may grow to kHeadroom octaves above 1, which costs no
+  // precision.  A workgroup that sees more walks its keys again, first for the
+  // rows' true maxima, then with those as references.
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // q is there: the waits below count tile loads only
+  for (int attempt = 0;; ++attempt) {
 #pragma unroll
-      for (int d = 0; d < kCols; ++d) o[d] *= alpha;
+    for (int d = 0; d < kCols; ++d) o[d] = v16f{};
+    float over = -INFINITY;  // the most octaves by which a logit passed its row's reference
+    for (int i = 0; i < steps; ++i) {
+      v16f x = logits(i);
+      const float mx = tile_max(x, A.c);
+      st.m = st.m == -INFINITY ? mx : st.m;
+      over = fmaxf(over, mx - st.m);
+      softmax_tile(x, st, A.c);
+      const typename T::v8 p0 = p_operand<T>(x, 0), p1 = p_operand<T>(x, 1);
+      const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
+      int va0 = vaddr0, va1 = vaddr1;
+      asm volatile("" : "+v"(va0), "+v"(va1));
+      // group g: columns of block row j = g / 2 for the keys of step g & 1
+      typename T::v8 v[2][4];
+      const auto read = [&](int g) __attribute__((always_inline)) {
+        const char* pa = tile + (va0 ^ (g >> 1 << 6)) + (g & 1) * 16 * kLatent * 2;
+        const char* pb = tile + (va1 ^ (g >> 1 << 6)) + (g & 1) * 16 * kLatent * 2;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) asm volatile("" : "+v"(q[s]));
-      asm volatile("" : "+v"(x), "+v"(kaddr), "+v"(raddr), "+v"(vaddr0), "+v"(vaddr1), "+v"(lane_r), "+v"(limit), "+v"(st.m), "+v"(st.l));
-      for (;;) {
-        softmax_tile(x, st, A.c);
-        const typename T::v8 p0 = p_operand<T>(x, 0), p1 = p_operand<T>(x, 1);
-        const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
-        int va0 = vaddr0, va1 = vaddr1;
-        asm volatile("" : "+v"(va0), "+v"(va1));
+        for (int u = 0; u < 4; ++u) v[g & 1][u] = cat<T>(lds_read_tr<T>(pa + 256 * u), lds_read_tr<T>(pb + 256 * u));
+      };
+      read(0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const char* pa = tile + (va0 ^ (j << 6));
-          const char* pb = tile + (va1 ^ (j << 6));
+      for (int g = 0; g < kCols / 2; ++g) {
+        if (g + 1 < kCols / 2) read(g + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int u = 0; u < kCols / 4; ++u) {
-            const int d = 4 * u + j;
-            o[d] = T::mfma(cat<T>(lds_read_tr<T>(pa + 256 * u), lds_read_tr<T>(pb + 256 * u)), p0, o[d]);
-            o[d] = T::mfma(cat<T>(lds_read_tr<T>(pa + 256 * u + 16 * kLatent * 2), lds_read_tr<T>(pb + 256 * u + 16 * kLatent * 2)),
-                           p1, o[d]);
-          }
+        for (int u = 0; u < 4; ++u) {
+          const int d = 4 * u + (g >> 1);
+          o[d] = T::mfma(v[g & 1][u], g & 1 ? p1 : p0, o[d]);
         }
-        tile_barrier();  // the tile is read: its buffer takes the next load
-        if (i + kRing < steps) load(i + kRing);
-        ++i;
-        if (i >= steps) break;
-        x = logits(i);
-        mx = tile_max(x, A.c);
-        if (must_move(st, mx)) break;
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (i >= steps) break;
+      tile_barrier();  // the tile is read: its buffer takes the next load
+      if (i + kRing < steps) load(i + kRing);
     }
+    if (attempt > 0) break;
+    if (tid == 0) s_again = 0;
+    __syncthreads();
+    if (__any(over > T::kHeadroom) && lane == 0) s_again = 1;
+    __syncthreads();
+    if (!__builtin_amdgcn_readfirstlane(s_again)) break;
+    st = RowStat{-INFINITY, 0.f};
+    load_first();
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+      const v16f x = logits(i);
+      st.m = fmaxf(st.m, tile_max(x, A.c));
+      tile_barrier();
+      if (i + kRing < steps) load(i + kRing);
+    }
+    load_first();
   }
   float l = st.l + other_half(st.l), m = st.m;
 
@@ -364,19 +387,20 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
         o[d][4 * g + 3] = o[d][4 * g + 3] * f0 + v.w * f1;
       }
   }
-  if (!have) return;
   if (part.parts > 1) {
-    const int64_t at = (int64_t)(wg * A.row_blocks + rb) * (32 * HG) + hg * 32 + col;
-    float* po = A.part_o + at * kLatent;
+    // in the order of the registers: whole lines, and the join adds them in that order too
+    const int64_t cell = (int64_t)(wg * A.row_blocks + rb) * HG + hg;
+    float* po = A.part_o + cell * (32 * kLatent) + lane * 4;
 #pragma unroll
     for (int d = 0; d < kCols; ++d)
 #pragma unroll
       for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<float4*>(po + 32 * d + 8 * g + 4 * h) =
+        *reinterpret_cast<float4*>(po + (d * 4 + g) * 256) =
             make_float4(o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]);
-    if (h == 0) A.part_ml[at] = make_float2(m, l);
+    if (h == 0) A.part_ml[cell * 32 + col] = make_float2(m, l);
     return;
   }
+  if (!have) return;
   const int64_t at = ((int64_t)b * A.S + step) * A.H + head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   typename T::elem* out = reinterpret_cast<typename T::elem*>(A.out) + at * kLatent;
@@ -393,40 +417,46 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
 }
 
 // Joins the parts of a row: o = sum_p 2^(m_p - m) o'_p / sum_p 2^(m_p - m) l_p.
-// Two rows a workgroup, four columns a thread.
+// A wave takes 256 of the 16384 numbers of a cell (32 rows x 512 columns in
+// the order of the walk's registers), a workgroup four such pieces.
 template <class T>
-__global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int block_rows, bool paged) {
-  const int rows = A.S * A.H;
-  const int64_t at = (int64_t)blockIdx.x * 2 + (threadIdx.x >> 7);
-  const int b = (int)(at / rows), row = (int)(at % rows), c = (threadIdx.x & 127) * 4;
-  if (b >= A.B) return;
+__global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int hgs, bool paged) {
+  const int lane = threadIdx.x & 63, piece = (blockIdx.x & 15) * 4 + (threadIdx.x >> 6);
+  const int groups = A.row_blocks * hgs;  // 32-row groups of a token or sequence
+  const int unit = blockIdx.x >> 4, b = unit / groups, group = unit % groups;
+  const int row = group * 32 + (lane & 31);
   int first = b * A.parts, n = A.parts;
   if (paged) {
     const int2 p = A.plan[b];
     first = p.x; n = p.y;
     if (n == 1) return;  // written by the walk
   }
-  const int64_t at0 = ((int64_t)first * A.row_blocks + row / block_rows) * block_rows + row % block_rows;
-  const int64_t stride = (int64_t)A.row_blocks * block_rows;
+  if (row >= A.S * A.H) return;
+  const int64_t cell0 = (int64_t)first * groups + group;
+  const float2* ml = A.part_ml + cell0 * 32 + (lane & 31);
+  const float4* po = reinterpret_cast<const float4*>(A.part_o + cell0 * (32 * kLatent) + piece * 256) + lane;
   float m = -INFINITY;
-  for (int p = 0; p < n; ++p) m = fmaxf(m, A.part_ml[at0 + p * stride].x);
+#pragma unroll 8
+  for (int p = 0; p < n; ++p) m = fmaxf(m, ml[(int64_t)p * groups * 32].x);
   const float m0 = m == -INFINITY ? 0.f : m;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int p = 0; p < n; ++p) {
-    const float2 ml = A.part_ml[at0 + p * stride];
-    const float4 v = *reinterpret_cast<const float4*>(A.part_o + (at0 + p * stride) * kLatent + c);
-    const float f = __builtin_amdgcn_exp2f(ml.x - m0);
-    l = fmaf(ml.y, f, l);
+    const float2 s = ml[(int64_t)p * groups * 32];
+    const float4 v = po[(int64_t)p * groups * (32 * kLatent / 4)];
+    const float f = __builtin_amdgcn_exp2f(s.x - m0);
+    l = fmaf(s.y, f, l);
     o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   typename T::v4 v;
   v[0] = (typename T::elem)(o.x * inv); v[1] = (typename T::elem)(o.y * inv);
   v[2] = (typename T::elem)(o.z * inv); v[3] = (typename T::elem)(o.w * inv);
-  *reinterpret_cast<typename T::v4*>(reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + c) = v;
-  if (A.lse && c == 0) A.lse[at] = row_lse(m, l);
+  const int64_t at = (int64_t)b * A.S * A.H + row;  // rows of a sequence are its steps' heads in order
+  const int column = 32 * (piece >> 2) + 8 * (piece & 3) + 4 * (lane >> 5);
+  *reinterpret_cast<typename T::v4*>(reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + column) = v;
+  if (A.lse && column == 0) A.lse[at] = row_lse(m, l);
 }
 
 // ------------------------------------------------------------------ host
@@ -491,13 +521,13 @@ static int launch(LatArgs A, const LatGeom& g, char* ws, hipStream_t stream) {
   A.part_ml = reinterpret_cast<float2*>(ws + g.ml);
   A.plan = reinterpret_cast<int2*>(ws + g.plan);
   const int64_t grid = (int64_t)(PAGED ? 1 : A.B) * g.parts * g.row_blocks;
-  const int64_t join = ((int64_t)A.B * A.S * A.H + 1) / 2;
+  const int64_t join = (int64_t)A.B * g.row_blocks * g.hg * 16;
   if (grid > 0x7fffffffLL || join > 0x7fffffffLL) return IDX_EUNSUPPORTED;
   const dim3 n((uint32_t)grid);
   if (g.hg == 1) k_latent<T, 1, 2, PAGED><<<n, dim3(128), 0, stream>>>(A);
   else if (g.hg == 2) k_latent<T, 2, 2, PAGED><<<n, dim3(256), 0, stream>>>(A);
   else k_latent<T, 4, 1, PAGED><<<n, dim3(256), 0, stream>>>(A);
-  if (g.cells) k_latent_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, 32 * g.hg, PAGED);
+  if (g.cells) k_latent_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, g.hg, PAGED);
   return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
 

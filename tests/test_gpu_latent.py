@@ -95,17 +95,21 @@ def test_selected_sizes(T, H, K, N):
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
 
 
-def test_selected_large_and_growing_logits():
-    """Logits that climb through the list move every row's reference again and again; magnitudes up to hundreds."""
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("H,N,rise", [(64, 640, 0.5), (128, 640, 0.5), (16, 640, 0.5), (64, 2048, 0.02), (100, 2048, 0.25), (64, 2048, 1.0)])
+def test_selected_large_and_growing_logits(H, N, rise, dtype):
+    """Logits that climb (and fall) through the list by tens to thousands, past any reference that the first keys give:
+    one token, whose list is split, and many, whose lists are not."""
     lib, g = _lib(), _gen(5)
-    N = 640
-    cache = _rand(g, N, 576, dtype=torch.bfloat16) * 0.05
-    cache[:, 0] = torch.arange(N) * 0.5
-    q = _rand(g, 2, 64, 576, dtype=torch.bfloat16)
-    q[0, :, 0], q[1, :, 0] = 1.0, -1.0
-    slots = torch.arange(N, dtype=torch.int32)[None].repeat(2, 1)
-    out, lse = lib.latent_selected(q.cuda(), cache.to(torch.bfloat16).cuda(), slots.cuda(), 1.0)
-    _check_selected(q, cache.to(torch.bfloat16), slots, out, lse, heads=[0, 31, 63], scale=1.0)
+    cache = (_rand(g, N, 576, dtype=torch.float32) * 0.05).to(dtype)
+    cache[:, 0] = (torch.arange(N) * rise).to(dtype)
+    for T in (2, 300):
+        q = _rand(g, T, H, 576, dtype=torch.float32).to(dtype)
+        q[0::2, :, 0], q[1::2, :, 0] = 1.0, -1.0
+        slots = torch.arange(N, dtype=torch.int32)[None].repeat(T, 1)
+        log("growing logits", H, N, rise, dtype, T)
+        out, lse = lib.latent_selected(q.cuda(), cache.cuda(), slots.cuda(), 1.0)
+        _check_selected(q[-2:], cache, slots[-2:], out[-2:], lse[-2:], heads=[0, H // 2, H - 1], scale=1.0)
 
 
 def test_selected_strides_streams_and_repeats():
@@ -225,6 +229,21 @@ def test_paged_sizes(lens, S, H):
     which = sorted({0, 1 if len(lens) > 1 else 0, len(lens) // 2, len(lens) - 1})
     _check_paged(q, rows, out, lse, sorted({0, H - 1}), which)
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_paged_growing_logits(dtype):
+    """As for listed slots: logits that climb through the sequences by hundreds, with early steps that see fewer keys."""
+    lib, g = _lib(), _gen(13)
+    q, cache, table, n, rows = _paged_case(g, [900, 3, 2000], 2, 40, dtype)
+    for b, r in enumerate(rows):
+        r *= 0.05
+        r[:, 0] = (torch.arange(len(r)) * 0.3).to(dtype)
+        for i in range(0, len(r), 64):
+            cache[int(table[b, i // 64]), :len(r[i:i + 64])] = r[i:i + 64]
+    q[:, :, ::2, 0], q[:, :, 1::2, 0] = 14.0, -14.0
+    out, lse = lib.latent_paged(q.cuda(), cache.cuda(), table.cuda(), n.cuda(), SCALE)
+    _check_paged(q, rows, out, lse, [0, 1, 39])
 
 
 def test_paged_bad_lengths_and_pages():
