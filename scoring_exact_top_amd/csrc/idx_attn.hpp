@@ -44,8 +44,8 @@ typedef int w4i __attribute__((ext_vector_type(4)));
 // c += A B with c in VGPRs.  The compiler gives the results of all MFMAs of a
 // kernel to one register file; where o' takes the whole accumulator file (256
 // registers: 512 columns of 32 rows), the logits must stay out of it.  The
-// two leading wait states cover a VALU write of an operand; sources that come
-// from loads are waited for by the compiler, and mfma_v_done() ends a chain.
+// operands must come from loads, which the compiler waits for (a VALU write of
+// one would need two wait states before), and mfma_v_done() ends a chain.
 #define IDX_MFMA_V(NAME, FIRST, NEXT)                                                       \
   static __device__ __forceinline__ void NAME(v16f& c, v8 a, v8 b, bool first) {            \
     if (first) asm(FIRST : "=&v"(c) : "v"(a), "v"(b));                                      \
@@ -64,8 +64,8 @@ struct TBf16 {
   static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  IDX_MFMA_V(mfma_v, "s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0",
-             "s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0")
+  IDX_MFMA_V(mfma_v, "v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0",
+             "v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0")
 };
 
 struct TF16 {
@@ -76,8 +76,8 @@ struct TF16 {
   static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
-  IDX_MFMA_V(mfma_v, "s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, 0",
-             "s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0")
+  IDX_MFMA_V(mfma_v, "v_mfma_f32_32x32x16_f16 %0, %1, %2, 0",
+             "v_mfma_f32_32x32x16_f16 %0, %1, %2, %0")
 };
 
 constexpr float kLog2e = 1.4426950408889634f;

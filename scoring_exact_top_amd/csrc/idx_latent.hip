@@ -24,6 +24,7 @@ constexpr int kLatSteps = kLatent / 16;   // ... of which in the latent part
 constexpr int kCols = kLatent / 32;       // 32-column blocks of the values
 constexpr int kRopeOff = kTileKeys * kLatent * 2;             // rotary part of a tile, behind the latent parts
 constexpr int kTileBytes = kTileKeys * kLatRow * 2;
+constexpr int kAhead = 6;                 // LDS reads of operands run this many products ahead
 constexpr int kBuffers = 4;               // tiles in LDS: 144 of the 160 KiB
 constexpr int kMaxList = IDX_TOPK_KMAX;
 constexpr int kPlanBatch = 1024;          // larger batches take one workgroup a sequence
@@ -257,24 +258,22 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
     int ka = kaddr, ra = raddr;
     asm volatile("" : "+v"(ka), "+v"(ra));  // the offsets below are made here, not kept in registers
-    // products of four steps on one set of operands while the next set is read
-    typename T::v8 k[2][4];
-    const auto read = [&](int g) __attribute__((always_inline)) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        k[g & 1][u] = g < kLatSteps / 4 ? lds_read<typename T::v8>(tile + (ka ^ (g << 5)) + 256 * u)
-                                        : lds_read<typename T::v8>(tile + (ra ^ (u << 5)));
+    // each product is followed by the read of the operand six products ahead
+    typename T::v8 k[kAhead];
+    const auto read = [&](int n) __attribute__((always_inline)) {
+      k[n % kAhead] = n < kLatSteps ? lds_read<typename T::v8>(tile + (ka ^ (n >> 2 << 5)) + 256 * (n & 3))
+                                    : lds_read<typename T::v8>(tile + (ra ^ ((n - kLatSteps) << 5)));
     };
     v16f x;
-    read(0);
 #pragma unroll
-    for (int g = 0; g < kSteps / 4; ++g) {
-      if (g + 1 < kSteps / 4) read(g + 1);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int n = 0; n < kAhead; ++n) read(n);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) T::mfma_v(x, k[g & 1][u], q[g < kLatSteps / 4 ? 8 * u + g : kLatSteps + u], g + u == 0);
+    for (int n = 0; n < kSteps; ++n) {
       __builtin_amdgcn_sched_barrier(0);
+      T::mfma_v(x, k[n % kAhead], q[n < kLatSteps ? 8 * (n & 3) + (n >> 2) : n], n == 0);
+      if (n + kAhead < kSteps) read(n + kAhead);
     }
+    __builtin_amdgcn_sched_barrier(0);
     mfma_v_done(x);
     const int key0 = (mine + i * KG) * kTileKeys;
     uint32_t live;
@@ -313,26 +312,22 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
       const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
       int va0 = vaddr0, va1 = vaddr1;
       asm volatile("" : "+v"(va0), "+v"(va1));
-      // group g: columns of block row j = g / 2 for the keys of step g & 1
-      typename T::v8 v[2][4];
-      const auto read = [&](int g) __attribute__((always_inline)) {
-        const char* pa = tile + (va0 ^ (g >> 1 << 6)) + (g & 1) * 16 * kLatent * 2;
-        const char* pb = tile + (va1 ^ (g >> 1 << 6)) + (g & 1) * 16 * kLatent * 2;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v[g & 1][u] = cat<T>(lds_read_tr<T>(pa + 256 * u), lds_read_tr<T>(pb + 256 * u));
+      // product n: column block d = 4 (n & 3) + n / 8 for the keys of step (n / 4) & 1
+      typename T::v8 v[kAhead];
+      const auto read = [&](int n) __attribute__((always_inline)) {
+        const int at = (n >> 2 & 1) * 16 * kLatent * 2 + 256 * (n & 3);
+        v[n % kAhead] = cat<T>(lds_read_tr<T>(tile + (va0 ^ (n >> 3 << 6)) + at), lds_read_tr<T>(tile + (va1 ^ (n >> 3 << 6)) + at));
       };
-      read(0);
 #pragma unroll
-      for (int g = 0; g < kCols / 2; ++g) {
-        if (g + 1 < kCols / 2) read(g + 1);
-        __builtin_amdgcn_sched_barrier(0);
+      for (int n = 0; n < kAhead; ++n) read(n);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int d = 4 * u + (g >> 1);
-          o[d] = T::mfma(v[g & 1][u], g & 1 ? p1 : p0, o[d]);
-        }
+      for (int n = 0; n < 2 * kCols; ++n) {
         __builtin_amdgcn_sched_barrier(0);
+        const int d = 4 * (n & 3) + (n >> 3);
+        o[d] = T::mfma(v[n % kAhead], n >> 2 & 1 ? p1 : p0, o[d]);
+        if (n + kAhead < 2 * kCols) read(n + kAhead);
       }
+      __builtin_amdgcn_sched_barrier(0);
       tile_barrier();  // the tile is read: its buffer takes the next load
       if (i + kRing < steps) load(i + kRing);
     }
