@@ -192,54 +192,70 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     const int pg = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)A.list)[(int64_t)b * A.K + key / IDX_TOPK_PAGE];
     return pg >= 0 && (int64_t)pg * IDX_TOPK_PAGE < A.num_slots ? pg : -1;
   };
-  // Starts this wave's share of step i's tile.
-  const auto load = [&](int i) __attribute__((always_inline)) {
-    const uint32_t dst = lds0 + (kg * kRing + i % kRing) * kTileBytes;
-    const char* const zero = reinterpret_cast<const char*>(kZeroRow);
-    const int key0 = (mine + i * KG) * kTileKeys;
-    int slots = 0, live = 0;
-    const char* page = zero;
-    int l16 = lane_r;  // 16 lane, made here as the offsets of the products below
-    asm volatile("" : "+v"(l16));
-    l16 = (l16 ^ (HG == 1 ? 0 : lat_swz(hg * kRows))) << 4;
+  // This wave's share of step i's tile, in kLoads loads: what they need, and
+  // load j of them.
+  struct Source {
+    uint32_t dst;
+    const char* page;  // paged: the tile's first row
+    int live;          // paged: its rows that are there
+    int slots;         // listed: the slot of row `col` of the tile
+    int l16;           // 16 * lane, swizzled as this wave's first row
+  };
+  const auto source = [&](int i) __attribute__((always_inline)) {
+    Source f;
+    f.dst = lds0 + (kg * kRing + i % kRing) * kTileBytes;
+    f.page = reinterpret_cast<const char*>(kZeroRow);
+    f.live = 0;
+    f.slots = -1;
     if (PAGED) {
+      const int key0 = (mine + i * KG) * kTileKeys;
       const int pg = __builtin_amdgcn_readfirstlane(page_of(i));
-      live = pg < 0 ? 0 : min(kTileKeys, len - key0);
-      if (pg >= 0) page = A.cache + ((int64_t)pg * IDX_TOPK_PAGE + key0 % IDX_TOPK_PAGE) * (kLatRow * 2);
+      if (pg >= 0) {
+        f.live = min(kTileKeys, len - key0);
+        f.page = A.cache + ((int64_t)pg * IDX_TOPK_PAGE + key0 % IDX_TOPK_PAGE) * (kLatRow * 2);
+      }
     } else {
-      slots = slot_of(i);
+      f.slots = slot_of(i);
     }
-#pragma unroll
-    for (int j = 0; j < kRows; ++j) {
+    f.l16 = lane_r;
+    asm volatile("" : "+v"(f.l16));  // made here, not kept in registers
+    f.l16 = (f.l16 ^ (HG == 1 ? 0 : lat_swz(hg * kRows))) << 4;
+    return f;
+  };
+  const auto load = [&](const Source& f, int i, int j) __attribute__((always_inline)) {
+    const char* const zero = reinterpret_cast<const char*>(kZeroRow);
+    if (j < kRows) {
       const int r = hg * kRows + j;
       const char* src;
       if (PAGED) {
-        src = r < live ? page + r * (kLatRow * 2) : zero;
+        src = r < f.live ? f.page + r * (kLatRow * 2) : zero;
       } else {
-        const int s = __builtin_amdgcn_readlane(slots, r);
+        const int s = __builtin_amdgcn_readlane(f.slots, r);
         const int64_t at = (int64_t)s * (kLatRow * 2);
         src = A.cache + (s >= 0 ? at : zero - A.cache);
       }
-      dma_row(src, l16 ^ (lat_swz(j) << 4), dst + r * (kLatent * 2));
-    }
-#pragma unroll
-    for (int j = 0; j < 4 / HG; ++j) {
-      const int l = l16 >> 4 ^ (HG == 1 ? 0 : lat_swz(hg * kRows));
-      const int r = 8 * (hg * (4 / HG) + j) + (l >> 3);
+      dma_row(src, f.l16 ^ (lat_swz(j) << 4), f.dst + r * (kLatent * 2));
+    } else {
+      const int n = hg * (4 / HG) + j - kRows;
+      const int l = f.l16 >> 4 ^ (HG == 1 ? 0 : lat_swz(hg * kRows));
+      const int r = 8 * n + (l >> 3);
       const char* src;
       if (PAGED) {
-        src = r < live ? page + r * (kLatRow * 2) : zero;
+        src = r < f.live ? f.page + r * (kLatRow * 2) : zero;
       } else {
         const int s = s_list[(i * KG + kg) * kTileKeys + r];
         src = s >= 0 ? A.cache + (int64_t)s * (kLatRow * 2) : zero;
       }
-      dma_lanes(src + kLatent * 2 + (((l & 7) ^ rope_swz(r)) << 4), dst + kRopeOff + (hg * (4 / HG) + j) * 1024);
+      dma_lanes(src + kLatent * 2 + (((l & 7) ^ rope_swz(r)) << 4), f.dst + kRopeOff + n * 1024);
     }
   };
-
   const auto load_first = [&]() __attribute__((always_inline)) {
 #pragma unroll 1
-    for (int i = 0; i < min(kRing, steps); ++i) load(i);
+    for (int i = 0; i < min(kRing - 1, steps); ++i) {
+      const Source f = source(i);
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) load(f, i, j);
+    }
   };
   load_first();
   typename T::v8 q[kSteps];  // a row past the last repeats the first: its results are dropped
@@ -252,9 +268,11 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
 
   // Waits for step i's tile and computes its logits, masked.
   const auto logits = [&](int i) __attribute__((always_inline)) {
-    if (i + kRing <= steps) dma_wait<(kRing - 1) * kLoads>();
+    if (i + kRing - 1 <= steps) dma_wait<(kRing - 2) * kLoads>();
     else dma_wait<0>();
-    tile_barrier();
+    tile_barrier();  // tile i is there and tile i - 1 is read: its buffer takes the next load
+    const bool more = i + kRing - 1 < steps;
+    const Source next = source(more ? i + kRing - 1 : i);
     const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
     int ka = kaddr, ra = raddr;
     asm volatile("" : "+v"(ka), "+v"(ra));  // the offsets below are made here, not kept in registers
@@ -272,6 +290,11 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
       __builtin_amdgcn_sched_barrier(0);
       T::mfma_v(x, k[n % kAhead], q[n < kLatSteps ? 8 * (n & 3) + (n >> 2) : n], n == 0);
       if (n + kAhead < kSteps) read(n + kAhead);
+      // a load every few products: a burst would wait for the memory pipeline
+      if (n % (kSteps / kLoads) == 0) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) load(next, i + kRing - 1, n / (kSteps / kLoads));
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     mfma_v_done(x);
@@ -328,9 +351,8 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
         if (n + kAhead < 2 * kCols) read(n + kAhead);
       }
       __builtin_amdgcn_sched_barrier(0);
-      tile_barrier();  // the tile is read: its buffer takes the next load
-      if (i + kRing < steps) load(i + kRing);
     }
+    tile_barrier();  // every tile is read
     if (attempt > 0) break;
     if (tid == 0) s_again = 0;
     __syncthreads();
@@ -343,9 +365,8 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     for (int i = 0; i < steps; ++i) {
       const v16f x = logits(i);
       st.m = fmaxf(st.m, tile_max(x, A.c));
-      tile_barrier();
-      if (i + kRing < steps) load(i + kRing);
     }
+    tile_barrier();
     load_first();
   }
   float l = st.l + other_half(st.l), m = st.m;
