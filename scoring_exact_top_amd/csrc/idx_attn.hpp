@@ -39,21 +39,7 @@
 namespace idxk {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef int w4i __attribute__((ext_vector_type(4)));
-
-// c += A B with c in VGPRs.  The compiler gives the results of all MFMAs of a
-// kernel to one register file; where o' takes the whole accumulator file (256
-// registers: 512 columns of 32 rows), the logits must stay out of it.  The
-// operands must come from loads, which the compiler waits for (a VALU write of
-// one would need two wait states before), and mfma_v_done() ends a chain.
-#define IDX_MFMA_V(NAME, FIRST, NEXT)                                                       \
-  static __device__ __forceinline__ void NAME(v16f& c, v8 a, v8 b, bool first) {            \
-    if (first) asm(FIRST : "=&v"(c) : "v"(a), "v"(b));                                      \
-    else asm(NEXT : "+v"(c) : "v"(a), "v"(b));                                              \
-  }
-
-// A 16-pass MFMA's result may be read by VALU instructions 18 wait states later.
-__device__ __forceinline__ void mfma_v_done(v16f& c) { asm volatile("s_nop 15\n\ts_nop 7" : "+v"(c)); }
+typedef float w4f __attribute__((ext_vector_type(4)));
 
 struct TBf16 {
   // octaves that p may pass 1 by: o' and l stay far inside FP32's 2^127
@@ -64,8 +50,9 @@ struct TBf16 {
   static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
-  IDX_MFMA_V(mfma_v, "v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0",
-             "v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0")
+  static __device__ __forceinline__ w4f mfma16(v8 a, v8 b, w4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
 };
 
 struct TF16 {
@@ -76,8 +63,9 @@ struct TF16 {
   static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
-  IDX_MFMA_V(mfma_v, "v_mfma_f32_32x32x16_f16 %0, %1, %2, 0",
-             "v_mfma_f32_32x32x16_f16 %0, %1, %2, %0")
+  static __device__ __forceinline__ w4f mfma16(v8 a, v8 b, w4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -120,6 +108,19 @@ __device__ __forceinline__ float other_half(float x) {
 __device__ __forceinline__ float max_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// Maximum and sum over the lanes l, l ^ 16, l ^ 32 and l ^ 48.
+__device__ __forceinline__ float max_quarters(float x) {
+  x = max_halves(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_quarters(float x) {
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
 // Key of a 32-key tile whose logit is in register r of wave half h.

@@ -7,10 +7,10 @@
 // sequence (latent_paged).  A key costs 2*(576+512) operations a head and 1152 bytes: with 64
 // heads 121 operations a byte.
 //
-// A workgroup takes one token (or sequence) and up to 128 rows (heads, or steps x heads), 32 a
-// wave; its waves share each 32-key tile in LDS (idx_attn.hpp has the arithmetic), read from
-// memory straight into LDS while earlier tiles are worked on.  With 64 rows or fewer the waves
-// form two key groups that take every other tile and are joined at the end.  Where tokens or
+// A workgroup takes one token (or sequence) and up to 128 rows (heads, or steps x heads), 16 a
+// wave; its waves share each 32-key tile in LDS, read from memory straight into LDS while earlier
+// tiles are worked on.  With 64 rows or fewer the waves form two key groups that take every other
+// tile and are joined at the end.  Where tokens or
 // sequences alone leave compute units idle, the keys are split over workgroups, whose partial
 // results a second kernel joins.
 #include "idx_attn.hpp"
@@ -19,12 +19,13 @@
 namespace idxk {
 
 constexpr int kTileKeys = 32;
-constexpr int kSteps = kLatRow / 16;      // 16-deep steps of the first product
-constexpr int kLatSteps = kLatent / 16;   // ... of which in the latent part
-constexpr int kCols = kLatent / 32;       // 32-column blocks of the values
+constexpr int kRowsWave = 16;             // attention rows of a wave
+constexpr int kSteps = kLatRow / 32;      // 32-deep steps of the first product
+constexpr int kLatSteps = kLatent / 32;   // ... of which in the latent part
+constexpr int kCols = kLatent / 16;       // 16-column blocks of the values
 constexpr int kRopeOff = kTileKeys * kLatent * 2;             // rotary part of a tile, behind the latent parts
 constexpr int kTileBytes = kTileKeys * kLatRow * 2;
-constexpr int kAhead = 6;                 // LDS reads of operands run this many products ahead
+
 constexpr int kBuffers = 4;               // tiles in LDS: 144 of the 160 KiB
 constexpr int kMaxList = IDX_TOPK_KMAX;
 constexpr int kPlanBatch = 1024;          // larger batches take one workgroup a sequence
@@ -43,8 +44,8 @@ struct LatArgs {
   float c;                         // scale * log2(e)
   char* out;
   float* lse;
-  float* part_o;                   // [(part * row_blocks + block) * HG + group] cells of 32 rows x 512 columns
-  float2* part_ml;                 // ... of 32 rows
+  float* part_o;                   // [(part * row_blocks + block) * HG + group] cells of 16 rows x 512 columns
+  float2* part_ml;                 // ... of 16 rows
   int2* plan;                      // paged: [B] first part and number of parts
 };
 
@@ -55,8 +56,8 @@ __device__ const uint4 kZeroRow[kLatRow * 2 / 16] = {};
 // LDS image of a tile: rows of 64 (latent) or 8 (rotary) 16-byte chunks; chunk
 // c of row r stands at c ^ lat_swz(r) or c ^ rope_swz(r), so that the 16-byte
 // reads of 16 rows at one chunk (first product) and the transposing 8-byte
-// reads of 4 rows x 4 chunks (second product) each cover all 64 banks once.
-__device__ __forceinline__ int lat_swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+// reads of 8 rows x 2 chunks (second product) each cover all 64 banks once.
+__device__ __forceinline__ int lat_swz(int r) { return (r & 7) << 1 | (r >> 2 & 1); }
 __device__ __forceinline__ int rope_swz(int r) { return (r >> 1) & 7; }
 
 // Workgroup `wg` of a paged call: its sequence, which of the sequence's parts
@@ -108,19 +109,31 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   return Part{-1, 0, 0, 0};  // a spare workgroup
 }
 
-// HG row groups of 32 (one wave each) x KG key groups: wave (kg, hg) walks
-// the tiles kg, kg + KG, ... of the workgroup's range for its 32 rows.
+// HG row groups of 16 (one wave each) x KG key groups: wave (kg, hg) walks
+// the tiles kg, kg + KG, ... of the workgroup's range for its 16 rows.
+//
+// Both products are v_mfma_f32_16x16x32, transposed as in idx_attn.hpp: logits^T
+// [16 keys x 16 rows] twice a tile, o'^T [16 columns x 16 rows].  In a result lane
+// 16g + c holds row c's entries 4g .. 4g + 3, so that the 8 logits a lane holds
+// of a tile, keys 4g + r and 16 + 4g + r, are the second product's B operand
+// with those keys in that order.  A wave of 16 rows reads every tile from LDS
+// for 16 rows only, twice what 32 rows would; but o' is then 128 registers and
+// q 72, two waves fit a SIMD, and one wave's softmax, LDS latency and stalls on
+// loads run beside the other's products (32 rows a wave, one wave a SIMD:
+// 4600 clocks a tile of 128 rows against 2176 of products alone).
 template <class T, int HG, int KG, bool PAGED>
-__global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_latent(LatArgs A) {
+__global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(LatArgs A) {
+  constexpr int kAhead = HG == 4 ? 3 : 4;        // LDS reads of operands run this many products ahead (as registers allow)
   constexpr int kRing = kBuffers / KG;           // tiles of a key group in LDS
   constexpr int kRows = kTileKeys / HG;          // rows of a tile that one wave loads
-  constexpr int kLoads = kRows + 4 / HG;         // its loads to LDS a tile
+  constexpr int kRope4 = HG < 4 ? 4 / HG : 1;    // its loads of rotary parts; with 8 waves the last four have none
+  constexpr int kLoads = kRows + kRope4;         // its loads to LDS a tile
   __shared__ __attribute__((aligned(1024))) char s_tile[kBuffers * kTileBytes];
   __shared__ int32_t s_again;
   __shared__ int32_t s_list[PAGED ? 4 : kMaxList + kTileKeys];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hg = wave % HG, kg = wave / HG;
-  const int h = lane >> 5, col = lane & 31;
+  const int g = lane >> 4, col = lane & 15;
   // workgroups of one chiplet (every eighth) take neighbouring work
   const int total = gridDim.x, per = total >> 3, extra = total & 7, x8 = blockIdx.x & 7, i8 = blockIdx.x >> 3;
   const int work = x8 * per + min(x8, extra) + i8;
@@ -159,7 +172,7 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     }
   }
   const int b = part.b;
-  const int row = (rb * HG + hg) * 32 + col;
+  const int row = (rb * HG + hg) * kRowsWave + col;
   const bool have = row < A.S * A.H;
   const int step = have ? row / A.H : 0, head = have ? row % A.H : 0;
   int limit = PAGED ? len - A.S + 1 + step : len;  // this lane's row sees keys below
@@ -167,23 +180,31 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
 
   if (!PAGED) __syncthreads();
 
-  v16f o[kCols];
+  w4f o[kCols];
   RowStat st{-INFINITY, 0.f};
-  // this lane's LDS byte offsets in a tile: its key's row (first product; step
-  // s at chunk 2s + h), and its two rows of the transposing reads (second)
-  const int tr = 4 * h + ((lane & 15) >> 2), tc = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-  int kaddr = col * (kLatent * 2) + ((h ^ lat_swz(col)) << 4), raddr = kRopeOff + col * (kRope * 2) + ((h ^ rope_swz(col)) << 4);
-  int vaddr0 = tr * (kLatent * 2) + ((tc ^ lat_swz(tr)) << 4) + (lane & 1) * 8;
-  int vaddr1 = (tr + 8) * (kLatent * 2) + ((tc ^ lat_swz(tr + 8)) << 4) + (lane & 1) * 8;
+  // This lane's LDS byte offsets in a tile: key `col` (first product; step s at
+  // chunk 4s + g; key 16 + col 16 rows on), its rotary part, and the lane's row
+  // of the transposing reads (second product; the other 16 rows on).  They are
+  // made where they are used: registers are short.
+  const auto own_lane = [&]() __attribute__((always_inline)) {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+  const auto key_at = [&](int l) __attribute__((always_inline)) { return (l & 15) * (kLatent * 2) + ((l >> 4 ^ lat_swz(l & 15)) << 4); };
+  const auto rope_at = [&](int l) __attribute__((always_inline)) { return kRopeOff + (l & 15) * (kRope * 2) + ((l >> 4 ^ rope_swz(l & 15)) << 4); };
+  const auto value_at = [&](int l) __attribute__((always_inline)) {
+    const int r = l >> 2;  // 4 (l / 16) + (l & 15) / 4
+    return r * (kLatent * 2) + (((l & 3) >> 1 ^ lat_swz(r)) << 4) + (l & 1) * 8;
+  };
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)s_tile;
 
-  int lane_r = lane;
   const int mine = __builtin_amdgcn_readfirstlane(tile0) + kg;  // this key group's first tile
   // the same for all key groups: barriers
   const int steps = __builtin_amdgcn_readfirstlane(tile1 > tile0 ? (tile1 - tile0 + KG - 1) / KG : 0);
 
-  // Slot of key `col` of step i's tile (-1: none).
-  const auto slot_of = [&](int i) __attribute__((always_inline)) -> int { return s_list[(i * KG + kg) * kTileKeys + (lane_r & 31)]; };
+  // Slot of key lane & 31 of step i's tile (-1: none).
+  const auto slot_of = [&](int i) __attribute__((always_inline)) -> int { return s_list[(i * KG + kg) * kTileKeys + (lane & 31)]; };
   // Physical page of step i's tile, -1: none (a tile lies in one page).
   const auto page_of = [&](int i) __attribute__((always_inline)) -> int {
     const int key = (mine + i * KG) * kTileKeys;
@@ -198,12 +219,13 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     uint32_t dst;
     const char* page;  // paged: the tile's first row
     int live;          // paged: its rows that are there
-    int slots;         // listed: the slot of row `col` of the tile
+    int slots;         // listed: the slot of row lane & 31 of the tile
     int l16;           // 16 * lane, swizzled as this wave's first row
   };
   const auto source = [&](int i) __attribute__((always_inline)) {
     Source f;
-    f.dst = lds0 + (kg * kRing + i % kRing) * kTileBytes;
+    f.dst = __builtin_amdgcn_readfirstlane(lds0 + (kg * kRing + i % kRing) * kTileBytes);
+    asm volatile("" : "+s"(f.dst));  // the loads' addresses are made from it, not kept in registers
     f.page = reinterpret_cast<const char*>(kZeroRow);
     f.live = 0;
     f.slots = -1;
@@ -217,9 +239,7 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     } else {
       f.slots = slot_of(i);
     }
-    f.l16 = lane_r;
-    asm volatile("" : "+v"(f.l16));  // made here, not kept in registers
-    f.l16 = (f.l16 ^ (HG == 1 ? 0 : lat_swz(hg * kRows))) << 4;
+    f.l16 = (own_lane() ^ (HG == 1 ? 0 : lat_swz(hg * kRows))) << 4;
     return f;
   };
   const auto load = [&](const Source& f, int i, int j) __attribute__((always_inline)) {
@@ -235,8 +255,8 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
         src = A.cache + (s >= 0 ? at : zero - A.cache);
       }
       dma_row(src, f.l16 ^ (lat_swz(j) << 4), f.dst + r * (kLatent * 2));
-    } else {
-      const int n = hg * (4 / HG) + j - kRows;
+    } else if (HG < 8 || hg < 4) {
+      const int n = hg * kRope4 + j - kRows;
       const int l = f.l16 >> 4 ^ (HG == 1 ? 0 : lat_swz(hg * kRows));
       const int r = 8 * n + (l >> 3);
       const char* src;
@@ -261,94 +281,110 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
   typename T::v8 q[kSteps];  // a row past the last repeats the first: its results are dropped
   {
     const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + step * A.q_token +
-                                head * A.q_head + 8 * h;
+                                head * A.q_head + 8 * g;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 16 * s);
+    for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 32 * s);
   }
 
-  // Waits for step i's tile and computes its logits, masked.
-  const auto logits = [&](int i) __attribute__((always_inline)) {
-    if (i + kRing - 1 <= steps) dma_wait<(kRing - 2) * kLoads>();
-    else dma_wait<0>();
+  // Waits for step i's tile, computes its logits x, masked, and starts the
+  // loads of a later tile on the way.
+  const auto logits = [&](int i, w4f (&x)[2]) __attribute__((always_inline)) {
+    if (i + kRing - 1 > steps) dma_wait<0>();
+    else if (HG < 8 || hg < 4) dma_wait<(kRing - 2) * kLoads>();
+    else dma_wait<(kRing - 2) * kRows>();
     tile_barrier();  // tile i is there and tile i - 1 is read: its buffer takes the next load
     const bool more = i + kRing - 1 < steps;
     const Source next = source(more ? i + kRing - 1 : i);
     const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
-    int ka = kaddr, ra = raddr;
-    asm volatile("" : "+v"(ka), "+v"(ra));  // the offsets below are made here, not kept in registers
-    // each product is followed by the read of the operand six products ahead
+    const int ka = key_at(own_lane()), ra = rope_at(own_lane());
+    // each product is followed by the read of the operand kAhead products on;
+    // product n: keys 16 (n & 1) on, step n / 2
     typename T::v8 k[kAhead];
     const auto read = [&](int n) __attribute__((always_inline)) {
-      k[n % kAhead] = n < kLatSteps ? lds_read<typename T::v8>(tile + (ka ^ (n >> 2 << 5)) + 256 * (n & 3))
-                                    : lds_read<typename T::v8>(tile + (ra ^ ((n - kLatSteps) << 5)));
+      const int s = n >> 1, u = n & 1;
+      k[n % kAhead] = s < kLatSteps ? lds_read<typename T::v8>(tile + (ka ^ ((s & 3) << 6)) + 256 * (s >> 2) + u * 16 * kLatent * 2)
+                                    : lds_read<typename T::v8>(tile + (ra ^ ((s - kLatSteps) << 6)) + u * 16 * kRope * 2);
     };
-    v16f x;
+    x[0] = w4f{};
+    x[1] = w4f{};
 #pragma unroll
     for (int n = 0; n < kAhead; ++n) read(n);
 #pragma unroll
-    for (int n = 0; n < kSteps; ++n) {
+    for (int n = 0; n < 2 * kSteps; ++n) {
       __builtin_amdgcn_sched_barrier(0);
-      T::mfma_v(x, k[n % kAhead], q[n < kLatSteps ? 8 * (n & 3) + (n >> 2) : n], n == 0);
-      if (n + kAhead < kSteps) read(n + kAhead);
+      x[n & 1] = T::mfma16(k[n % kAhead], q[n >> 1], x[n & 1]);
+      if (n + kAhead < 2 * kSteps) read(n + kAhead);
       // a load every few products: a burst would wait for the memory pipeline
-      if (n % (kSteps / kLoads) == 0) {
+      constexpr int kEvery = 2 * kSteps / kLoads;
+      if (n % kEvery == 0 && n / kEvery < kLoads) {
         __builtin_amdgcn_sched_barrier(0);
-        if (more) load(next, i + kRing - 1, n / (kSteps / kLoads));
+        if (more) load(next, i + kRing - 1, n / kEvery);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    mfma_v_done(x);
     const int key0 = (mine + i * KG) * kTileKeys;
     uint32_t live;
     if (PAGED) live = __builtin_amdgcn_readfirstlane(page_of(i)) < 0 ? 0u : ~0u;
     else live = (uint32_t)__ballot(slot_of(i) >= 0);
     if (live != ~0u || key0 + kTileKeys > limit_min) {
-      int h4 = lane_r >> 5 << 2;
-      asm volatile("" : "+v"(h4));
-      const uint32_t live_h = live >> h4;
-      const int limit_h = limit - key0 - h4;
+      const int g4 = own_lane() >> 4 << 2;
+      const uint32_t live_g = live >> g4;
+      const int limit_g = limit - key0 - g4;
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (!(live_h >> key_of(r, 0) & 1) || key_of(r, 0) >= limit_h) x[r] = -INFINITY;
+      for (int r = 0; r < 8; ++r) {
+        const int key = (r & 3) + 16 * (r >> 2);
+        if (!(live_g >> key & 1) || key >= limit_g) x[r >> 2][r & 3] = -INFINITY;
+      }
     }
-    return x;
+  };
+  // The largest logit of each row in a tile, in octaves.
+  const auto largest = [&](const w4f (&x)[2]) __attribute__((always_inline)) {
+    float mx = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])), fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
+    return max_quarters(mx) * A.c;
   };
 
-  // o' fills the accumulator registers and q most of the others, so rescaling
-  // o' where a row's maximum grows would take all of it through registers
-  // that are not there.  The reference stays at the row's first live tile's
-  // maximum instead: p may grow to kHeadroom octaves above 1, which costs no
-  // precision.  A workgroup that sees more walks its keys again, first for the
-  // rows' true maxima, then with those as references.
+  // Rescaling o' where a row's maximum grows would take all of its registers
+  // through others that are not there.  The reference stays at the row's first
+  // live tile's maximum instead: p may grow to kHeadroom octaves above 1, which
+  // costs no precision.  A workgroup that sees more walks its keys again, first
+  // for the rows' true maxima, then with those as references.
   __builtin_amdgcn_s_waitcnt(0x0F70);  // q is there: the waits below count tile loads only
   for (int attempt = 0;; ++attempt) {
 #pragma unroll
-    for (int d = 0; d < kCols; ++d) o[d] = v16f{};
-    float over = -INFINITY;  // the most octaves by which a logit passed its row's reference
+    for (int d = 0; d < kCols; ++d) o[d] = w4f{};
+    bool over = false;  // a logit passed its row's reference by too much
     for (int i = 0; i < steps; ++i) {
-      v16f x = logits(i);
-      const float mx = tile_max(x, A.c);
+      w4f x[2];
+      logits(i, x);
+      const float mx = largest(x);
       st.m = st.m == -INFINITY ? mx : st.m;
-      over = fmaxf(over, mx - st.m);
-      softmax_tile(x, st, A.c);
-      const typename T::v8 p0 = p_operand<T>(x, 0), p1 = p_operand<T>(x, 1);
+      over |= __any(mx - st.m > T::kHeadroom);
+      const float m = st.m == -INFINITY ? 0.f : st.m;  // a row without a live key yet: p = 0
+      typename T::v8 p;
+      float l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float e = __builtin_amdgcn_exp2f(fmaf(x[r >> 2][r & 3], A.c, -m));
+        l[r & 1] += e;
+        p[r] = (typename T::elem)e;
+      }
+      st.l += l[0] + l[1];  // this quarter's keys; the quarters are added at the end
       const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
-      int va0 = vaddr0, va1 = vaddr1;
-      asm volatile("" : "+v"(va0), "+v"(va1));
-      // product n: column block d = 4 (n & 3) + n / 8 for the keys of step (n / 4) & 1
+      const int va = value_at(own_lane());
       typename T::v8 v[kAhead];
+      // product n: column block d = n / 4 + 8 (n & 3)
       const auto read = [&](int n) __attribute__((always_inline)) {
-        const int at = (n >> 2 & 1) * 16 * kLatent * 2 + 256 * (n & 3);
-        v[n % kAhead] = cat<T>(lds_read_tr<T>(tile + (va0 ^ (n >> 3 << 6)) + at), lds_read_tr<T>(tile + (va1 ^ (n >> 3 << 6)) + at));
+        const char* a = tile + (va ^ (n >> 2 << 5)) + 256 * (n & 3);
+        v[n % kAhead] = cat<T>(lds_read_tr<T>(a), lds_read_tr<T>(a + 16 * kLatent * 2));
       };
 #pragma unroll
       for (int n = 0; n < kAhead; ++n) read(n);
 #pragma unroll
-      for (int n = 0; n < 2 * kCols; ++n) {
+      for (int n = 0; n < kCols; ++n) {
         __builtin_amdgcn_sched_barrier(0);
-        const int d = 4 * (n & 3) + (n >> 3);
-        o[d] = T::mfma(v[n % kAhead], n >> 2 & 1 ? p1 : p0, o[d]);
-        if (n + kAhead < 2 * kCols) read(n + kAhead);
+        const int d = (n >> 2) + 8 * (n & 3);
+        o[d] = T::mfma16(v[n % kAhead], p, o[d]);
+        if (n + kAhead < kCols) read(n + kAhead);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -356,33 +392,29 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     if (attempt > 0) break;
     if (tid == 0) s_again = 0;
     __syncthreads();
-    if (__any(over > T::kHeadroom) && lane == 0) s_again = 1;
+    if (over && lane == 0) s_again = 1;
     __syncthreads();
     if (!__builtin_amdgcn_readfirstlane(s_again)) break;
     st = RowStat{-INFINITY, 0.f};
     load_first();
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
-      const v16f x = logits(i);
-      st.m = fmaxf(st.m, tile_max(x, A.c));
+      w4f x[2];
+      logits(i, x);
+      st.m = fmaxf(st.m, largest(x));
     }
     tile_barrier();
     load_first();
   }
-  float l = st.l + other_half(st.l), m = st.m;
+  float l = sum_quarters(st.l), m = st.m;
 
   // key groups are joined through LDS (nothing is in flight there any more):
   // group 1 hands over m, l and o', 16 bytes a lane at a time
   if (KG == 2) {
-    char* const buf = s_tile + hg * (kCols * 16 * 256 + 512);
+    char* const buf = s_tile + hg * (kCols * 1024 + 512);
     if (kg == 1) {
 #pragma unroll
-      for (int d = 0; d < kCols; ++d)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float4 v = make_float4(o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]);
-          *reinterpret_cast<float4*>(buf + 512 + ((d * 4 + g) * 64 + lane) * 16) = v;
-        }
+      for (int d = 0; d < kCols; ++d) *reinterpret_cast<w4f*>(buf + 512 + d * 1024 + lane * 16) = o[d];
       *reinterpret_cast<float2*>(buf + lane * 8) = make_float2(m, l);
     }
     __syncthreads();
@@ -393,75 +425,94 @@ __global__ __launch_bounds__(64 * HG * KG) __attribute__((amdgpu_waves_per_eu(1,
     l = l * f0 + ml.y * f1;
     m = top;
 #pragma unroll
-    for (int d = 0; d < kCols; ++d)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float4 v = *reinterpret_cast<const float4*>(buf + 512 + ((d * 4 + g) * 64 + lane) * 16);
-        o[d][4 * g] = o[d][4 * g] * f0 + v.x * f1;
-        o[d][4 * g + 1] = o[d][4 * g + 1] * f0 + v.y * f1;
-        o[d][4 * g + 2] = o[d][4 * g + 2] * f0 + v.z * f1;
-        o[d][4 * g + 3] = o[d][4 * g + 3] * f0 + v.w * f1;
-      }
+    for (int d = 0; d < kCols; ++d) o[d] = o[d] * f0 + *reinterpret_cast<const w4f*>(buf + 512 + d * 1024 + lane * 16) * f1;
   }
   if (part.parts > 1) {
     // in the order of the registers: whole lines, and the join adds them in that order too
     const int64_t cell = (int64_t)(wg * A.row_blocks + rb) * HG + hg;
-    float* po = A.part_o + cell * (32 * kLatent) + lane * 4;
+    float* po = A.part_o + cell * (kRowsWave * kLatent) + lane * 4;
 #pragma unroll
-    for (int d = 0; d < kCols; ++d)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<float4*>(po + (d * 4 + g) * 256) =
-            make_float4(o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]);
-    if (h == 0) A.part_ml[cell * 32 + col] = make_float2(m, l);
+    for (int d = 0; d < kCols; ++d) *reinterpret_cast<w4f*>(po + d * 256) = o[d];
+    if (g == 0) A.part_ml[cell * kRowsWave + col] = make_float2(m, l);
     return;
   }
   if (!have) return;
   const int64_t at = ((int64_t)b * A.S + step) * A.H + head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  typename T::elem* out = reinterpret_cast<typename T::elem*>(A.out) + at * kLatent;
+  typename T::elem* out = reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + 4 * g;
 #pragma unroll
-  for (int d = 0; d < kCols; ++d)
+  for (int d = 0; d < kCols; ++d) {
+    typename T::v4 v;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      typename T::v4 v;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = (typename T::elem)(o[d][4 * g + j] * inv);
-      *reinterpret_cast<typename T::v4*>(out + 32 * d + 8 * g + 4 * h) = v;
-    }
-  if (A.lse && h == 0) A.lse[at] = row_lse(m, l);
+    for (int j = 0; j < 4; ++j) v[j] = (typename T::elem)(o[d][j] * inv);
+    *reinterpret_cast<typename T::v4*>(out + 16 * d) = v;
+  }
+  if (A.lse && g == 0) A.lse[at] = row_lse(m, l);
 }
 
 // Joins the parts of a row: o = sum_p 2^(m_p - m) o'_p / sum_p 2^(m_p - m) l_p.
-// A wave takes 256 of the 16384 numbers of a cell (32 rows x 512 columns in
-// the order of the walk's registers), a workgroup four such pieces.
+// A workgroup takes 256 of the 8192 numbers of a cell (16 rows x 512 columns in
+// the order of the walk's registers), each wave every fourth part, so that few
+// loads wait on one another.
 template <class T>
 __global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int hgs, bool paged) {
-  const int lane = threadIdx.x & 63, piece = (blockIdx.x & 15) * 4 + (threadIdx.x >> 6);
-  const int groups = A.row_blocks * hgs;  // 32-row groups of a token or sequence
-  const int unit = blockIdx.x >> 4, b = unit / groups, group = unit % groups;
-  const int row = group * 32 + (lane & 31);
+  __shared__ float4 s_o[3][64];
+  __shared__ float2 s_ml[3][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, piece = blockIdx.x & (kCols - 1);
+  const int groups = A.row_blocks * hgs;  // 16-row groups of a token or sequence
+  const int unit = blockIdx.x / kCols, b = unit / groups, group = unit % groups;
+  const int row = group * kRowsWave + (lane & 15);
   int first = b * A.parts, n = A.parts;
   if (paged) {
     const int2 p = A.plan[b];
     first = p.x; n = p.y;
     if (n == 1) return;  // written by the walk
   }
-  if (row >= A.S * A.H) return;
+  if (group * kRowsWave >= A.S * A.H) return;
   const int64_t cell0 = (int64_t)first * groups + group;
-  const float2* ml = A.part_ml + cell0 * 32 + (lane & 31);
-  const float4* po = reinterpret_cast<const float4*>(A.part_o + cell0 * (32 * kLatent) + piece * 256) + lane;
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int p = 0; p < n; ++p) m = fmaxf(m, ml[(int64_t)p * groups * 32].x);
-  const float m0 = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
+  const float2* ml = A.part_ml + cell0 * kRowsWave + (lane & 15);
+  const float4* po = reinterpret_cast<const float4*>(A.part_o + cell0 * (kRowsWave * kLatent) + piece * 256) + lane;
+  float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int p = 0; p < n; ++p) {
-    const float2 s = ml[(int64_t)p * groups * 32];
-    const float4 v = po[(int64_t)p * groups * (32 * kLatent / 4)];
-    const float f = __builtin_amdgcn_exp2f(s.x - m0);
+  constexpr int kBatch = 8;
+  for (int p0 = wave; p0 < n; p0 += 4 * kBatch) {
+    float2 s[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int p = p0 + 4 * u < n ? p0 + 4 * u : p0;
+      s[u] = ml[(int64_t)p * groups * kRowsWave];
+      v[u] = po[(int64_t)p * groups * (kRowsWave * kLatent / 4)];
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, s[u].x);
+    const float t0 = top == -INFINITY ? 0.f : top, old = __builtin_amdgcn_exp2f(m - t0);
+    m = top;
+    l *= old; o.x *= old; o.y *= old; o.z *= old; o.w *= old;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float f = p0 + 4 * u < n ? __builtin_amdgcn_exp2f(s[u].x - t0) : 0.f;
+      l = fmaf(s[u].y, f, l);
+      o.x = fmaf(v[u].x, f, o.x); o.y = fmaf(v[u].y, f, o.y); o.z = fmaf(v[u].z, f, o.z); o.w = fmaf(v[u].w, f, o.w);
+    }
+  }
+  if (wave > 0) {
+    s_o[wave - 1][lane] = o;
+    s_ml[wave - 1][lane] = make_float2(m, l);
+  }
+  __syncthreads();
+  if (wave > 0 || row >= A.S * A.H) return;
+  float top = m;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) top = fmaxf(top, s_ml[w][lane].x);
+  const float t0 = top == -INFINITY ? 0.f : top, f0 = __builtin_amdgcn_exp2f(m - t0);
+  l *= f0; o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) {
+    const float2 s = s_ml[w][lane];
+    const float4 v = s_o[w][lane];
+    const float f = __builtin_amdgcn_exp2f(s.x - t0);
     l = fmaf(s.y, f, l);
     o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
   }
@@ -470,9 +521,9 @@ __global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int hgs, bool pa
   v[0] = (typename T::elem)(o.x * inv); v[1] = (typename T::elem)(o.y * inv);
   v[2] = (typename T::elem)(o.z * inv); v[3] = (typename T::elem)(o.w * inv);
   const int64_t at = (int64_t)b * A.S * A.H + row;  // rows of a sequence are its steps' heads in order
-  const int column = 32 * (piece >> 2) + 8 * (piece & 3) + 4 * (lane >> 5);
+  const int column = 16 * piece + 4 * (lane >> 4);
   *reinterpret_cast<typename T::v4*>(reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + column) = v;
-  if (A.lse && column == 0) A.lse[at] = row_lse(m, l);
+  if (A.lse && column == 0) A.lse[at] = row_lse(top, l);
 }
 
 // ------------------------------------------------------------------ host
@@ -480,15 +531,19 @@ __global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int hgs, bool pa
 static inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 static inline size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// How a call is cut: 32 * hg rows a workgroup, `parts` as in LatArgs.
+// How a call is cut: 16 * hg rows a workgroup, `parts` as in LatArgs.
 struct LatGeom {
   int hg, row_blocks, parts;
-  int64_t cells;  // partial results of 32 * hg rows each (0: none)
+  int64_t cells;  // partial results of 16 * hg rows each (0: none)
   size_t o, ml, plan, total;
 };
 
+// Waves that rows need: all eight of a workgroup beyond 64 rows, else half as
+// many, or fewer, beside as many of a second key group.
+static int row_groups(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
+
 static LatGeom layout(LatGeom g, int64_t B) {
-  const size_t rows = (size_t)(g.cells * 32 * g.hg);
+  const size_t rows = (size_t)(g.cells * kRowsWave * g.hg);
   size_t at = 0;
   g.o = at; at = a256(at + rows * kLatent * 4);
   g.ml = at; at = a256(at + rows * 8);
@@ -499,8 +554,8 @@ static LatGeom layout(LatGeom g, int64_t B) {
 
 static LatGeom listed_geom(int32_t T, int32_t H, int32_t K) {
   LatGeom g{};
-  g.hg = H <= 32 ? 1 : H <= 64 ? 2 : 4;
-  g.row_blocks = (H + 32 * g.hg - 1) / (32 * g.hg);
+  g.hg = row_groups(H);
+  g.row_blocks = (H + kRowsWave * g.hg - 1) / (kRowsWave * g.hg);
   // lists are split where the tokens alone leave compute units idle; a part
   // keeps at least two tiles
   const int64_t groups = (int64_t)T * g.row_blocks;
@@ -515,8 +570,8 @@ static LatGeom listed_geom(int32_t T, int32_t H, int32_t K) {
 static LatGeom paged_geom(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
   LatGeom g{};
   const int rows = S * H;
-  g.hg = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
-  g.row_blocks = (rows + 32 * g.hg - 1) / (32 * g.hg);
+  g.hg = row_groups(rows);
+  g.row_blocks = (rows + kRowsWave * g.hg - 1) / (kRowsWave * g.hg);
   int64_t parts = B;
   if (B <= kPlanBatch && max_pages > kMinPages) {
     parts = kUnits / g.row_blocks;
@@ -537,12 +592,13 @@ static int launch(LatArgs A, const LatGeom& g, char* ws, hipStream_t stream) {
   A.part_ml = reinterpret_cast<float2*>(ws + g.ml);
   A.plan = reinterpret_cast<int2*>(ws + g.plan);
   const int64_t grid = (int64_t)(PAGED ? 1 : A.B) * g.parts * g.row_blocks;
-  const int64_t join = (int64_t)A.B * g.row_blocks * g.hg * 16;
+  const int64_t join = (int64_t)A.B * g.row_blocks * g.hg * kCols;
   if (grid > 0x7fffffffLL || join > 0x7fffffffLL) return IDX_EUNSUPPORTED;
   const dim3 n((uint32_t)grid);
   if (g.hg == 1) k_latent<T, 1, 2, PAGED><<<n, dim3(128), 0, stream>>>(A);
   else if (g.hg == 2) k_latent<T, 2, 2, PAGED><<<n, dim3(256), 0, stream>>>(A);
-  else k_latent<T, 4, 1, PAGED><<<n, dim3(256), 0, stream>>>(A);
+  else if (g.hg == 4) k_latent<T, 4, 2, PAGED><<<n, dim3(512), 0, stream>>>(A);
+  else k_latent<T, 8, 1, PAGED><<<n, dim3(512), 0, stream>>>(A);
   if (g.cells) k_latent_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, g.hg, PAGED);
   return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
