@@ -123,10 +123,11 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
 // 4600 clocks a tile of 128 rows against 2176 of products alone).
 template <class T, int HG, int KG, bool PAGED>
 __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(LatArgs A) {
-  constexpr int kAhead = HG == 4 ? 3 : 4;        // LDS reads of operands run this many products ahead (as registers allow)
+  constexpr int kAhead = 5;      // LDS reads of operands run this many products ahead (as registers allow)
   constexpr int kRing = kBuffers / KG;           // tiles of a key group in LDS
   constexpr int kRows = kTileKeys / HG;          // rows of a tile that one wave loads
-  constexpr int kRope4 = HG < 4 ? 4 / HG : 1;    // its loads of rotary parts; with 8 waves the last four have none
+  constexpr int kFlight = kRing - 1;             // of which on their way
+  constexpr int kRope4 = HG < 4 ? 4 / HG : 1;    // its loads of rotary parts (with 8 waves two load each part)
   constexpr int kLoads = kRows + kRope4;         // its loads to LDS a tile
   __shared__ __attribute__((aligned(1024))) char s_tile[kBuffers * kTileBytes];
   __shared__ int32_t s_again;
@@ -203,81 +204,89 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   // the same for all key groups: barriers
   const int steps = __builtin_amdgcn_readfirstlane(tile1 > tile0 ? (tile1 - tile0 + KG - 1) / KG : 0);
 
-  // Slot of key lane & 31 of step i's tile (-1: none).
-  const auto slot_of = [&](int i) __attribute__((always_inline)) -> int { return s_list[(i * KG + kg) * kTileKeys + (lane & 31)]; };
-  // Physical page of step i's tile, -1: none (a tile lies in one page).
-  const auto page_of = [&](int i) __attribute__((always_inline)) -> int {
-    const int key = (mine + i * KG) * kTileKeys;
-    if (key >= len) return -1;
-    // a scalar load: vector loads would queue behind the tile loads
-    const int pg = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)A.list)[(int64_t)b * A.K + key / IDX_TOPK_PAGE];
-    return pg >= 0 && (int64_t)pg * IDX_TOPK_PAGE < A.num_slots ? pg : -1;
-  };
-  // This wave's share of step i's tile, in kLoads loads: what they need, and
-  // load j of them.
+  // This wave's share of a tile, in kLoads loads: lane j < kRows has the address
+  // of load j's row, each lane its own of the rotary parts'.  Keys that are not
+  // there (bit clear in `live`) come from the zero row; so does a whole tile
+  // past the walk's end, so that every step has the same loads in flight.
+  // Nothing here or in load() branches: a branch between products costs more
+  // than the loads.
   struct Source {
-    uint32_t dst;
-    const char* page;  // paged: the tile's first row
-    int live;          // paged: its rows that are there
-    int slots;         // listed: the slot of row lane & 31 of the tile
-    int l16;           // 16 * lane, swizzled as this wave's first row
+    uint32_t dst, live;
+    uint32_t lo, hi, rlo[kRope4], rhi[kRope4];
   };
-  const auto source = [&](int i) __attribute__((always_inline)) {
+  const auto source = [&](int t) __attribute__((always_inline)) {
     Source f;
-    f.dst = __builtin_amdgcn_readfirstlane(lds0 + (kg * kRing + i % kRing) * kTileBytes);
+    f.dst = __builtin_amdgcn_readfirstlane(lds0 + (kg * kRing + t % kRing) * kTileBytes);
     asm volatile("" : "+s"(f.dst));  // the loads' addresses are made from it, not kept in registers
-    f.page = reinterpret_cast<const char*>(kZeroRow);
-    f.live = 0;
-    f.slots = -1;
+    const bool in = t < steps;
+    const uint64_t zero = (uint64_t)(uintptr_t)kZeroRow, cache = (uint64_t)(uintptr_t)A.cache;
+    const int l = own_lane();
+    const int row_l = (hg * kRows + l) & (kTileKeys - 1);
+    uint64_t page = 0;
+    int rows = 0;  // paged: rows of the tile that are there
     if (PAGED) {
-      const int key0 = (mine + i * KG) * kTileKeys;
-      const int pg = __builtin_amdgcn_readfirstlane(page_of(i));
-      if (pg >= 0) {
-        f.live = min(kTileKeys, len - key0);
-        f.page = A.cache + ((int64_t)pg * IDX_TOPK_PAGE + key0 % IDX_TOPK_PAGE) * (kLatRow * 2);
-      }
-    } else {
-      f.slots = slot_of(i);
+      const int key0 = (mine + t * KG) * kTileKeys;
+      // a scalar load: vector loads would queue behind the tile loads.  A tile
+      // lies in one page; page 0 of the table stands in for tiles past the end
+      const auto* table = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)A.list) + (int64_t)b * A.K;
+      const bool some = in && key0 < len;
+      const int pg = table[some ? key0 / IDX_TOPK_PAGE : 0];
+      rows = some && pg >= 0 && (int64_t)pg * IDX_TOPK_PAGE < A.num_slots ? min(kTileKeys, len - key0) : 0;
+      page = cache + ((int64_t)pg * IDX_TOPK_PAGE + key0 % IDX_TOPK_PAGE) * (kLatRow * 2);
+      f.live = rows > 0 ? ~0u : 0u;
     }
-    f.l16 = (own_lane() ^ (HG == 1 ? 0 : lat_swz(hg * kRows))) << 4;
+    const int tile_slot = (min(t, steps - 1) * KG + kg) * kTileKeys;
+    const auto row_at = [&](int r, bool& there) __attribute__((always_inline)) {
+      if (PAGED) {
+        there = r < rows;
+        return page + (uint32_t)r * (uint32_t)(kLatRow * 2);
+      }
+      const int s = s_list[tile_slot + r];
+      there = in && s >= 0;
+      return cache + (uint64_t)(uint32_t)s * (uint32_t)(kLatRow * 2);
+    };
+    bool there;
+    uint64_t p = row_at(row_l, there);
+    if (!PAGED) {
+      const uint32_t w = (uint32_t)__ballot(there);
+      f.live = __builtin_amdgcn_readfirstlane(hg * kRows == 0 ? w : w << (hg * kRows) | w >> (kTileKeys - hg * kRows));
+    }
+    p = there ? p : zero;
+    f.lo = (uint32_t)p;
+    f.hi = (uint32_t)(p >> 32);
+#pragma unroll
+    for (int j = 0; j < kRope4; ++j) {
+      const int r = 8 * ((hg * kRope4 + j) & 3) + (l >> 3);
+      uint64_t o = row_at(r, there);
+      o = (there ? o : zero) + kLatent * 2 + (uint32_t)(((l & 7) ^ rope_swz(r)) << 4);
+      f.rlo[j] = (uint32_t)o;
+      f.rhi[j] = (uint32_t)(o >> 32);
+    }
     return f;
   };
-  const auto load = [&](const Source& f, int i, int j) __attribute__((always_inline)) {
-    const char* const zero = reinterpret_cast<const char*>(kZeroRow);
+  const auto load = [&](const Source& f, int j) __attribute__((always_inline)) {
     if (j < kRows) {
-      const int r = hg * kRows + j;
-      const char* src;
-      if (PAGED) {
-        src = r < f.live ? f.page + r * (kLatRow * 2) : zero;
-      } else {
-        const int s = __builtin_amdgcn_readlane(f.slots, r);
-        const int64_t at = (int64_t)s * (kLatRow * 2);
-        src = A.cache + (s >= 0 ? at : zero - A.cache);
-      }
-      dma_row(src, f.l16 ^ (lat_swz(j) << 4), f.dst + r * (kLatent * 2));
-    } else if (HG < 8 || hg < 4) {
-      const int n = hg * kRope4 + j - kRows;
-      const int l = f.l16 >> 4 ^ (HG == 1 ? 0 : lat_swz(hg * kRows));
-      const int r = 8 * n + (l >> 3);
-      const char* src;
-      if (PAGED) {
-        src = r < f.live ? f.page + r * (kLatRow * 2) : zero;
-      } else {
-        const int s = s_list[(i * KG + kg) * kTileKeys + r];
-        src = s >= 0 ? A.cache + (int64_t)s * (kLatRow * 2) : zero;
-      }
-      dma_lanes(src + kLatent * 2 + (((l & 7) ^ rope_swz(r)) << 4), f.dst + kRopeOff + n * 1024);
+      const uint64_t p = (uint32_t)__builtin_amdgcn_readlane(f.lo, j) | (uint64_t)(uint32_t)__builtin_amdgcn_readlane(f.hi, j) << 32;
+      const int l16 = (own_lane() ^ (HG == 1 ? 0 : lat_swz(hg * kRows))) << 4;
+      dma_row(reinterpret_cast<const char*>((uintptr_t)p), l16 ^ (lat_swz(j) << 4), f.dst + (hg * kRows + j) * (kLatent * 2));
+    } else {
+      const int n = (hg * kRope4 + j - kRows) & 3;
+      dma_lanes(reinterpret_cast<const char*>((uintptr_t)(f.rlo[j - kRows] | (uint64_t)f.rhi[j - kRows] << 32)), f.dst + kRopeOff + n * 1024);
     }
   };
+  Source next;
+  uint32_t live[kFlight + 1];  // of this step's tile and the ones in flight
   const auto load_first = [&]() __attribute__((always_inline)) {
-#pragma unroll 1
-    for (int i = 0; i < min(kRing - 1, steps); ++i) {
-      const Source f = source(i);
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) load(f, i, j);
+    for (int t = 0; t < kFlight; ++t) {
+      next = source(t);
+      live[t + 1] = next.live;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) load(next, j);
     }
+    next = source(kFlight);
   };
-  load_first();
+  if (steps > 0) load_first();
   typename T::v8 q[kSteps];  // a row past the last repeats the first: its results are dropped
   {
     const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + step * A.q_token +
@@ -289,21 +298,18 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   // Waits for step i's tile, computes its logits x, masked, and starts the
   // loads of a later tile on the way.
   const auto logits = [&](int i, w4f (&x)[2]) __attribute__((always_inline)) {
-    if (i + kRing - 1 > steps) dma_wait<0>();
-    else if (HG < 8 || hg < 4) dma_wait<(kRing - 2) * kLoads>();
-    else dma_wait<(kRing - 2) * kRows>();
+    dma_wait<(kFlight - 1) * kLoads>();
     tile_barrier();  // tile i is there and tile i - 1 is read: its buffer takes the next load
-    const bool more = i + kRing - 1 < steps;
-    const Source next = source(more ? i + kRing - 1 : i);
     const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
     const int ka = key_at(own_lane()), ra = rope_at(own_lane());
     // each product is followed by the read of the operand kAhead products on;
-    // product n: keys 16 (n & 1) on, step n / 2
+    // product n: keys 16 (n & 1) on, step step_of(n)
     typename T::v8 k[kAhead];
+    const auto step_of = [](int n) { return n / 2 < kLatSteps ? 4 * (n / 2 & 3) + (n / 2 >> 2) : n / 2; };
     const auto read = [&](int n) __attribute__((always_inline)) {
-      const int s = n >> 1, u = n & 1;
-      k[n % kAhead] = s < kLatSteps ? lds_read<typename T::v8>(tile + (ka ^ ((s & 3) << 6)) + 256 * (s >> 2) + u * 16 * kLatent * 2)
-                                    : lds_read<typename T::v8>(tile + (ra ^ ((s - kLatSteps) << 6)) + u * 16 * kRope * 2);
+      const int j = n >> 1, u = n & 1;  // latent step 4 (j & 3) + j / 4: four reads from one address
+      k[n % kAhead] = j < kLatSteps ? lds_read<typename T::v8>(tile + (ka ^ (j >> 2 << 6)) + 256 * (j & 3) + u * 16 * kLatent * 2)
+                                    : lds_read<typename T::v8>(tile + (ra ^ ((j - kLatSteps) << 6)) + u * 16 * kRope * 2);
     };
     x[0] = w4f{};
     x[1] = w4f{};
@@ -312,23 +318,24 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
 #pragma unroll
     for (int n = 0; n < 2 * kSteps; ++n) {
       __builtin_amdgcn_sched_barrier(0);
-      x[n & 1] = T::mfma16(k[n % kAhead], q[n >> 1], x[n & 1]);
+      x[n & 1] = T::mfma16(k[n % kAhead], q[step_of(n)], x[n & 1]);
       if (n + kAhead < 2 * kSteps) read(n + kAhead);
       // a load every few products: a burst would wait for the memory pipeline
       constexpr int kEvery = 2 * kSteps / kLoads;
       if (n % kEvery == 0 && n / kEvery < kLoads) {
         __builtin_amdgcn_sched_barrier(0);
-        if (more) load(next, i + kRing - 1, n / kEvery);
+        load(next, n / kEvery);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int t = 0; t < kFlight; ++t) live[t] = live[t + 1];
+    live[kFlight] = next.live;
+    next = source(i + 1 + kFlight);
     const int key0 = (mine + i * KG) * kTileKeys;
-    uint32_t live;
-    if (PAGED) live = __builtin_amdgcn_readfirstlane(page_of(i)) < 0 ? 0u : ~0u;
-    else live = (uint32_t)__ballot(slot_of(i) >= 0);
-    if (live != ~0u || key0 + kTileKeys > limit_min) {
+    if (live[0] != ~0u || key0 + kTileKeys > limit_min) {
       const int g4 = own_lane() >> 4 << 2;
-      const uint32_t live_g = live >> g4;
+      const uint32_t live_g = live[0] >> g4;
       const int limit_g = limit - key0 - g4;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
@@ -388,8 +395,9 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    tile_barrier();  // every tile is read
-    if (attempt > 0) break;
+    dma_wait<0>();
+    tile_barrier();  // every tile is read, every load done
+    if (attempt > 0 || steps == 0) break;
     if (tid == 0) s_again = 0;
     __syncthreads();
     if (over && lane == 0) s_again = 1;
@@ -403,6 +411,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
       logits(i, x);
       st.m = fmaxf(st.m, largest(x));
     }
+    dma_wait<0>();
     tile_barrier();
     load_first();
   }
