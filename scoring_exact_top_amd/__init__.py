@@ -437,50 +437,75 @@ def latent_expanded_workspace_bytes(Tq: int, B: int, max_q: int, max_k: int, H: 
 
 
 def _dtype16(t: torch.Tensor) -> int:
-    if t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError("expected bfloat16 or float16, got %s" % t.dtype)
-    return _DTYPES[t.dtype]
-
-
-def _rows16(t: torch.Tensor, dtype, *shape):
-    """Pointer of a strided 16-bit input whose last dimension is contiguous;
-    `shape` gives its trailing sizes (None: any)."""
     if not t.is_cuda:
         raise ValueError("expected a device tensor")
+    return code
+
+
+# The checks below cost a few hundred nanoseconds a call in all: a decode step's
+# launches wait for them.
+
+def _at(t: torch.Tensor, dtype, dev) -> int:
+    """Address of a contiguous tensor of this type on this device."""
     if t.dtype != dtype:
         raise ValueError("expected dtype %s, got %s" % (dtype, t.dtype))
-    if t.dim() != len(shape) or any(n is not None and t.shape[i] != n for i, n in enumerate(shape)):
+    if t.device != dev:
+        raise ValueError("expected all tensors on %s, got one on %s" % (dev, t.device))
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows_at(t: torch.Tensor, dtype, dev, shape) -> int:
+    """Address of a strided input of this shape whose last dimension is contiguous."""
+    if t.dtype != dtype:
+        raise ValueError("expected dtype %s, got %s" % (dtype, t.dtype))
+    if t.device != dev:
+        raise ValueError("expected all tensors on %s, got one on %s" % (dev, t.device))
+    if t.shape != shape:
         raise ValueError("expected shape %s, got %s" % (list(shape), list(t.shape)))
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError("expected unit stride along the last dimension")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stride(t: torch.Tensor, dim: int) -> int:
-    """Stride in numbers; a dimension of one has none that matters."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
+def _strides(t: torch.Tensor):
+    """Strides in numbers but the last; a dimension of one has none that matters."""
+    return [n if size > 1 else 0 for n, size in zip(t.stride(), t.shape)][:-1]
 
 
-def _out(t: Optional[torch.Tensor], shape, dtype, device):
-    """The caller's output, checked, or a new one."""
+def _out(t: Optional[torch.Tensor], shape, dtype, dev):
+    """The caller's output, checked, or a new one; and its address."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    if t.shape != shape:
         raise ValueError("expected an output of shape %s, got %s" % (list(shape), list(t.shape)))
-    _ptr(t, dtype)
-    return t
+    return t, _at(t, dtype, dev)
 
 
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("expected all tensors on %s, got one on %s" % (dev, t.device))
+def _scratch(workspace: Optional[torch.Tensor], need: int, dev):
+    """Address and size of the caller's workspace or a new one (and the tensor, to hold it)."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        return workspace.data_ptr(), max(need, 256), workspace
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("expected a contiguous workspace on %s" % dev)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _cache_rows(cache: torch.Tensor, width: int, dtype):
+def _on(stream, dev) -> int:
+    """Handle of `stream`, or of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _cache_at(cache: torch.Tensor, width: int, dtype, dev):
     if cache.shape[-1] != width:
         raise ValueError("expected a cache of rows of %d, got shape %s" % (width, list(cache.shape)))
-    return _ptr(cache, dtype), cache.numel() // width
+    return _at(cache, dtype, dev), cache.numel() // width
 
 
 def latent_selected(q, cache, slots, scale: float, out=None, lse=None, workspace=None, stream=None):
@@ -491,22 +516,19 @@ def latent_selected(q, cache, slots, scale: float, out=None, lse=None, workspace
     int32 (the output of prefill or decode_paged: -1 entries are skipped).
     Returns (out [T,H,512], lse [T,H] f32).
     """
-    dt = _dtype16(q)
-    q_ptr = _rows16(q, q.dtype, None, None, LATENT_ROW)
-    T, H = int(q.shape[0]), int(q.shape[1])
-    if slots.dim() != 2 or slots.shape[0] != T:
-        raise ValueError("expected slots of shape [%d, K], got %s" % (T, list(slots.shape)))
-    K = int(slots.shape[1])
-    dev = q.device
-    cache_ptr, num_slots = _cache_rows(cache, LATENT_ROW, q.dtype)
-    out = _out(out, (T, H, LATENT), q.dtype, dev)
-    lse = _out(lse, (T, H), torch.float32, dev)
-    _same_device(dev, cache, slots, out, lse, workspace)
-    if workspace is None:
-        workspace = alloc_workspace(latent_selected_workspace_bytes(T, H, K), dev)
-    _check(_lib.idx_topk_latent_selected(q_ptr, _stride(q, 0), _stride(q, 1), cache_ptr, num_slots, _ptr(slots, torch.int32),
-                                         K, T, H, float(scale), dt, _ptr(out), _ptr(lse), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+    dt, dev, dtype = _dtype16(q), q.device, q.dtype
+    if q.dim() != 3 or slots.dim() != 2 or slots.shape[0] != q.shape[0]:
+        raise ValueError("expected q [T,H,576] and slots [T,K], got %s and %s" % (list(q.shape), list(slots.shape)))
+    T, H, _ = q.shape
+    K = slots.shape[1]
+    q_at = _rows_at(q, dtype, dev, (T, H, LATENT_ROW))
+    q_token, q_head = _strides(q)
+    cache_at, num_slots = _cache_at(cache, LATENT_ROW, dtype, dev)
+    out, out_at = _out(out, (T, H, LATENT), dtype, dev)
+    lse, lse_at = _out(lse, (T, H), torch.float32, dev)
+    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_selected_workspace(T, H, K), dev)
+    _check(_lib.idx_topk_latent_selected(q_at, q_token, q_head, cache_at, num_slots, _at(slots, torch.int32, dev), K, T, H,
+                                         scale, dt, out_at, lse_at, ws_at, ws_bytes, _on(stream, dev)))
     return out, lse
 
 
@@ -517,25 +539,22 @@ def latent_paged(q, cache, page_table, seq_lens, scale: float, out=None, lse=Non
     [P,64,576], page_table [B,max_pages] int32, seq_lens [B] int32 (device).
     Returns (out [B,S,H,512], lse [B,S,H] f32).
     """
-    dt = _dtype16(q)
-    q_ptr = _rows16(q, q.dtype, None, None, None, LATENT_ROW)
-    B, S, H = (int(n) for n in q.shape[:3])
-    if cache.dim() != 3 or cache.shape[1] != PAGE:
-        raise ValueError("expected a cache of shape [pages, 64, 576], got %s" % list(cache.shape))
-    if page_table.dim() != 2 or page_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+    dt, dev, dtype = _dtype16(q), q.device, q.dtype
+    if q.dim() != 4 or cache.dim() != 3 or cache.shape[1] != PAGE:
+        raise ValueError("expected q [B,S,H,576] and a cache [pages,64,576], got %s and %s" % (list(q.shape), list(cache.shape)))
+    B, S, H, _ = q.shape
+    if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("expected page_table [%d, max_pages] and seq_lens [%d]" % (B, B))
-    dev = q.device
-    cache_ptr, num_slots = _cache_rows(cache, LATENT_ROW, q.dtype)
-    max_pages = int(page_table.shape[1])
-    out = _out(out, (B, S, H, LATENT), q.dtype, dev)
-    lse = _out(lse, (B, S, H), torch.float32, dev)
-    _same_device(dev, cache, page_table, seq_lens, out, lse, workspace)
-    if workspace is None:
-        workspace = alloc_workspace(latent_paged_workspace_bytes(B, S, H, max_pages), dev)
-    _check(_lib.idx_topk_latent_paged(q_ptr, _stride(q, 0), _stride(q, 1), _stride(q, 2), cache_ptr, num_slots // PAGE,
-                                      _ptr(page_table, torch.int32), max_pages, _ptr(seq_lens, torch.int32), B, S, H,
-                                      float(scale), dt, _ptr(out), _ptr(lse), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(stream)))
+    max_pages = page_table.shape[1]
+    q_at = _rows_at(q, dtype, dev, (B, S, H, LATENT_ROW))
+    q_seq, q_token, q_head = _strides(q)
+    cache_at, num_slots = _cache_at(cache, LATENT_ROW, dtype, dev)
+    out, out_at = _out(out, (B, S, H, LATENT), dtype, dev)
+    lse, lse_at = _out(lse, (B, S, H), torch.float32, dev)
+    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_paged_workspace(B, S, H, max_pages), dev)
+    _check(_lib.idx_topk_latent_paged(q_at, q_seq, q_token, q_head, cache_at, num_slots // PAGE,
+                                      _at(page_table, torch.int32, dev), max_pages, _at(seq_lens, torch.int32, dev), B, S, H,
+                                      scale, dt, out_at, lse_at, ws_at, ws_bytes, _on(stream, dev)))
     return out, lse
 
 
@@ -549,25 +568,23 @@ def latent_expanded(q, kv, k_rope, cu_q, cu_k, max_q: int, max_k: int, scale: fl
     counts, max_q and max_k the longest prompt's query tokens and keys.
     Returns (out [Tq,H,128], lse [Tq,H] f32).
     """
-    dt = _dtype16(q)
-    Tq, H, Tk = int(q.shape[0]), int(q.shape[1]), int(kv.shape[0])
-    q_ptr = _rows16(q, q.dtype, None, None, NOPE + ROPE)
-    kv_ptr = _rows16(kv, q.dtype, None, H, NOPE + VALUE)
-    rope_ptr = _rows16(k_rope, q.dtype, Tk, ROPE)
+    dt, dev, dtype = _dtype16(q), q.device, q.dtype
+    if q.dim() != 3 or kv.dim() != 3:
+        raise ValueError("expected q [Tq,H,192] and kv [Tk,H,256], got %s and %s" % (list(q.shape), list(kv.shape)))
+    Tq, H, _ = q.shape
+    Tk = kv.shape[0]
+    q_at = _rows_at(q, dtype, dev, (Tq, H, NOPE + ROPE))
+    kv_at = _rows_at(kv, dtype, dev, (Tk, H, NOPE + VALUE))
+    rope_at = _rows_at(k_rope, dtype, dev, (Tk, ROPE))
     if cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.shape[0] < 1:
         raise ValueError("expected cu_q and cu_k of shape [B+1]")
-    B = int(cu_q.shape[0]) - 1
-    dev = q.device
-    out = _out(out, (Tq, H, VALUE), q.dtype, dev)
-    lse = _out(lse, (Tq, H), torch.float32, dev)
-    _same_device(dev, kv, k_rope, cu_q, cu_k, out, lse, workspace)
-    if workspace is None:
-        workspace = alloc_workspace(latent_expanded_workspace_bytes(Tq, B, max_q, max_k, H), dev)
-    _check(_lib.idx_topk_latent_expanded(q_ptr, _stride(q, 0), _stride(q, 1), kv_ptr, _stride(kv, 0), _stride(kv, 1), rope_ptr,
-                                         _stride(k_rope, 0), _ptr(cu_q, torch.int32), _ptr(cu_k, torch.int32), B, Tq, Tk,
-                                         int(max_q), int(max_k), H, float(scale), 1 if causal else 0, dt, _ptr(out),
-                                         _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                         _stream(stream)))
+    B = cu_q.shape[0] - 1
+    out, out_at = _out(out, (Tq, H, VALUE), dtype, dev)
+    lse, lse_at = _out(lse, (Tq, H), torch.float32, dev)
+    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_expanded_workspace(Tq, B, max_q, max_k, H), dev)
+    _check(_lib.idx_topk_latent_expanded(q_at, *_strides(q), kv_at, *_strides(kv), rope_at, *_strides(k_rope),
+                                         _at(cu_q, torch.int32, dev), _at(cu_k, torch.int32, dev), B, Tq, Tk, max_q, max_k,
+                                         H, scale, 1 if causal else 0, dt, out_at, lse_at, ws_at, ws_bytes, _on(stream, dev)))
     return out, lse
 
 
@@ -581,22 +598,24 @@ def norm_quant(x, weight, eps: float, residual=None, group: int = 0, codes=None,
     f32, x + residual or None): the last one is residual_out, or with a
     residual and no residual_out a new tensor.
     """
-    dt = _dtype16(x)
-    x_ptr = _rows16(x, x.dtype, None, None)
-    R, W = int(x.shape[0]), int(x.shape[1])
-    dev = x.device
-    res_ptr = None if residual is None else _rows16(residual, x.dtype, R, W)
-    if weight is not None and tuple(weight.shape) != (W,):
+    dt, dev, dtype = _dtype16(x), x.device, x.dtype
+    if x.dim() != 2:
+        raise ValueError("expected x [R,W], got %s" % list(x.shape))
+    R, W = shape = x.shape
+    x_at = _rows_at(x, dtype, dev, shape)
+    res_at, res_stride = None, 0
+    if residual is not None:
+        res_at = _rows_at(residual, dtype, dev, shape)
+        res_stride, = _strides(residual)
+    if weight is not None and weight.shape != (W,):
         raise ValueError("expected a weight of shape [%d], got %s" % (W, list(weight.shape)))
-    groups = W // group if group > 0 else 1
-    codes = _out(codes, (R, W), torch.float8_e4m3fn, dev)
-    scales = _out(scales, (R, groups), torch.float32, dev)
+    codes, codes_at = _out(codes, shape, torch.float8_e4m3fn, dev)
+    scales, scales_at = _out(scales, (R, W // group if group > 0 else 1), torch.float32, dev)
+    out_at = None
     if residual is not None or residual_out is not None:
-        residual_out = _out(residual_out, (R, W), x.dtype, dev)
-    _same_device(dev, residual, weight, codes, scales, residual_out)
-    _check(_lib.idx_topk_norm_quant(x_ptr, _stride(x, 0), res_ptr, 0 if residual is None else _stride(residual, 0),
-                                    _ptr(weight, x.dtype), float(eps), R, W, int(group), dt, _ptr(codes), _ptr(scales),
-                                    _ptr(residual_out), _stream(stream)))
+        residual_out, out_at = _out(residual_out, shape, dtype, dev)
+    _check(_lib.idx_topk_norm_quant(x_at, *_strides(x), res_at, res_stride, None if weight is None else _at(weight, dtype, dev),
+                                    eps, R, W, group, dt, codes_at, scales_at, out_at, _on(stream, dev)))
     return codes, scales, residual_out
 
 
@@ -611,29 +630,27 @@ def cache_append(latents, index_keys, slots, latent_cache, k_cache, k_scale, str
     one = latents if latents is not None else index_keys
     if one is None:
         raise ValueError("expected latents, index_keys or both")
-    dt, dev, T = _dtype16(one), one.device, int(one.shape[0])
-    if (latents is None) != (latent_cache is None) or len({index_keys is None, k_cache is None, k_scale is None}) != 1:
+    dt, dev, dtype, T = _dtype16(one), one.device, one.dtype, one.shape[0]
+    if (latents is None) != (latent_cache is None) or (index_keys is None) != (k_cache is None) or (k_cache is None) != (k_scale is None):
         raise ValueError("latents come with latent_cache, index_keys with k_cache and k_scale")
-    if tuple(slots.shape) != (T,):
+    if slots.shape != (T,):
         raise ValueError("expected slots of shape [%d], got %s" % (T, list(slots.shape)))
-    lat_ptr = key_ptr = cache_ptr = kc_ptr = ks_ptr = None
-    num = []
+    lat_at = cache_at = key_at = kc_at = ks_at = None
+    lat_stride = key_stride = 0
+    num = n = None
     if latents is not None:
-        lat_ptr = _rows16(latents, one.dtype, T, LATENT_ROW)
-        cache_ptr, n = _cache_rows(latent_cache, LATENT_ROW, one.dtype)
-        num.append(n)
+        lat_at = _rows_at(latents, dtype, dev, (T, LATENT_ROW))
+        lat_stride, = _strides(latents)
+        cache_at, num = _cache_at(latent_cache, LATENT_ROW, dtype, dev)
     if index_keys is not None:
-        key_ptr = _rows16(index_keys, one.dtype, T, DIM)
-        kc = k_cache.view(torch.uint8) if k_cache.dtype == torch.float8_e4m3fn else k_cache
-        kc_ptr, n = _cache_rows(kc, DIM, torch.uint8)
-        ks_ptr = _ptr(k_scale, torch.float32)
-        num += [n, k_scale.numel()]
-    if len(set(num)) != 1:
-        raise ValueError("the caches hold different numbers of slots: %s" % num)
-    _same_device(dev, latents, index_keys, slots, latent_cache, k_cache, k_scale)
-    _check(_lib.idx_topk_cache_append(lat_ptr, 0 if latents is None else _stride(latents, 0), key_ptr,
-                                      0 if index_keys is None else _stride(index_keys, 0), _ptr(slots, torch.int32), T, dt,
-                                      cache_ptr, kc_ptr, ks_ptr, num[0], _stream(stream)))
+        key_at = _rows_at(index_keys, dtype, dev, (T, DIM))
+        key_stride, = _strides(index_keys)
+        kc_at, n = _cache_at(k_cache, DIM, torch.float8_e4m3fn if k_cache.dtype == torch.float8_e4m3fn else torch.uint8, dev)
+        ks_at = _at(k_scale, torch.float32, dev)
+        if k_scale.numel() != n or (num is not None and num != n):
+            raise ValueError("the caches hold different numbers of slots: %s" % [num, n, k_scale.numel()])
+    _check(_lib.idx_topk_cache_append(lat_at, lat_stride, key_at, key_stride, _at(slots, torch.int32, dev), T, dt, cache_at,
+                                      kc_at, ks_at, n if num is None else num, _on(stream, dev)))
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
