@@ -165,12 +165,6 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     const int tiles = (len + kTileKeys - 1) / kTileKeys;
     tile0 = tiles * part.part / A.parts;
     tile1 = tiles * (part.part + 1) / A.parts;
-    // this range's slots, -1 for what is not to be read
-    for (int i = tid; i < (tile1 - tile0) * kTileKeys + kTileKeys; i += 64 * HG * KG) {
-      const int at = tile0 * kTileKeys + i;
-      const int s = at < min(len, tile1 * kTileKeys) ? A.list[(int64_t)part.b * A.K + at] : -1;
-      s_list[i] = s >= 0 && s < A.num_slots ? s : -1;
-    }
   }
   const int b = part.b;
   const int row = (rb * HG + hg) * kRowsWave + col;
@@ -179,7 +173,28 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   int limit = PAGED ? len - A.S + 1 + step : len;  // this lane's row sees keys below
   const int limit_min = PAGED ? len - A.S + 1 : len;     // every row does
 
-  if (!PAGED) __syncthreads();
+  // The first memory the wave waits for: this range's slots (-1 for what is not
+  // to be read) go to LDS behind q's loads, which are under way meanwhile.
+  const int n_list = PAGED ? 0 : (tile1 - tile0) * kTileKeys + kTileKeys;
+  const auto listed = [&](int i) __attribute__((always_inline)) {
+    const int at = tile0 * kTileKeys + i;
+    return i < n_list && at < min(len, tile1 * kTileKeys) ? A.list[(int64_t)b * A.K + at] : -1;
+  };
+  int slot = PAGED ? -1 : listed(tid);
+  typename T::v8 q[kSteps];  // a row past the last repeats the first: its results are dropped
+  {
+    const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + step * A.q_token +
+                                head * A.q_head + 8 * g;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 32 * s);
+  }
+  if (!PAGED) {
+    for (int i = tid; i < n_list; i += 64 * HG * KG) {
+      s_list[i] = slot >= 0 && slot < A.num_slots ? slot : -1;
+      slot = listed(i + 64 * HG * KG);
+    }
+    __syncthreads();
+  }
 
   w4f o[kCols];
   RowStat st{-INFINITY, 0.f};
@@ -287,13 +302,6 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     next = source(kFlight);
   };
   if (steps > 0) load_first();
-  typename T::v8 q[kSteps];  // a row past the last repeats the first: its results are dropped
-  {
-    const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + step * A.q_token +
-                                head * A.q_head + 8 * g;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 32 * s);
-  }
 
   // Waits for step i's tile, computes its logits x, masked, and starts the
   // loads of a later tile on the way.
