@@ -569,32 +569,44 @@ static LatGeom layout(LatGeom g, int64_t B) {
   return g;
 }
 
+// Few tokens or sequences are cut in two ways that both fill the compute units:
+// many parts of all rows, or fewer parts of fewer rows.  The fixed costs of a
+// workgroup (its rows of q read, their partial results written and joined) go
+// with its rows, and a step of 32 rows costs three quarters of one of 64, so
+// where parts would be short the rows are halved first: 16 tokens x 64 heads x
+// 2048 keys take 24 us as 8 parts of 32 rows against 28 us as 16 parts of 64.
+constexpr int kManyParts = 8;     // listed: more parts a token than these are short
+constexpr int kShortKeys = 512;   // paged: keys a part at most, where the table says so
+
 static LatGeom listed_geom(int32_t T, int32_t H, int32_t K) {
   LatGeom g{};
   g.hg = row_groups(H);
-  g.row_blocks = (H + kRowsWave * g.hg - 1) / (kRowsWave * g.hg);
-  // lists are split where the tokens alone leave compute units idle; a part
-  // keeps at least two tiles
-  const int64_t groups = (int64_t)T * g.row_blocks;
-  int64_t parts = groups > 0 ? kUnits / groups : 1;
-  const int most = (K + 2 * kTileKeys - 1) / (2 * kTileKeys);
-  if (parts > most) parts = most;
-  g.parts = parts < 1 ? 1 : (int)parts;
-  g.cells = g.parts > 1 ? groups * g.parts : 0;
+  const int most = (K + 2 * kTileKeys - 1) / (2 * kTileKeys);  // a part keeps at least two tiles
+  for (;; g.hg /= 2) {
+    g.row_blocks = (H + kRowsWave * g.hg - 1) / (kRowsWave * g.hg);
+    const int64_t groups = (int64_t)T * g.row_blocks;
+    const int64_t parts = groups > 0 ? kUnits / groups : 1;
+    g.parts = parts < 1 ? 1 : parts > most ? most : (int)parts;
+    if (g.hg == 1) break;
+    const bool idle = 2 * groups * g.parts <= kUnits;  // half the units without work even so
+    if (!idle && (g.hg == 2 || g.parts <= kManyParts)) break;
+  }
+  g.cells = g.parts > 1 ? (int64_t)T * g.row_blocks * g.parts : 0;
   return layout(g, 0);
 }
 
 static LatGeom paged_geom(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
   LatGeom g{};
   const int rows = S * H;
-  g.hg = row_groups(rows);
-  g.row_blocks = (rows + kRowsWave * g.hg - 1) / (kRowsWave * g.hg);
   int64_t parts = B;
-  if (B <= kPlanBatch && max_pages > kMinPages) {
+  for (g.hg = row_groups(rows);; g.hg /= 2) {
+    g.row_blocks = (rows + kRowsWave * g.hg - 1) / (kRowsWave * g.hg);
+    if (B > kPlanBatch || max_pages <= kMinPages) break;
     parts = kUnits / g.row_blocks;
     if (parts < 2 * (int64_t)B) parts = 2 * (int64_t)B;
     const int64_t most = (int64_t)B * ((max_pages + kMinPages - 1) / kMinPages) + B;
     if (parts > most) parts = most;
+    if (g.hg <= 2 || (int64_t)B * max_pages * IDX_TOPK_PAGE / parts >= kShortKeys) break;
   }
   g.parts = (int)parts;
   g.cells = parts > B ? parts * g.row_blocks : 0;
