@@ -402,8 +402,8 @@ size_t idx_topk_latent_paged_workspace(int32_t B, int32_t S, int32_t H, int32_t 
  *              [0, max_pages * 64] is taken as 0
  *   out        [B][S][H][512], lse [B][S][H] float or NULL
  * Keys in pages whose id lies outside [0, num_pages) are skipped, as are cache slots past a
- * sequence's length (they may hold anything).  A step that sees no key gives o = 0 and
- * lse = -inf.
+ * sequence's length (they may hold anything; the S last tokens, which some steps see and others
+ * not, must be finite).  A step that sees no key gives o = 0 and lse = -inf.
  */
 int idx_topk_latent_paged(const void *q, int64_t q_seq, int64_t q_token, int64_t q_head,
                           const void *cache, int32_t num_pages, const int32_t *page_table,
@@ -494,8 +494,9 @@ const char *idx_topk_strerror(int code);
  *                                  capture mode; the legacy NULL stream cannot
  *                                  be captured: IDX_EINVAL)
  *   ... any of idx_topk_prefill, _prefill_debug (no timing events),
- *       _prefill_unfused, _rows, _decode_paged, _scan_bf16, _stream_floor
- *       on `stream`, in any number and order ...
+ *       _prefill_unfused, _rows, _decode_paged, _scan_bf16, _stream_floor,
+ *       _latent_selected, _latent_paged, _latent_expanded, _norm_quant,
+ *       _cache_append on `stream`, in any number and order ...
  *   idx_topk_graph_end(stream, &g) stops recording and instantiates the graph;
  *                                  on failure (a capture that was invalidated,
  *                                  a call that failed) returns IDX_EHIP, *g =

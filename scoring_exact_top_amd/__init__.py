@@ -477,20 +477,29 @@ def _strides(t: torch.Tensor):
     return [n if size > 1 else 0 for n, size in zip(t.stride(), t.shape)][:-1]
 
 
-def _out(t: Optional[torch.Tensor], shape, dtype, dev):
+def _empty(shape, dtype, dev, stream):
+    """A new tensor that belongs to the stream it is written on: one of the
+    current stream's could be memory that work still pending there uses."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _out(t: Optional[torch.Tensor], shape, dtype, dev, stream):
     """The caller's output, checked, or a new one; and its address."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = _empty(shape, dtype, dev, stream)
         return t, t.data_ptr()
     if t.shape != shape:
         raise ValueError("expected an output of shape %s, got %s" % (list(shape), list(t.shape)))
     return t, _at(t, dtype, dev)
 
 
-def _scratch(workspace: Optional[torch.Tensor], need: int, dev):
+def _scratch(workspace: Optional[torch.Tensor], need: int, dev, stream):
     """Address and size of the caller's workspace or a new one (and the tensor, to hold it)."""
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = _empty(max(need, 256), torch.uint8, dev, stream)
         return workspace.data_ptr(), max(need, 256), workspace
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("expected a contiguous workspace on %s" % dev)
@@ -498,7 +507,9 @@ def _scratch(workspace: Optional[torch.Tensor], need: int, dev):
 
 
 def _on(stream, dev) -> int:
-    """Handle of `stream`, or of the device's current stream."""
+    """Handle of `stream`, or of the current stream; the launch goes to the current device."""
+    if dev.index != torch._C._cuda_getDevice():
+        raise ValueError("expected tensors on the current device, got %s" % dev)
     return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
@@ -524,9 +535,9 @@ def latent_selected(q, cache, slots, scale: float, out=None, lse=None, workspace
     q_at = _rows_at(q, dtype, dev, (T, H, LATENT_ROW))
     q_token, q_head = _strides(q)
     cache_at, num_slots = _cache_at(cache, LATENT_ROW, dtype, dev)
-    out, out_at = _out(out, (T, H, LATENT), dtype, dev)
-    lse, lse_at = _out(lse, (T, H), torch.float32, dev)
-    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_selected_workspace(T, H, K), dev)
+    out, out_at = _out(out, (T, H, LATENT), dtype, dev, stream)
+    lse, lse_at = _out(lse, (T, H), torch.float32, dev, stream)
+    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_selected_workspace(T, H, K), dev, stream)
     _check(_lib.idx_topk_latent_selected(q_at, q_token, q_head, cache_at, num_slots, _at(slots, torch.int32, dev), K, T, H,
                                          scale, dt, out_at, lse_at, ws_at, ws_bytes, _on(stream, dev)))
     return out, lse
@@ -549,9 +560,9 @@ def latent_paged(q, cache, page_table, seq_lens, scale: float, out=None, lse=Non
     q_at = _rows_at(q, dtype, dev, (B, S, H, LATENT_ROW))
     q_seq, q_token, q_head = _strides(q)
     cache_at, num_slots = _cache_at(cache, LATENT_ROW, dtype, dev)
-    out, out_at = _out(out, (B, S, H, LATENT), dtype, dev)
-    lse, lse_at = _out(lse, (B, S, H), torch.float32, dev)
-    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_paged_workspace(B, S, H, max_pages), dev)
+    out, out_at = _out(out, (B, S, H, LATENT), dtype, dev, stream)
+    lse, lse_at = _out(lse, (B, S, H), torch.float32, dev, stream)
+    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_paged_workspace(B, S, H, max_pages), dev, stream)
     _check(_lib.idx_topk_latent_paged(q_at, q_seq, q_token, q_head, cache_at, num_slots // PAGE,
                                       _at(page_table, torch.int32, dev), max_pages, _at(seq_lens, torch.int32, dev), B, S, H,
                                       scale, dt, out_at, lse_at, ws_at, ws_bytes, _on(stream, dev)))
@@ -579,9 +590,9 @@ def latent_expanded(q, kv, k_rope, cu_q, cu_k, max_q: int, max_k: int, scale: fl
     if cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.shape[0] < 1:
         raise ValueError("expected cu_q and cu_k of shape [B+1]")
     B = cu_q.shape[0] - 1
-    out, out_at = _out(out, (Tq, H, VALUE), dtype, dev)
-    lse, lse_at = _out(lse, (Tq, H), torch.float32, dev)
-    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_expanded_workspace(Tq, B, max_q, max_k, H), dev)
+    out, out_at = _out(out, (Tq, H, VALUE), dtype, dev, stream)
+    lse, lse_at = _out(lse, (Tq, H), torch.float32, dev, stream)
+    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_expanded_workspace(Tq, B, max_q, max_k, H), dev, stream)
     _check(_lib.idx_topk_latent_expanded(q_at, *_strides(q), kv_at, *_strides(kv), rope_at, *_strides(k_rope),
                                          _at(cu_q, torch.int32, dev), _at(cu_k, torch.int32, dev), B, Tq, Tk, max_q, max_k,
                                          H, scale, 1 if causal else 0, dt, out_at, lse_at, ws_at, ws_bytes, _on(stream, dev)))
@@ -609,11 +620,11 @@ def norm_quant(x, weight, eps: float, residual=None, group: int = 0, codes=None,
         res_stride, = _strides(residual)
     if weight is not None and weight.shape != (W,):
         raise ValueError("expected a weight of shape [%d], got %s" % (W, list(weight.shape)))
-    codes, codes_at = _out(codes, shape, torch.float8_e4m3fn, dev)
-    scales, scales_at = _out(scales, (R, W // group if group > 0 else 1), torch.float32, dev)
+    codes, codes_at = _out(codes, shape, torch.float8_e4m3fn, dev, stream)
+    scales, scales_at = _out(scales, (R, W // group if group > 0 else 1), torch.float32, dev, stream)
     out_at = None
     if residual is not None or residual_out is not None:
-        residual_out, out_at = _out(residual_out, shape, dtype, dev)
+        residual_out, out_at = _out(residual_out, shape, dtype, dev, stream)
     _check(_lib.idx_topk_norm_quant(x_at, *_strides(x), res_at, res_stride, None if weight is None else _at(weight, dtype, dev),
                                     eps, R, W, group, dt, codes_at, scales_at, out_at, _on(stream, dev)))
     return codes, scales, residual_out

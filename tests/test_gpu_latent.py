@@ -133,6 +133,24 @@ def test_selected_strides_streams_and_repeats():
     _check_selected(q, cache, slots.cpu(), *lib.latent_selected(q, cache, slots, SCALE), heads=[0, 19])
 
 
+def test_new_outputs_belong_to_the_stream_of_the_call():
+    """Memory freed on the current stream may still be in use there: a call on another stream takes none of it."""
+    lib, g = _lib(), _gen(61)
+    q = _rand(g, 4, 16, 576, dtype=torch.bfloat16).cuda()
+    cache = _rand(g, 100, 576, dtype=torch.bfloat16).cuda()
+    slots = torch.randint(0, 100, (4, 33), generator=g).to(torch.int32).cuda()
+    want, want_lse = lib.latent_selected(q, cache, slots, SCALE)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    freed = [torch.empty(4, 16, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(4, 16, device="cuda")]
+    at = [t.data_ptr() for t in freed]
+    del freed
+    out, lse = lib.latent_selected(q, cache, slots, SCALE, stream=s)
+    assert out.data_ptr() not in at and lse.data_ptr() not in at
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
 def test_selected_offsets_past_32_bits():
     """A cache of more than 4 GiB: slots on both sides of 2^31 and 2^32 bytes."""
     lib, g = _lib(), _gen(7)
