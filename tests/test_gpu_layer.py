@@ -28,3 +28,64 @@ def test_layer(lens, steps):
     assert picks < 2 ** -7, picks
     for n, s in zip(lens, share):
         assert s == min(1.0, 2048 / (n + steps)), (n, s)
+
+
+def test_chain_in_a_graph():
+    """The five operators recorded once and replayed with eager work between: each replay equals the eager calls on the
+    data (tokens, slots, lengths, lists) then in place."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator().manual_seed(3)
+    B, H, P, most = 3, 20, 40, 12
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g).bfloat16().cuda()
+
+    cache, keys, scale = rand(P, 64, 576), torch.zeros(P, 64, 128, dtype=torch.uint8, device="cuda"), torch.zeros(P, 64, device="cuda")
+    table = torch.randperm(P, generator=g)[:B * most].view(B, most).to(torch.int32).cuda()
+    x, latents, q, kv = rand(B * 4, 128), rand(B, 576), rand(B, H, 576), rand(70, H, 256)
+    qe, rope = rand(70, H, 192), rand(70, 64)
+    new, slots = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, 300, dtype=torch.int32, device="cuda")
+    lens, cu = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+
+    def buffers():
+        def empty(*shape, dtype=torch.bfloat16):
+            return torch.zeros(*shape, dtype=dtype, device="cuda")
+        return {"codes": empty(B * 4, 128, dtype=torch.float8_e4m3fn), "scales": empty(B * 4, 1, dtype=torch.float32),
+                "selected": empty(B, H, 512), "selected_lse": empty(B, H, dtype=torch.float32), "paged": empty(B, 1, H, 512),
+                "paged_lse": empty(B, 1, H, dtype=torch.float32), "expanded": empty(70, H, 128),
+                "expanded_lse": empty(70, H, dtype=torch.float32), "cache": cache.clone(), "keys": keys.clone(), "key_scale": scale.clone()}
+
+    ws = [lib.alloc_workspace(n, "cuda") for n in (lib.latent_selected_workspace_bytes(B, H, 300),
+                                                   lib.latent_paged_workspace_bytes(B, 1, H, most),
+                                                   lib.latent_expanded_workspace_bytes(70, 2, 70, 70, H))]
+
+    def chain(b):
+        lib.norm_quant(x, None, 1e-6, codes=b["codes"], scales=b["scales"])
+        lib.cache_append(latents, x[:B], new, b["cache"], b["keys"], b["key_scale"])
+        lib.latent_selected(q, b["cache"], slots, 0.07, out=b["selected"], lse=b["selected_lse"], workspace=ws[0])
+        lib.latent_paged(q[:, None], b["cache"], table, lens, 0.07, out=b["paged"], lse=b["paged_lse"], workspace=ws[1])
+        lib.latent_expanded(qe, kv, rope, cu, cu, 70, 70, 0.07, out=b["expanded"], lse=b["expanded_lse"], workspace=ws[2])
+
+    recorded = buffers()
+    graph = lib.capture(lambda: chain(recorded))
+    for i in range(4):
+        log("replay", i)
+        x.copy_(rand(B * 4, 128))
+        latents.copy_(rand(B, 576))
+        q.copy_(rand(B, H, 576))
+        slots.copy_(torch.randint(-1, P * 64, (B, 300), generator=g))
+        lens.copy_(torch.tensor([64 * most, 1 + 200 * i, 0 if i == 2 else 65]))
+        at = lens.clamp(min=1) - 1
+        new.copy_(table[torch.arange(B, device="cuda"), at // 64] * 64 + at % 64)
+        cu.copy_(torch.tensor([0, 20 * i, 70]))
+        want = buffers()
+        chain(want)
+        for name, t in buffers().items():
+            recorded[name].copy_(t)
+        torch.cuda.synchronize()
+        graph.launch()
+        torch.cuda.synchronize()
+        for name in want:
+            a, b = recorded[name].view(torch.uint8), want[name].view(torch.uint8)
+            assert torch.equal(a, b), "replay %d: %s" % (i, name)
+    graph.destroy()
