@@ -23,6 +23,7 @@
 //                                                  once, where power holds the clock at 1.6 GHz; join 14
 //   16 tokens x 64 heads x 2048 of 262144 rows      24 us  walk 18, join 6: latency
 //   one token, 128 heads, 2048 rows                 16 us  walk 13, join 4: latency
+#include <type_traits>
 #include "idx_attn.hpp"
 #include "idx_latent.hpp"
 
@@ -317,8 +318,8 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   if (steps > 0) load_first();
 
   // Waits for step i's tile, computes its logits x, masked, and starts the
-  // loads of a later tile on the way.
-  const auto logits = [&](int i, w4f (&x)[2]) __attribute__((always_inline)) {
+  // loads of a later tile on the way (kMore).
+  const auto logits = [&](auto kMore, int i, w4f (&x)[2]) __attribute__((always_inline)) {
     dma_wait<(kFlight - 1) * kLoads>();
     tile_barrier();  // tile i is there and tile i - 1 is read: its buffer takes the next load
     const char* tile = s_tile + (kg * kRing + i % kRing) * kTileBytes;
@@ -343,7 +344,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
       if (n + kAhead < 2 * kSteps) read(n + kAhead);
       // a load every few products: a burst would wait for the memory pipeline
       constexpr int kEvery = 2 * kSteps / kLoads;
-      if (n % kEvery == 0 && n / kEvery < kLoads) {
+      if (kMore && n % kEvery == 0 && n / kEvery < kLoads) {
         __builtin_amdgcn_sched_barrier(0);
         load(next, n / kEvery);
       }
@@ -351,8 +352,10 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < kFlight; ++t) live[t] = live[t + 1];
-    live[kFlight] = next.live;
-    next = source(i + 1 + kFlight);
+    if constexpr (kMore) {
+      live[kFlight] = next.live;
+      next = source(i + 1 + kFlight);
+    }
     const int key0 = (mine + i * KG) * kTileKeys;
     if (live[0] != ~0u || key0 + kTileKeys > limit_min) {
       const int g4 = own_lane() >> 4 << 2;
@@ -363,6 +366,17 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
         const int key = (r & 3) + 16 * (r >> 2);
         if (!(live_g >> key & 1) || key >= limit_g) x[r >> 2][r & 3] = -INFINITY;
       }
+    }
+  };
+  // f(i) for every step, and whether it loads.  Two key groups have one tile each under way and a last step
+  // without loads: in a short walk loads of zeros would cost as much as the others (a token's 2048 keys
+  // over 32 workgroups: 2900 of 18700 clocks).
+  const auto walk = [&](const auto& f) __attribute__((always_inline)) {
+    if constexpr (kFlight > 1) {
+      for (int i = 0; i < steps; ++i) f(std::true_type{}, i);
+    } else {
+      for (int i = 0; i + 1 < steps; ++i) f(std::true_type{}, i);
+      if (steps > 0) f(std::false_type{}, steps - 1);
     }
   };
   // The largest logit of each row in a tile, in octaves.
@@ -381,9 +395,9 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
 #pragma unroll
     for (int d = 0; d < kCols; ++d) o[d] = w4f{};
     bool over = false;  // a logit passed its row's reference by too much
-    for (int i = 0; i < steps; ++i) {
+    walk([&](auto kMore, int i) __attribute__((always_inline)) {
       w4f x[2];
-      logits(i, x);
+      logits(kMore, i, x);
       const float mx = largest(x);
       st.m = st.m == -INFINITY ? mx : st.m;
       over |= __any(mx - st.m > T::kHeadroom);
@@ -415,7 +429,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
         if (n + kAhead < kCols) read(n + kAhead);
       }
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
     dma_wait<0>();
     tile_barrier();  // every tile is read, every load done
     if (attempt > 0 || steps == 0) break;
@@ -426,12 +440,11 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     if (!__builtin_amdgcn_readfirstlane(s_again)) break;
     st = RowStat{-INFINITY, 0.f};
     load_first();
-#pragma unroll 1
-    for (int i = 0; i < steps; ++i) {
+    walk([&](auto kMore, int i) __attribute__((always_inline)) {
       w4f x[2];
-      logits(i, x);
+      logits(kMore, i, x);
       st.m = fmaxf(st.m, largest(x));
-    }
+    });
     dma_wait<0>();
     tile_barrier();
     load_first();
