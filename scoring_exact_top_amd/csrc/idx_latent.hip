@@ -451,46 +451,59 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   }
   float l = sum_quarters(st.l), m = st.m;
 
-  // key groups are joined through LDS (nothing is in flight there any more):
-  // group 1 hands over m, l and o', 16 bytes a lane at a time
+  // Key groups are joined through LDS (nothing is in flight there any more): each hands the other m, l and
+  // half of o', 16 bytes a lane at a time, and goes on with its own half of the columns.
+  constexpr int kOwn = kCols / KG;
+  w4f r[kOwn];
   if (KG == 2) {
-    char* const buf = s_tile + hg * (kCols * 1024 + 512);
-    if (kg == 1) {
+    char* const give = s_tile + wave * (kOwn * 1024 + 512);
+    const char* const take = s_tile + (wave + HG) % (HG * KG) * (kOwn * 1024 + 512);
+    *reinterpret_cast<float2*>(give + lane * 8) = make_float2(m, l);
+    const auto hand = [&](auto from) __attribute__((always_inline)) {
 #pragma unroll
-      for (int d = 0; d < kCols; ++d) *reinterpret_cast<w4f*>(buf + 512 + d * 1024 + lane * 16) = o[d];
-      *reinterpret_cast<float2*>(buf + lane * 8) = make_float2(m, l);
-    }
+      for (int d = 0; d < kOwn; ++d) *reinterpret_cast<w4f*>(give + 512 + d * 1024 + lane * 16) = o[from + d];
+    };
+    const auto add = [&](auto own, float f0, float f1) __attribute__((always_inline)) {
+#pragma unroll
+      for (int d = 0; d < kOwn; ++d) r[d] = o[own + d] * f0 + *reinterpret_cast<const w4f*>(take + 512 + d * 1024 + lane * 16) * f1;
+    };
+    const std::integral_constant<int, 0> low;
+    const std::integral_constant<int, kCols / 2> high;
+    if (kg == 0) hand(high);
+    else hand(low);
     __syncthreads();
-    if (kg == 1) return;
-    const float2 ml = *reinterpret_cast<const float2*>(buf + lane * 8);
+    const float2 ml = *reinterpret_cast<const float2*>(take + lane * 8);
     const float top = fmaxf(m, ml.x);
     const float f0 = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top), f1 = ml.x == top ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);
+    if (kg == 0) add(low, f0, f1);
+    else add(high, f0, f1);
     l = l * f0 + ml.y * f1;
     m = top;
+  } else {
 #pragma unroll
-    for (int d = 0; d < kCols; ++d) o[d] = o[d] * f0 + *reinterpret_cast<const w4f*>(buf + 512 + d * 1024 + lane * 16) * f1;
+    for (int d = 0; d < kOwn; ++d) r[d] = o[d];
   }
   if (part.parts > 1) {
     // in the order of the registers: whole lines, and the join adds them in that order too
     const int64_t cell = (int64_t)(wg * A.row_blocks + rb) * HG + hg;
-    float* po = A.part_o + cell * (kRowsWave * kLatent) + lane * 4;
+    float* po = A.part_o + cell * (kRowsWave * kLatent) + kg * kOwn * 256 + lane * 4;
 #pragma unroll
-    for (int d = 0; d < kCols; ++d) *reinterpret_cast<w4f*>(po + d * 256) = o[d];
-    if (g == 0) A.part_ml[cell * kRowsWave + col] = make_float2(m, l);
+    for (int d = 0; d < kOwn; ++d) *reinterpret_cast<w4f*>(po + d * 256) = r[d];
+    if (g == 0 && kg == 0) A.part_ml[cell * kRowsWave + col] = make_float2(m, l);
     return;
   }
   if (!have) return;
   const int64_t at = ((int64_t)b * A.S + step) * A.H + head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  typename T::elem* out = reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + 4 * g;
+  typename T::elem* out = reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + 16 * kg * kOwn + 4 * g;
 #pragma unroll
-  for (int d = 0; d < kCols; ++d) {
+  for (int d = 0; d < kOwn; ++d) {
     typename T::v4 v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = (typename T::elem)(o[d][j] * inv);
+    for (int j = 0; j < 4; ++j) v[j] = (typename T::elem)(r[d][j] * inv);
     *reinterpret_cast<typename T::v4*>(out + 16 * d) = v;
   }
-  if (A.lse && g == 0) A.lse[at] = row_lse(m, l);
+  if (A.lse && g == 0 && kg == 0) A.lse[at] = row_lse(m, l);
 }
 
 // Joins the parts of a row: o = sum_p 2^(m_p - m) o'_p / sum_p 2^(m_p - m) l_p.
