@@ -315,6 +315,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     }
     next = source(kFlight);
   };
+  if (tid == 0) s_again = 0;  // before the barriers of the walk
   if (steps > 0) load_first();
 
   // Waits for step i's tile, computes its logits x, masked, and starts the
@@ -394,6 +395,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   for (int attempt = 0;; ++attempt) {
 #pragma unroll
     for (int d = 0; d < kCols; ++d) o[d] = w4f{};
+    if (steps == 0) break;
     bool over = false;  // a logit passed its row's reference by too much
     walk([&](auto kMore, int i) __attribute__((always_inline)) {
       w4f x[2];
@@ -430,14 +432,10 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
       }
       __builtin_amdgcn_sched_barrier(0);
     });
+    if (over && lane == 0) s_again = 1;
     dma_wait<0>();
     tile_barrier();  // every tile is read, every load done
-    if (attempt > 0 || steps == 0) break;
-    if (tid == 0) s_again = 0;
-    __syncthreads();
-    if (over && lane == 0) s_again = 1;
-    __syncthreads();
-    if (!__builtin_amdgcn_readfirstlane(s_again)) break;
+    if (attempt > 0 || !__builtin_amdgcn_readfirstlane(s_again)) break;
     st = RowStat{-INFINITY, 0.f};
     load_first();
     walk([&](auto kMore, int i) __attribute__((always_inline)) {
