@@ -296,8 +296,9 @@ int cache_append(const void* latents, int64_t latent_token, const void* index_ke
                  int64_t num_slots, hipStream_t stream) {
   if (T < 0 || num_slots < 0 || latent_token < 0 || (latent_token & 7) || key_token < 0 || (key_token & 7)) return IDX_EINVAL;
   if (dtype != IDX_TOPK_BF16 && dtype != IDX_TOPK_F16) return IDX_EINVAL;
+  if (T == 0 || num_slots == 0) return IDX_OK;  // empty tensors have no address
   if ((!latents) != (!latent_cache) || (!index_keys) != (!k_cache) || (!k_cache) != (!k_scale)) return IDX_EINVAL;
-  if (T == 0 || num_slots == 0 || (!latents && !index_keys)) return IDX_OK;
+  if (!latents && !index_keys) return IDX_OK;
   if (!slots || !aligned16(latents) || !aligned16(latent_cache) || !aligned16(index_keys) || !aligned16(k_cache) ||
       ((uintptr_t)k_scale & 3u))
     return IDX_EINVAL;

@@ -394,3 +394,29 @@ def test_refusals():
             bad()
     out, lse = lib.latent_selected(q[:0], cache, slots[:0], SCALE)
     assert out.shape == (0, 4, 512) and lse.shape == (0, 4)
+
+
+def test_empty_calls():
+    """No tokens, sequences or prompts give empty outputs; caches without slots, tables without pages and no keys give
+    rows without keys."""
+    lib = _lib()
+
+    def zeros(*shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+    def no_keys(out, lse, shape):
+        torch.cuda.synchronize()
+        assert out.shape == shape and lse.shape == shape[:-1]
+        assert not out.any() and bool((lse == -math.inf).all())
+
+    i32 = torch.int32
+    no_keys(*lib.latent_selected(zeros(0, 20, 576), zeros(5, 576), zeros(0, 7, dtype=i32), SCALE), (0, 20, 512))
+    no_keys(*lib.latent_selected(zeros(2, 20, 576), zeros(0, 576), zeros(2, 7, dtype=i32), SCALE), (2, 20, 512))
+    no_keys(*lib.latent_paged(zeros(0, 1, 20, 576), zeros(5, 64, 576), zeros(0, 4, dtype=i32), zeros(0, dtype=i32), SCALE), (0, 1, 20, 512))
+    no_keys(*lib.latent_paged(zeros(2, 3, 20, 576), zeros(5, 64, 576), zeros(2, 0, dtype=i32), zeros(2, dtype=i32), SCALE), (2, 3, 20, 512))
+    no_keys(*lib.latent_paged(zeros(2, 3, 20, 576), zeros(0, 64, 576), zeros(2, 4, dtype=i32), zeros(2, dtype=i32) + 100, SCALE), (2, 3, 20, 512))
+    no_keys(*lib.latent_expanded(zeros(0, 4, 192), zeros(9, 4, 256), zeros(9, 64), zeros(2, dtype=i32), zeros(2, dtype=i32), 0, 9, SCALE), (0, 4, 128))
+    cu_q = torch.tensor([0, 6], dtype=i32, device="cuda")
+    no_keys(*lib.latent_expanded(zeros(6, 4, 192), zeros(0, 4, 256), zeros(0, 64), cu_q, zeros(2, dtype=i32), 6, 0, SCALE), (6, 4, 128))
+    out, lse = lib.latent_expanded(zeros(0, 4, 192), zeros(0, 4, 256), zeros(0, 64), zeros(1, dtype=i32), zeros(1, dtype=i32), 0, 0, SCALE)
+    assert out.shape == (0, 4, 128)

@@ -187,3 +187,22 @@ def test_append_one_cache_only_and_refusals():
                 lambda: lib.norm_quant(torch.zeros(1, 16385, dtype=torch.bfloat16, device="cuda"), None, 1e-6)):
         with pytest.raises(lib.IdxTopkError):
             bad()
+
+
+def test_empty_calls():
+    """No rows, no tokens, caches without slots: nothing is done and nothing refused."""
+    import scoring_exact_top_amd as lib
+
+    def zeros(*shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+    codes, scales, h = lib.norm_quant(zeros(0, 256), zeros(256), 1e-5, residual=zeros(0, 256), group=128)
+    assert codes.shape == (0, 256) and scales.shape == (0, 2) and h.shape == (0, 256)
+    for tokens, slots in ((0, 10), (3, 0), (0, 0)):
+        cache, keys, scale = zeros(slots, 576), zeros(slots, 128, dtype=torch.uint8), zeros(slots, dtype=torch.float32)
+        at = zeros(tokens, dtype=torch.int32)
+        lib.cache_append(zeros(tokens, 576) + 1, zeros(tokens, 128) + 1, at, cache, keys, scale)
+        lib.cache_append(zeros(tokens, 576) + 1, None, at, cache, None, None)
+        lib.cache_append(None, zeros(tokens, 128) + 1, at, None, keys, scale)
+        torch.cuda.synchronize()
+        assert not cache.any() and not keys.any() and not scale.any()
