@@ -452,8 +452,8 @@ def _at(t: torch.Tensor, dtype, dev) -> int:
     """Address of a contiguous tensor of this type on this device."""
     if t.dtype != dtype:
         raise ValueError("expected dtype %s, got %s" % (dtype, t.dtype))
-    if t.device != dev:
-        raise ValueError("expected all tensors on %s, got one on %s" % (dev, t.device))
+    if t.get_device() != dev:
+        raise ValueError("expected all tensors on cuda:%d, got one on %s" % (dev, t.device))
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return t.data_ptr()
@@ -463,8 +463,8 @@ def _rows_at(t: torch.Tensor, dtype, dev, shape) -> int:
     """Address of a strided input of this shape whose last dimension is contiguous."""
     if t.dtype != dtype:
         raise ValueError("expected dtype %s, got %s" % (dtype, t.dtype))
-    if t.device != dev:
-        raise ValueError("expected all tensors on %s, got one on %s" % (dev, t.device))
+    if t.get_device() != dev:
+        raise ValueError("expected all tensors on cuda:%d, got one on %s" % (dev, t.device))
     if t.shape != shape:
         raise ValueError("expected shape %s, got %s" % (list(shape), list(t.shape)))
     if t.stride(-1) != 1 and shape[-1] > 1:
@@ -474,6 +474,8 @@ def _rows_at(t: torch.Tensor, dtype, dev, shape) -> int:
 
 def _strides(t: torch.Tensor):
     """Strides in numbers but the last; a dimension of one has none that matters."""
+    if 1 not in t.shape:
+        return t.stride()[:-1]
     return [n if size > 1 else 0 for n, size in zip(t.stride(), t.shape)][:-1]
 
 
@@ -501,16 +503,16 @@ def _scratch(workspace: Optional[torch.Tensor], need: int, dev, stream):
     if workspace is None:
         workspace = _empty(max(need, 256), torch.uint8, dev, stream)
         return workspace.data_ptr(), max(need, 256), workspace
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("expected a contiguous workspace on %s" % dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("expected a contiguous workspace on cuda:%d" % dev)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _on(stream, dev) -> int:
     """Handle of `stream`, or of the current stream; the launch goes to the current device."""
-    if dev.index != torch._C._cuda_getDevice():
-        raise ValueError("expected tensors on the current device, got %s" % dev)
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("expected tensors on the current device, got cuda:%d" % dev)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _cache_at(cache: torch.Tensor, width: int, dtype, dev):
@@ -527,7 +529,7 @@ def latent_selected(q, cache, slots, scale: float, out=None, lse=None, workspace
     int32 (the output of prefill or decode_paged: -1 entries are skipped).
     Returns (out [T,H,512], lse [T,H] f32).
     """
-    dt, dev, dtype = _dtype16(q), q.device, q.dtype
+    dt, dev, dtype = _dtype16(q), q.get_device(), q.dtype
     if q.dim() != 3 or slots.dim() != 2 or slots.shape[0] != q.shape[0]:
         raise ValueError("expected q [T,H,576] and slots [T,K], got %s and %s" % (list(q.shape), list(slots.shape)))
     T, H, _ = q.shape
@@ -550,7 +552,7 @@ def latent_paged(q, cache, page_table, seq_lens, scale: float, out=None, lse=Non
     [P,64,576], page_table [B,max_pages] int32, seq_lens [B] int32 (device).
     Returns (out [B,S,H,512], lse [B,S,H] f32).
     """
-    dt, dev, dtype = _dtype16(q), q.device, q.dtype
+    dt, dev, dtype = _dtype16(q), q.get_device(), q.dtype
     if q.dim() != 4 or cache.dim() != 3 or cache.shape[1] != PAGE:
         raise ValueError("expected q [B,S,H,576] and a cache [pages,64,576], got %s and %s" % (list(q.shape), list(cache.shape)))
     B, S, H, _ = q.shape
@@ -579,7 +581,7 @@ def latent_expanded(q, kv, k_rope, cu_q, cu_k, max_q: int, max_k: int, scale: fl
     counts, max_q and max_k the longest prompt's query tokens and keys.
     Returns (out [Tq,H,128], lse [Tq,H] f32).
     """
-    dt, dev, dtype = _dtype16(q), q.device, q.dtype
+    dt, dev, dtype = _dtype16(q), q.get_device(), q.dtype
     if q.dim() != 3 or kv.dim() != 3:
         raise ValueError("expected q [Tq,H,192] and kv [Tk,H,256], got %s and %s" % (list(q.shape), list(kv.shape)))
     Tq, H, _ = q.shape
@@ -609,7 +611,7 @@ def norm_quant(x, weight, eps: float, residual=None, group: int = 0, codes=None,
     f32, x + residual or None): the last one is residual_out, or with a
     residual and no residual_out a new tensor.
     """
-    dt, dev, dtype = _dtype16(x), x.device, x.dtype
+    dt, dev, dtype = _dtype16(x), x.get_device(), x.dtype
     if x.dim() != 2:
         raise ValueError("expected x [R,W], got %s" % list(x.shape))
     R, W = shape = x.shape
@@ -641,7 +643,7 @@ def cache_append(latents, index_keys, slots, latent_cache, k_cache, k_scale, str
     one = latents if latents is not None else index_keys
     if one is None:
         raise ValueError("expected latents, index_keys or both")
-    dt, dev, dtype, T = _dtype16(one), one.device, one.dtype, one.shape[0]
+    dt, dev, dtype, T = _dtype16(one), one.get_device(), one.dtype, one.shape[0]
     if (latents is None) != (latent_cache is None) or (index_keys is None) != (k_cache is None) or (k_cache is None) != (k_scale is None):
         raise ValueError("latents come with latent_cache, index_keys with k_cache and k_scale")
     if slots.shape != (T,):
