@@ -453,8 +453,7 @@ int idx_topk_latent_expanded(const void *q, int64_t q_token, int64_t q_head, con
  *   codes     [rows][width] uint8, scales [rows][width / group] float (group 0: [rows])
  *   residual_out  NULL or [rows][width] in `dtype`: h rounded once; may be `residual` or `x`
  *             itself where that one's row stride is `width`
- * Here strides may be any non-negative number and pointers aligned to their type only; rows
- * that are 16-byte aligned with a width that is a multiple of 8 take the fast path.
+ * Here strides may be any non-negative number and pointers aligned to their type only.
  * Inputs must be finite.  No workspace.
  */
 int idx_topk_norm_quant(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
