@@ -180,9 +180,11 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 
 // 64 lanes x 16 bytes from src + off (a lane's) to 1 KiB of LDS in lane order,
 // without registers.  The compiler does not see the write: the tile waits
-// below order it.
+// below order it.  Nor does it see a memory instruction here, so the five wait
+// states that one needs after a vector instruction has written its scalar
+// address (v_readlane) are in the text: the s_mov and four of the s_nop.
 __device__ __forceinline__ void dma_row(const char* src, int off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(src));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(src));
 }
 __device__ __forceinline__ void dma_lanes(const char* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src));
