@@ -17,9 +17,9 @@
 // results a second kernel joins.
 //
 // Measured, and what bounds it (a call in a loop; walk and join as traced alone):
-//   4096 tokens x 64 heads x 2048 of 32768 rows   1301 us  898 TFLOP/s; 9.7 GB of rows gathered at
-//                                                  7.5 TB/s (the gather alone reaches 8.5)
-//   16 sequences to 65536 keys, 128 heads           159 us  walk 145: 3.5 TB/s and 830 TFLOP/s at
+//   4096 tokens x 64 heads x 2048 of 32768 rows   1316 us  888 TFLOP/s; 9.7 GB of rows gathered at
+//                                                  7.3 TB/s (the gather alone reaches 8.5)
+//   16 sequences to 65536 keys, 128 heads           163 us  walk 148: 3.4 TB/s and 810 TFLOP/s at
 //                                                  once, where power holds the clock at 1.6 GHz; join 14
 //   16 tokens x 64 heads x 2048 of 262144 rows      24 us  walk 19, join 6: latency
 //   one token, 128 heads, 2048 rows                 14 us  walk 11, join 4: latency

