@@ -638,7 +638,7 @@ static LatGeom paged_geom(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
   int64_t parts = B;
   for (g.hg = row_groups(rows);; g.hg /= 2) {
     g.row_blocks = (rows + kRowsWave * g.hg - 1) / (kRowsWave * g.hg);
-    if (B > kPlanBatch || max_pages <= kMinPages) break;
+    if (B == 0 || B > kPlanBatch || max_pages <= kMinPages) break;
     parts = kUnits / g.row_blocks;
     if (parts < 2 * (int64_t)B) parts = 2 * (int64_t)B;
     const int64_t most = (int64_t)B * ((max_pages + kMinPages - 1) / kMinPages) + B;

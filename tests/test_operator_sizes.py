@@ -1,0 +1,22 @@
+"""Workspace queries and size limits of the operators around the indexer, all
+answered on the host (no GPU needed)."""
+import pytest
+
+import scoring_exact_top_amd as st
+
+
+@pytest.mark.parametrize("B", [0, 1])
+@pytest.mark.parametrize("S,H,max_pages", [(1, 64, 16), (1, 128, 1024), (3, 20, 4), (16, 128, 3), (1, 1, 0), (1, 33, 2), (2, 128, 1)])
+def test_paged_workspace_of_smallest_batches(B, S, H, max_pages):
+    """A decode step without sequences is a call like any other: its workspace is small and not zero."""
+    need = st.latent_paged_workspace_bytes(B, S, H, max_pages)
+    assert need >= 256
+    if B == 0:
+        assert need == 256
+
+
+@pytest.mark.parametrize("H", [1, 20, 64, 128])
+def test_other_workspaces_of_empty_calls(H):
+    assert st.latent_selected_workspace_bytes(0, H, 2048) == 256
+    for sizes in ((0, 0, 0, 0), (0, 3, 0, 9000), (0, 3, 50, 9000), (40, 3, 0, 0), (40, 0, 40, 40)):
+        assert 0 < st.latent_expanded_workspace_bytes(*sizes, H) <= 512, sizes
