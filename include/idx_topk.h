@@ -388,7 +388,8 @@ int idx_topk_latent_selected(const void *q, int64_t q_token, int64_t q_head, con
                              float scale, int32_t dtype, void *out, float *lse, void *workspace,
                              size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace idx_topk_latent_paged needs (0 for arguments it rejects). */
+/* Bytes of workspace idx_topk_latent_paged needs (0 for arguments it rejects): at most 528 MiB,
+ * whatever the batch. */
 size_t idx_topk_latent_paged_workspace(int32_t B, int32_t S, int32_t H, int32_t max_pages);
 
 /*

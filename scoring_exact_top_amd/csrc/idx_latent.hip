@@ -55,9 +55,9 @@ struct LatArgs {
   float c;                         // scale * log2(e)
   char* out;
   float* lse;
-  float* part_o;                   // [(part * row_blocks + block) * HG + group] cells of 16 rows x 512 columns
+  float* part_o;                   // [(cell * row_blocks + block) * HG + group] 16 rows x 512 columns
   float2* part_ml;                 // ... of 16 rows
-  int2* plan;                      // paged: [B] first part and number of parts
+  int2* plan;                      // paged: [B] first cell and number of parts
 };
 
 // A row of zeros for keys that a tile does not have: they are masked, and
@@ -74,9 +74,11 @@ __device__ __forceinline__ int rope_swz(int r) { return (r >> 1) & 7; }
 // Workgroup `wg` of a paged call: its sequence, which of the sequence's parts
 // it takes and how many there are.  A sequence gets parts in proportion to its
 // pages, at least one and none under kMinPages; every workgroup (its first
-// wave) works the plan out from the lengths.
+// wave) works the plan out from the lengths.  Only the parts of sequences that
+// have several write partial results: they are numbered by themselves, `cell`
+// being the first of the sequence's.
 struct Part {
-  int b, part, parts, first;
+  int b, part, parts, cell;
 };
 constexpr int kMinPages = 2;
 
@@ -95,7 +97,7 @@ __device__ __forceinline__ int seq_len(const LatArgs& A, int b) {
 }
 
 __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
-  if (A.parts == A.B) return Part{wg, 0, 1, wg};
+  if (A.parts == A.B) return Part{wg, 0, 1, 0};
   int64_t total = 0;
   for (int b0 = 0; b0 < A.B; b0 += 64) {
     const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
@@ -104,16 +106,18 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   // sum of max(1, ceil(n / unit)) <= total / unit + B <= parts
   int unit = (int)((total + (A.parts - A.B) - 1) / (A.parts - A.B));
   unit = unit < kMinPages ? kMinPages : unit;
-  int base = 0;
+  int base = 0;  // sums over the sequences before: parts, and 2^16 x parts with a cell (2^11 at most each)
   for (int b0 = 0; b0 < A.B; b0 += 64) {
     const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
     const int parts = b0 + lane < A.B ? max(1, (n + unit - 1) / unit) : 0;
-    const int end = base + wave_incl_scan(parts, lane);
-    const uint64_t mine = __ballot(wg >= end - parts && wg < end);
+    const int both = parts > 1 ? parts << 16 | parts : parts;
+    const int end = base + wave_incl_scan(both, lane);
+    const int last = end & 0xFFFF;
+    const uint64_t mine = __ballot(wg >= last - parts && wg < last);
     if (mine) {
       const int at = __ffsll((unsigned long long)mine) - 1;
-      const int n_at = __shfl(parts, at, 64), first = __shfl(end, at, 64) - n_at;
-      return Part{b0 + at, wg - first, n_at, first};
+      const int n_at = __shfl(parts, at, 64), before = __shfl(end - both, at, 64);
+      return Part{b0 + at, wg - (before & 0xFFFF), n_at, before >> 16};
     }
     base = __shfl(end, 63, 64);
   }
@@ -160,8 +164,8 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     if (wave == 0) {
       part = plan_part(A, wg, lane);
       if (lane == 0) {
-        s_list[0] = part.b; s_list[1] = part.part; s_list[2] = part.parts; s_list[3] = part.first;
-        if (rb == 0 && part.b >= 0 && part.part == 0) A.plan[part.b] = make_int2(part.first, part.parts);
+        s_list[0] = part.b; s_list[1] = part.part; s_list[2] = part.parts; s_list[3] = part.cell;
+        if (A.parts > A.B && rb == 0 && part.b >= 0 && part.part == 0) A.plan[part.b] = make_int2(part.cell, part.parts);
       }
     }
     __syncthreads();
@@ -483,7 +487,8 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   }
   if (part.parts > 1) {
     // in the order of the registers: whole lines, and the join adds them in that order too
-    const int64_t cell = (int64_t)(wg * A.row_blocks + rb) * HG + hg;
+    const int of = PAGED ? __builtin_amdgcn_readfirstlane(s_list[3]) + part.part : wg;
+    const int64_t cell = ((int64_t)of * A.row_blocks + rb) * HG + hg;
     float* po = A.part_o + cell * (kRowsWave * kLatent) + kg * kOwn * 256 + lane * 4;
 #pragma unroll
     for (int d = 0; d < kOwn; ++d) *reinterpret_cast<w4f*>(po + d * 256) = r[d];
@@ -588,7 +593,7 @@ static inline size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
 // How a call is cut: 16 * hg rows a workgroup, `parts` as in LatArgs.
 struct LatGeom {
   int hg, row_blocks, parts;
-  int64_t cells;  // partial results of 16 * hg rows each (0: none)
+  int64_t cells;  // partial results of 16 * hg rows each (0: none), row blocks included
   size_t o, ml, plan, total;
 };
 
@@ -615,6 +620,16 @@ static LatGeom layout(LatGeom g, int64_t B) {
 constexpr int kManyParts = 8;     // listed: more parts a token than these are short
 constexpr int kShortKeys = 512;   // paged: keys a part at most, where the table says so
 
+// A paged call has B parts and `extra` more, and no part has more pages than
+// the total over `extra` (plan_part): as many extra parts as sequences, so that
+// a sequence longer than the average is cut, but no more than make the longest
+// part a quarter of a compute unit's share (half of it: 6% more time for 1024
+// sequences of up to 4096 keys, 128 heads).  Sequences cut into several parts have
+// less than 2 * extra of them together (n / unit + 1 < 2 n / unit each): that
+// many cells, at most 8 * 256 and a rounding of row blocks of 128 rows, which is
+// 521 MiB whatever the batch.
+constexpr int kExtraRounds = 4;
+
 static LatGeom listed_geom(int32_t T, int32_t H, int32_t K) {
   LatGeom g{};
   g.hg = row_groups(H);
@@ -639,15 +654,17 @@ static LatGeom paged_geom(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
   for (g.hg = row_groups(rows);; g.hg /= 2) {
     g.row_blocks = (rows + kRowsWave * g.hg - 1) / (kRowsWave * g.hg);
     if (B == 0 || B > kPlanBatch || max_pages <= kMinPages) break;
+    const int64_t extra = (kExtraRounds * kUnits + g.row_blocks - 1) / g.row_blocks;
     parts = kUnits / g.row_blocks;
-    if (parts < 2 * (int64_t)B) parts = 2 * (int64_t)B;
+    if (parts < B + (extra < B ? extra : B)) parts = B + (extra < B ? extra : B);
     const int64_t most = (int64_t)B * ((max_pages + kMinPages - 1) / kMinPages) + B;
     if (parts > most) parts = most;
     if (g.hg <= 2 || (int64_t)B * max_pages * IDX_TOPK_PAGE / parts >= kShortKeys) break;
   }
   g.parts = (int)parts;
-  g.cells = parts > B ? parts * g.row_blocks : 0;
-  return layout(g, B);
+  const int64_t cut = 2 * (parts - B);
+  g.cells = (cut < parts ? cut : parts) * g.row_blocks;
+  return layout(g, g.cells ? B : 0);
 }
 
 template <class T, bool PAGED>

@@ -20,3 +20,13 @@ def test_other_workspaces_of_empty_calls(H):
     assert st.latent_selected_workspace_bytes(0, H, 2048) == 256
     for sizes in ((0, 0, 0, 0), (0, 3, 0, 9000), (0, 3, 50, 9000), (40, 3, 0, 0), (40, 0, 40, 40)):
         assert 0 < st.latent_expanded_workspace_bytes(*sizes, H) <= 512, sizes
+
+
+@pytest.mark.parametrize("B", [1, 2, 16, 100, 128, 256, 300, 512, 700, 1023, 1024, 1025, 5000, 1 << 30])
+def test_paged_workspace_is_bounded(B):
+    """Whatever the batch, steps, heads and table: the bound that the header states."""
+    for S in (1, 2, 3, 4, 7, 13, 16):
+        for H in (1, 16, 20, 33, 64, 100, 113, 128):
+            for max_pages in (1, 3, 8, 16, 1024, 1 << 20):
+                need = st.latent_paged_workspace_bytes(B, S, H, max_pages)
+                assert 256 <= need <= 528 << 20, (B, S, H, max_pages, need)
