@@ -31,7 +31,12 @@
 //
 // P is rounded to the inputs' 16-bit type for the matrix core: its relative
 // rounding error (2^-8 at most for bfloat16, 2^-11 for half) is that of the output's
-// own rounding.  Logits, maxima, sums and o' stay in FP32; l sums the FP32 p.
+// own rounding.  Half has that precision from 2^-14 on only; below, p is off by up
+// to 2^-25, and under a key that dominates a row thousands of small p may all be
+// rounded the same way.  So half's reference stands some octaves under the maximum
+// and p runs up to 2^15: with lift L, l is at least 2^L, and n keys together move the
+// output by at most n 2^-(25 + L) of the largest value.  Logits, maxima, sums and o'
+// stay in FP32; l sums the FP32 p.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -44,6 +49,8 @@ typedef float w4f __attribute__((ext_vector_type(4)));
 struct TBf16 {
   // octaves that p may pass 1 by: o' and l stay far inside FP32's 2^127
   static constexpr float kHeadroom = 64.f;
+  static constexpr float kLift = 0.f;       // a moved reference is that many octaves below the maximum
+  static constexpr float kFullLift = 0.f;   // ... one that never has to move
   typedef __bf16 elem;
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
   typedef __bf16 v4 __attribute__((ext_vector_type(4)));
@@ -57,6 +64,8 @@ struct TBf16 {
 
 struct TF16 {
   static constexpr float kHeadroom = 15.f;  // half ends below 2^16
+  static constexpr float kLift = 7.f;       // n 2^-32: 2^-13 of the largest value at half a million keys
+  static constexpr float kFullLift = 15.f;
   typedef _Float16 elem;
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
   typedef _Float16 v4 __attribute__((ext_vector_type(4)));
@@ -72,8 +81,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // o' and l are rescaled only where a row's maximum passes its reference by
-// this many octaves: p stays below 2^8, far from any type's limit, and
-// rescaling o' (all its registers) becomes rare.  The quotient is the same.
+// this many octaves beyond the lift: p stays below 2^8 (half: 2^15), inside the
+// type, and rescaling o' (all its registers) becomes rare.  The quotient is the same.
 constexpr float kRescaleOctaves = 8.f;
 
 template <class V>
@@ -142,11 +151,15 @@ __device__ __forceinline__ float tile_max(const v16f& x, float c) {
 
 // Whether some row of the wave has to move its reference for a tile of
 // maximum mx (the first live keys move it from -inf).
-__device__ __forceinline__ bool must_move(const RowStat& st, float mx) { return __any(mx > st.m + kRescaleOctaves); }
+template <class T>
+__device__ __forceinline__ bool must_move(const RowStat& st, float mx) {
+  return __any(mx > st.m + (T::kLift + kRescaleOctaves));
+}
 
 // Moves the references to cover mx; returns the factor of o'.
+template <class T>
 __device__ __forceinline__ float move_reference(RowStat& st, float mx) {
-  const float m = fmaxf(st.m, mx);
+  const float m = fmaxf(st.m, mx - T::kLift);
   const float alpha = st.m == m ? 1.f : __builtin_amdgcn_exp2f(st.m - m);  // 0 where m was -inf
   st.m = m;
   st.l *= alpha;

@@ -153,8 +153,8 @@ __global__ __launch_bounds__(64 * kXWaves, 2) void k_expanded(ExpArgs A) {
           if (32 * u + key_of(r, 0) >= below) x[u][r] = -INFINITY;
     }
     const float mx = fmaxf(tile_max(x[0], A.c), tile_max(x[1], A.c));
-    if (must_move(st, mx)) {
-      const float alpha = move_reference(st, mx);
+    if (must_move<T>(st, mx)) {
+      const float alpha = move_reference<T>(st, mx);
 #pragma unroll
       for (int d = 0; d < kXCols; ++d) o[d] *= alpha;
     }

@@ -395,6 +395,10 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   // live tile's maximum instead: p may grow to kHeadroom octaves above 1, which
   // costs no precision.  A workgroup that sees more walks its keys again, first
   // for the rows' true maxima, then with those as references.
+  // Half's first reference is lifted only as the walk's n keys need it for an error
+  // of at most 2^-13 (n 2^-(25 + lift); none up to 4096 keys, 8 octaves for a million),
+  // since every octave of it is one less to grow before keys are walked again.
+  const float lift = T::kFullLift > 0.f ? (float)min(8, max(0, 25 - __builtin_clz(max(steps, 2) - 1))) : 0.f;
   __builtin_amdgcn_s_waitcnt(0x0F70);  // q is there: the waits below count tile loads only
   for (int attempt = 0;; ++attempt) {
 #pragma unroll
@@ -405,7 +409,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
       w4f x[2];
       logits(kMore, i, x);
       const float mx = largest(x);
-      st.m = st.m == -INFINITY ? mx : st.m;
+      st.m = st.m == -INFINITY ? mx - lift : st.m;
       over |= __any(mx - st.m > T::kHeadroom);
       const float m = st.m == -INFINITY ? 0.f : st.m;  // a row without a live key yet: p = 0
       typename T::v8 p;
@@ -447,6 +451,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
       logits(kMore, i, x);
       st.m = fmaxf(st.m, largest(x));
     });
+    st.m -= T::kFullLift;
     dma_wait<0>();
     tile_barrier();
     load_first();

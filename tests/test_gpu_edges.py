@@ -56,3 +56,60 @@ def test_paged_large_batches(B, S, H, long):
             for h in sorted({0, H - 1}):
                 want = attn_util.attend(q[b, j, h].double(), rows[:seen], rows[:seen, :512], SCALE)
                 attn_util.check_row(out[b, j, h], lse[b, j, h], want, seen, out.dtype, "sequence %d step %d head %d" % (b, j, h))
+
+
+def _sink_bound(q, k, v, scale):
+    """The definition, and the derived bound (attn_util) with half's absolute rounding of small weights on top: what it
+    moves is at most 2^-13 of the largest value, up to 2^19 keys."""
+    o, l, W, dl = attn_util.attend(q, k, v, scale)
+    n, u, e = k.shape[0], attn_util.U[torch.float16], attn_util.E
+    return o, l, u * o.abs() + (1.02 * u + 2.1 * dl + (n + 64) * e) * W + 2.0 ** -13 * v.abs().amax(0) + 2.0 ** -25, dl + (n + 64) * e + 2 * e * abs(l)
+
+
+@pytest.mark.parametrize("octaves", [12.5, 16.4, 20.5, 23.3, 25.5])
+@pytest.mark.parametrize("at", [0, 17000, 29999])
+def test_half_paged_tail_under_a_dominant_key(octaves, at):
+    """One key with value zero far above 29999 equal ones (first, in the middle, last): the output is the weight that the
+    small ones keep together.  More sequences than are ever cut, all over the same pages, so that one workgroup sees it all."""
+    import scoring_exact_top_amd as lib
+    n, B, H = 30000, 1025, 2
+    cache = torch.zeros((n + 63) // 64, 64, 576, dtype=torch.float16)
+    flat = cache.view(-1, 576)
+    flat[:, :512] = torch.linspace(0.5, 1.5, 512).half()
+    flat[at, :512] = 0
+    flat[at, 512] = octaves * math.log(2)
+    q = torch.zeros(B, 1, H, 576, dtype=torch.float16)
+    q[..., 512] = 1
+    table = torch.arange(cache.shape[0], dtype=torch.int32)[None].repeat(B, 1)
+    lens = torch.full((B,), n, dtype=torch.int32)
+    log("half paged tail", octaves, at)
+    out, lse = lib.latent_paged(q.cuda(), cache.cuda(), table.cuda(), lens.cuda(), 1.0)
+    o, l, tol, tol_l = _sink_bound(q[0, 0, 0].double(), flat[:n].double(), flat[:n, :512].double(), 1.0)
+    for b, h in ((0, 0), (500, 1), (B - 1, 0)):
+        off = (out[b, 0, h].double().cpu() - o).abs() - tol
+        assert float(off.max()) <= 0, "sequence %d: off by %.3g over the bound" % (b, float(off.max()))
+        assert abs(float(lse[b, 0, h]) - l) <= tol_l
+
+
+@pytest.mark.parametrize("octaves", [12.5, 16.4, 20.5, 23.3, 25.5])
+@pytest.mark.parametrize("at", [0, 17000, 29999])
+def test_half_expanded_tail_under_a_dominant_key(octaves, at):
+    """The same through the expanded form: two prompts of one query and 128 heads (one tensor broadcast), uncut."""
+    import scoring_exact_top_amd as lib
+    n, H = 30000, 128
+    kv = torch.zeros(n, 1, 256, dtype=torch.float16)
+    kv[..., 128:] = torch.linspace(0.5, 1.5, 128).half()
+    kv[at] = 0
+    rope = torch.zeros(n, 64, dtype=torch.float16)
+    rope[at, 0] = octaves * math.log(2)
+    q = torch.zeros(2, H, 192, dtype=torch.float16)
+    q[..., 128] = 1
+    cu_q, cu_k = torch.tensor([0, 1, 2], dtype=torch.int32).cuda(), torch.tensor([0, n, 2 * n], dtype=torch.int32).cuda()
+    log("half expanded tail", octaves, at)
+    out, lse = lib.latent_expanded(q.cuda(), torch.cat([kv, kv]).cuda().expand(-1, H, -1), torch.cat([rope, rope]).cuda(), cu_q, cu_k, 1, n, 1.0)
+    k = torch.cat([kv[:, 0, :128], rope], 1).double()
+    o, l, tol, tol_l = _sink_bound(q[0, 0].double(), k, kv[:, 0, 128:].double(), 1.0)
+    for b, h in ((0, 0), (1, 77), (1, H - 1)):
+        off = (out[b, h].double().cpu() - o).abs() - tol
+        assert float(off.max()) <= 0, "prompt %d: off by %.3g over the bound" % (b, float(off.max()))
+        assert abs(float(lse[b, h]) - l) <= tol_l
