@@ -382,7 +382,8 @@ size_t idx_topk_latent_selected_workspace(int32_t T, int32_t H, int32_t K);
  *   lse       [T][H] float or NULL
  * Sums and softmax statistics are FP32; the softmax weights are rounded to `dtype` for the
  * matrix cores (half: weights far below the row's largest to absolute steps, which moves an
- * output by at most 2^-13 of the largest value for up to 2^19 keys).  The result does not depend
+ * output by at most 2^-13 of the largest value for up to 2^19 keys).  Sums of bfloat16 values
+ * beyond 2^76 in magnitude (2^19 keys; 2^84 with 2^11) may leave FP32.  The result does not depend
  * on timing (no atomics on numbers).  This holds for the two forms below as well.
  */
 int idx_topk_latent_selected(const void *q, int64_t q_token, int64_t q_head, const void *cache,

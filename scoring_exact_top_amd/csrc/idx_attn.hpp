@@ -47,10 +47,13 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef float w4f __attribute__((ext_vector_type(4)));
 
 struct TBf16 {
-  // octaves that p may pass 1 by: o' and l stay far inside FP32's 2^127
-  static constexpr float kHeadroom = 64.f;
+  // A reference that never moves stands 32 octaves above the first maximum, so that logits may climb
+  // by 64 with p <= 2^32: o' then stays inside FP32 for values up to 2^(127 - 32) / n keys, and
+  // values down to 2^-70 keep all their bits.
+  static constexpr float kHeadroom = 32.f;  // octaves that p may pass 1 by
+  static __device__ __forceinline__ float first_lift(int) { return -32.f; }
   static constexpr float kLift = 0.f;       // a moved reference is that many octaves below the maximum
-  static constexpr float kFullLift = 0.f;   // ... one that never has to move
+  static constexpr float kFullLift = 0.f;   // ... one at the true maximum
   typedef __bf16 elem;
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
   typedef __bf16 v4 __attribute__((ext_vector_type(4)));
@@ -64,6 +67,11 @@ struct TBf16 {
 
 struct TF16 {
   static constexpr float kHeadroom = 15.f;  // half ends below 2^16
+  // A reference that never moves, over 32 * tiles keys: lifted only as they need it for an error of at
+  // most 2^-13 (none up to 4096 keys, 8 octaves for a million), since each octave is one less to climb.
+  static __device__ __forceinline__ float first_lift(int tiles) {
+    return (float)min(8, max(0, 25 - __builtin_clz(max(tiles, 2) - 1)));
+  }
   static constexpr float kLift = 7.f;       // n 2^-32: 2^-13 of the largest value at half a million keys
   static constexpr float kFullLift = 15.f;
   typedef _Float16 elem;
@@ -187,8 +195,10 @@ __device__ __forceinline__ typename T::v8 p_operand(const v16f& p, int s) {
   return o;
 }
 
+// log(sum exp).  m is a logit and a whole number of octaves, which l's exponent takes back without rounding.
 __device__ __forceinline__ float row_lse(float m, float l) {
-  return l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+  const float e = (float)__builtin_amdgcn_frexp_expf(l);
+  return l > 0.f ? (m + e + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(l))) * kLn2 : (l == 0.f ? -INFINITY : l);
 }
 
 // 64 lanes x 16 bytes from src + off (a lane's) to 1 KiB of LDS in lane order,

@@ -391,14 +391,11 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   };
 
   // Rescaling o' where a row's maximum grows would take all of its registers
-  // through others that are not there.  The reference stays at the row's first
-  // live tile's maximum instead: p may grow to kHeadroom octaves above 1, which
-  // costs no precision.  A workgroup that sees more walks its keys again, first
-  // for the rows' true maxima, then with those as references.
-  // Half's first reference is lifted only as the walk's n keys need it for an error
-  // of at most 2^-13 (n 2^-(25 + lift); none up to 4096 keys, 8 octaves for a million),
-  // since every octave of it is one less to grow before keys are walked again.
-  const float lift = T::kFullLift > 0.f ? (float)min(8, max(0, 25 - __builtin_clz(max(steps, 2) - 1))) : 0.f;
+  // through others that are not there.  The reference stays where the row's first
+  // live tile's maximum puts it instead: p may grow to kHeadroom octaves above 1,
+  // which costs no precision.  A workgroup that sees more walks its keys again,
+  // first for the rows' true maxima, then with those as references.
+  const float lift = T::first_lift(steps);
   __builtin_amdgcn_s_waitcnt(0x0F70);  // q is there: the waits below count tile loads only
   for (int attempt = 0;; ++attempt) {
 #pragma unroll

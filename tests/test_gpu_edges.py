@@ -113,3 +113,25 @@ def test_half_expanded_tail_under_a_dominant_key(octaves, at):
         off = (out[b, h].double().cpu() - o).abs() - tol
         assert float(off.max()) <= 0, "prompt %d: off by %.3g over the bound" % (b, float(off.max()))
         assert abs(float(lse[b, h]) - l) <= tol_l
+
+
+@pytest.mark.parametrize("power", [72, -60])
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("span", [0.0, 40.0, 300.0])
+def test_bfloat16_values_of_any_size(H, power, span):
+    """Values of 2^72 and of 2^-60 under logits that climb by 40 nats (inside what the first reference allows) and by 300,
+    through a list that is split and many that are not."""
+    import scoring_exact_top_amd as lib
+    g, n = torch.Generator().manual_seed(H), 640
+    cache = (torch.randn(n, 576, generator=g) * 2.0 ** power).bfloat16()
+    cache[:, 512:] = 0
+    cache[:, 512] = (torch.arange(n) * (span / n)).bfloat16()
+    for T in (2, 300):
+        q = torch.zeros(T, H, 576, dtype=torch.bfloat16)
+        q[..., 512] = 1
+        slots = torch.arange(n, dtype=torch.int32)[None].repeat(T, 1)
+        log("bfloat16 values", H, power, span, T)
+        out, lse = lib.latent_selected(q.cuda(), cache.cuda(), slots.cuda(), 1.0)
+        want = attn_util.attend(q[0, 0].double(), cache.double(), cache[:, :512].double(), 1.0)
+        for t, h in ((0, 0), (T - 1, H // 2), (T // 2, H - 1)):
+            attn_util.check_row(out[t, h], lse[t, h], want, n, out.dtype, "token %d head %d" % (t, h))
