@@ -458,7 +458,9 @@ int idx_topk_latent_expanded(const void *q, int64_t q_token, int64_t q_head, con
  *   residual_out  NULL or [rows][width] in `dtype`: h rounded once; may be `residual` or `x`
  *             itself where that one's row stride is `width`
  * Here strides may be any non-negative number and pointers aligned to their type only.
- * Inputs must be finite.  No workspace.
+ * A row of zeros gives codes 0 (with eps = 0 too).  A NaN or an infinity in a row of x or residual,
+ * or squares that leave FP32, give that row NaN codes (0x7F) and scale 1; one in the weight does so
+ * in the groups it stands in.  Such codes are not valid inputs of the indexer.  No workspace.
  */
 int idx_topk_norm_quant(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
                         const void *weight, float eps, int32_t rows, int32_t width, int32_t group,
@@ -469,7 +471,8 @@ int idx_topk_norm_quant(const void *x, int64_t x_stride, const void *residual, i
  *   latent_cache[slots[t],:] = latents[t,:]
  *   k_scale[slots[t]] = max|index_keys[t,:]| / 448 (1 for an all-zero key),
  *   k_cache[slots[t],:] = nearest e4m3fn of index_keys[t,:] / k_scale[slots[t]]
- * Tokens with other slots (-1: padding) are not stored.  The slots of one call must be distinct
+ * A key with a NaN or an infinity is stored as NaN codes (0x7F) with scale 1, which the indexer does
+ * not take.  Tokens with other slots (-1: padding) are not stored.  The slots of one call must be distinct
  * (two tokens of one slot leave a mixture there).
  *   latents     [T][576] stride latent_token, latent_cache [num_slots][576]; both NULL: not stored
  *   index_keys  [T][128] stride key_token, k_cache [num_slots][128] uint8, k_scale [num_slots];

@@ -31,18 +31,26 @@ __device__ __forceinline__ float wave_sum(float x) {
   for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
   return x;
 }
-__device__ __forceinline__ float wave_max(float x) {
+
+// Largest magnitudes are taken over the bits of |y| as integers: these order
+// finite numbers as the numbers do, infinity above them and every NaN above
+// that, so that a maximum keeps what fmaxf would drop.
+__device__ __forceinline__ uint32_t magnitude(float y) { return __float_as_uint(y) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
+  for (int d = 32; d >= 1; d >>= 1) x = max(x, (uint32_t)__shfl_xor((int)x, d, 64));
   return x;
 }
+__device__ __forceinline__ bool finite(uint32_t top) { return top < 0x7f800000u; }
 
 // The scale of a group whose largest magnitude is top: 1 for an all-zero group
-// (and for one so small that its scale would round to 0).
-__device__ __forceinline__ float scale_of(float top) {
-  const float s = top / kE4m3Max;
-  return s > 0.f ? s : 1.f;
+// (and for one so small that its scale would round to 0), and for one with a NaN
+// or an infinity, whose codes are all NaN.
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  const float s = __uint_as_float(top) / kE4m3Max;
+  return finite(top) && s > 0.f ? s : 1.f;
 }
+constexpr uint32_t kNanCodes = 0x7f7f7f7fu;
 
 // value / scale as value * up * inv: one division a group.  `up` lifts scales
 // whose reciprocal would overflow (a power of two: exact).
@@ -77,7 +85,8 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs A) {
   typedef E v8 __attribute__((ext_vector_type(8)));
   typedef E v8u __attribute__((ext_vector_type(8), aligned(2)));
   typedef uint32_t u2u __attribute__((ext_vector_type(2), aligned(1)));
-  __shared__ float s_red[2][4];
+  __shared__ float s_sum[4];
+  __shared__ uint32_t s_top[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t row = (int64_t)blockIdx.x * (256 / TPR) + tid / TPR;
   const int at = tid % TPR;  // this thread's first chunk
@@ -113,9 +122,9 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs A) {
 #pragma unroll
   for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1) ss += __shfl_xor(ss, d, 64);
   if (TPR == 256) {
-    if (lane == 0) s_red[0][wave] = ss;
+    if (lane == 0) s_sum[wave] = ss;
     __syncthreads();
-    ss = (s_red[0][0] + s_red[0][1]) + (s_red[0][2] + s_red[0][3]);
+    ss = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
   }
   if (A.residual_out) {
     E* out = static_cast<E*>(A.residual_out) + row * A.width;  // it may be x or residual itself: what this thread read
@@ -134,35 +143,43 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs A) {
           if (8 * i + j < A.width) out[8 * i + j] = v[j];
     }
   }
-  const float rstd = 1.f / sqrtf(ss / (float)A.width + A.eps);
-  float top[NC];
+  const float ms = ss / (float)A.width + A.eps;
+  float rstd = ms < INFINITY ? 1.f / sqrtf(ms) : NAN;  // a NaN or an infinity in the row, or its squares left FP32
+  if (ms == 0.f) {  // no eps: zeros stay zeros, and numbers whose squares are lost have no norm here
+    rstd = 1.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[c][j] = h[c][j] == 0.f ? 0.f : INFINITY;
+  }
+  uint32_t top[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int i = at + c * TPR;
     v8 wv = {};
     if (w && i < chunks) wv = load8<kAny>(w + 8 * i, A.width - 8 * i);
-    top[c] = 0.f;
+    top[c] = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       h[c][j] = h[c][j] * rstd * (w ? (float)wv[j] : 1.f);
-      top[c] = fmaxf(top[c], fabsf(h[c][j]));
+      top[c] = max(top[c], magnitude(h[c][j]));
     }
   }
   if (A.group) {
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) top[c] = fmaxf(top[c], __shfl_xor(top[c], d, 64));
+      for (int d = 1; d < 16; d <<= 1) top[c] = max(top[c], (uint32_t)__shfl_xor((int)top[c], d, 64));
   } else {
-    float t = top[0];
+    uint32_t t = top[0];
 #pragma unroll
-    for (int c = 1; c < NC; ++c) t = fmaxf(t, top[c]);
+    for (int c = 1; c < NC; ++c) t = max(t, top[c]);
 #pragma unroll
-    for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1) t = fmaxf(t, __shfl_xor(t, d, 64));
+    for (int d = 1; d < (TPR < 64 ? TPR : 64); d <<= 1) t = max(t, (uint32_t)__shfl_xor((int)t, d, 64));
     if (TPR == 256) {
-      if (lane == 0) s_red[1][wave] = t;
+      if (lane == 0) s_top[wave] = t;
       __syncthreads();
-      t = fmaxf(fmaxf(s_red[1][0], s_red[1][1]), fmaxf(s_red[1][2], s_red[1][3]));
+      t = max(max(s_top[0], s_top[1]), max(s_top[2], s_top[3]));
     }
 #pragma unroll
     for (int c = 0; c < NC; ++c) top[c] = t;
@@ -177,6 +194,7 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs A) {
     uint2 v;
     v.x = e4m3x2_enc(to(h[c][0]), to(h[c][1])) | e4m3x2_enc(to(h[c][2]), to(h[c][3])) << 16;
     v.y = e4m3x2_enc(to(h[c][4]), to(h[c][5])) | e4m3x2_enc(to(h[c][6]), to(h[c][7])) << 16;
+    if (!finite(top[c])) v.x = v.y = kNanCodes;
     uint8_t* codes = A.codes + row * A.width + 8 * i;
     if (!kAny) *reinterpret_cast<uint2*>(codes) = v;
     else if (8 * i + 8 <= A.width) *reinterpret_cast<u2u*>(codes) = u2u{v.x, v.y};
@@ -249,10 +267,10 @@ __global__ __launch_bounds__(256) void k_append(AppendArgs A) {
   if (A.k_cache) {
     const E* k = reinterpret_cast<const E*>(A.keys) + t * A.key_token + 2 * lane;
     const float a = (float)k[0], b = (float)k[1];
-    const float top = wave_max(fmaxf(fabsf(a), fabsf(b)));
+    const uint32_t top = wave_max(max(magnitude(a), magnitude(b)));
     const float scale = scale_of(top);
     const Scaler to(scale);
-    reinterpret_cast<uint16_t*>(A.k_cache + slot * kD)[lane] = (uint16_t)e4m3x2_enc(to(a), to(b));
+    reinterpret_cast<uint16_t*>(A.k_cache + slot * kD)[lane] = (uint16_t)(finite(top) ? e4m3x2_enc(to(a), to(b)) : kNanCodes);
     if (lane == 0) A.k_scale[slot] = scale;
   }
 }

@@ -135,3 +135,73 @@ def test_bfloat16_values_of_any_size(H, power, span):
         want = attn_util.attend(q[0, 0].double(), cache.double(), cache[:, :512].double(), 1.0)
         for t, h in ((0, 0), (T - 1, H // 2), (T // 2, H - 1)):
             attn_util.check_row(out[t, h], lse[t, h], want, n, out.dtype, "token %d head %d" % (t, h))
+
+
+# ------------------------------------------------------------------ quantisers
+
+def _nan(codes):
+    return codes.float().isnan()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("W,group", [(128, 0), (100, 0), (256, 128), (1000, 0), (2048, 128), (5120, 128), (5121, 0)])
+def test_norm_non_finite_rows(W, group, dtype):
+    """A NaN or an infinity anywhere in a row of x or of the residual gives NaN codes and scale 1 throughout the row; the
+    other rows keep their bits.  One in the weight does so in the groups it stands in."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator().manual_seed(W)
+    x, res = (torch.randn(7, W, generator=g).to(dtype).cuda() for _ in range(2))
+    w = (1 + 0.3 * torch.randn(W, generator=g)).to(dtype).cuda()
+    want, want_scales, _ = lib.norm_quant(x, w, 1e-6, residual=res, group=group)
+    assert not _nan(want).any()
+    bx, bres = x.clone(), res.clone()
+    bx[1, W // 2], bx[3, 0], bres[4, W - 1], bres[6, 1] = math.nan, math.inf, -math.inf, math.nan
+    bad = [1, 3, 4, 6]
+    codes, scales, _ = lib.norm_quant(bx, w, 1e-6, residual=bres, group=group)
+    for r in range(7):
+        if r in bad:
+            assert _nan(codes[r]).all() and (scales[r] == 1).all(), r
+        else:
+            assert torch.equal(codes[r].view(torch.uint8), want[r].view(torch.uint8)) and torch.equal(scales[r], want_scales[r])
+    for value in (math.nan, math.inf):
+        bw = w.clone()
+        bw[W - 3] = value
+        codes, scales, _ = lib.norm_quant(x, bw, 1e-6, residual=res, group=group)
+        n = group or W
+        assert _nan(codes[:, W - n:]).all() and (scales[:, -1] == 1).all()
+        assert torch.equal(codes[:, :W - n].contiguous().view(torch.uint8), want[:, :W - n].contiguous().view(torch.uint8))
+        assert torch.equal(scales[:, :-1], want_scales[:, :-1])
+
+
+@pytest.mark.parametrize("W,group", [(128, 0), (100, 0), (256, 128), (2048, 0), (5120, 128)])
+def test_norm_zero_rows_without_eps(W, group):
+    """eps = 0 is accepted: a row of zeros is codes 0 with scale 1, the others are what they are with a tiny eps."""
+    import scoring_exact_top_amd as lib
+    x = torch.randn(5, W, generator=torch.Generator().manual_seed(W)).bfloat16().cuda()
+    x[0], x[3] = 0, -0.0
+    codes, scales, _ = lib.norm_quant(x, None, 0.0, group=group)
+    want, want_scales, _ = lib.norm_quant(x, None, 1e-30, group=group)
+    for r in (0, 3):
+        assert (codes[r].float() == 0).all() and (scales[r] == 1).all(), r
+    assert torch.equal(codes.float(), want.float()) and torch.equal(scales, want_scales)
+
+
+def test_append_non_finite_keys():
+    """An index key with a NaN or an infinity is stored as NaN codes with scale 1; the other keys keep theirs."""
+    import scoring_exact_top_amd as lib
+    key = torch.randn(6, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    slots = torch.tensor([9, 0, 63, -1, 40, 5], dtype=torch.int32, device="cuda")
+
+    def stored(k):
+        kc, ks = torch.zeros(64, 128, dtype=torch.uint8, device="cuda"), torch.zeros(64, device="cuda")
+        lib.cache_append(None, k, slots, None, kc, ks)
+        return kc, ks
+
+    want, want_scales = stored(key)
+    bad = key.clone()
+    bad[0, 127], bad[2, 0], bad[3, 5], bad[4, 64] = math.nan, math.inf, math.nan, -math.inf
+    codes, scales = stored(bad)
+    for slot in (9, 63, 40):
+        assert _nan(codes[slot].view(torch.float8_e4m3fn)).all() and float(scales[slot]) == 1
+        codes[slot], scales[slot] = want[slot], want_scales[slot]
+    assert torch.equal(codes, want) and torch.equal(scales, want_scales)
