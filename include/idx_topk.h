@@ -447,7 +447,7 @@ int idx_topk_latent_expanded(const void *q, int64_t q_token, int64_t q_head, con
  * Root-mean-square norm with the residual's addition, quantised to e4m3:
  *   h = x + residual,  y = h * rsqrt(mean(h^2) + eps) * weight      (FP32, per row)
  *   scale = max|y| / 448 over each group of a row (1 where the group is all zero),
- *   codes = nearest e4m3fn of y / scale (ties to even)
+ *   codes = nearest e4m3fn of y / scale (an FP32 quotient; ties to even)
  * With rows of 128 numbers and group 0 the outputs are q and q_scale (or k and k_scale) of
  * idx_topk_prefill and idx_topk_decode_paged.
  *   x         [rows][width], row stride x_stride

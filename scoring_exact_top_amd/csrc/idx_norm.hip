@@ -52,12 +52,19 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
 }
 constexpr uint32_t kNanCodes = 0x7f7f7f7fu;
 
-// value / scale as value * up * inv: one division a group.  `up` lifts scales
-// whose reciprocal would overflow (a power of two: exact).
+// value / scale, rounded to FP32 once, with one division a group: the product
+// with the reciprocal is corrected by its own remainder, which an FMA gives
+// exactly (r = v - q s; q + r / s).  The product alone falls on the other side of
+// a tie between codes for one in 2000 of 16-bit keys.  `up` lifts small scales
+// so that neither the reciprocal nor the remainder leaves FP32 (a power of two: exact).
 struct Scaler {
-  float up, inv;
-  __device__ __forceinline__ explicit Scaler(float scale) : up(scale < 0x1p-100f ? 0x1p60f : 1.f), inv(1.f / (scale * up)) {}
-  __device__ __forceinline__ float operator()(float v) const { return v * up * inv; }
+  float up, s, inv;
+  __device__ __forceinline__ explicit Scaler(float scale)
+      : up(scale < 0x1p-64f ? 0x1p96f : 1.f), s(scale * up), inv(1.f / s) {}
+  __device__ __forceinline__ float operator()(float v) const {
+    const float q = v * up * inv;
+    return fmaf(fmaf(-q, s, v * up), inv, q);
+  }
 };
 
 // Eight numbers at p, or the n there are and zeros.  kAny: at any address (the memory pipeline takes

@@ -205,3 +205,49 @@ def test_append_non_finite_keys():
         assert _nan(codes[slot].view(torch.float8_e4m3fn)).all() and float(scales[slot]) == 1
         codes[slot], scales[slot] = want[slot], want_scales[slot]
     assert torch.equal(codes, want) and torch.equal(scales, want_scales)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_append_codes_are_the_nearest(dtype):
+    """Bit for bit the codes of k / scale, the quotient rounded to FP32 once: 16-bit keys meet ties often."""
+    import scoring_exact_top_amd as lib
+    g, T = torch.Generator().manual_seed(2), 8192
+    key = torch.randn(T, 128, generator=g).to(dtype)
+    key[0, :], key[0, 0], key[0, 1] = 0, 3.0625, 1.3671875
+    key[1::7] *= 2.0 ** -12
+    kc, ks = torch.zeros(T, 128, dtype=torch.uint8, device="cuda"), torch.zeros(T, device="cuda")
+    lib.cache_append(None, key.cuda(), torch.arange(T, dtype=torch.int32).cuda(), None, kc, ks)
+    scale = key.float().abs().amax(1) / 448
+    want = (key.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert torch.equal(ks.cpu(), scale)
+    assert float(want[0, 1].float()) == 192
+    assert torch.equal(kc.cpu().view(torch.float8_e4m3fn).float(), want.float())
+
+
+@pytest.mark.parametrize("W,group", [(128, 0), (128, 128), (1024, 128), (1027, 0)])
+def test_norm_codes_are_the_nearest(W, group):
+    """Rows whose mean square is exactly 1, so that y is x times the weight with no rounding before the quotient."""
+    import scoring_exact_top_amd as lib
+    g, R = torch.Generator().manual_seed(W), 512
+    a = torch.randint(-11, 12, (R, W), generator=g)
+    a[:, -6:] = 0
+    for r in range(R):                                             # sum of squares 64 W, in eighths: mean square 1
+        left = 64 * W - int((a[r] * a[r]).sum())
+        assert left > 0
+        for j in range(W - 1, -1, -1):
+            if left == 0:
+                break
+            if a[r, j] == 0:
+                a[r, j] = min(127, math.isqrt(left))
+                left -= int(a[r, j]) ** 2
+        assert left == 0
+    x = (a.double() / 8).bfloat16()
+    assert torch.equal(x.double() * 8, a.double())
+    w = (1 + 0.5 * torch.randn(W, generator=g)).bfloat16()
+    codes, scales, _ = lib.norm_quant(x.cuda(), w.cuda(), 0.0, group=group)
+    n = group or W
+    y = (x.float() * w.float()).view(R, -1, n)
+    scale = y.abs().amax(-1) / 448
+    want = (y / scale[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert torch.equal(scales.cpu(), scale)
+    assert torch.equal(codes.cpu().view(R, -1, n).float(), want.float())
