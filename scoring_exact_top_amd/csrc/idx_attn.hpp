@@ -205,13 +205,19 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // without registers.  The compiler does not see the write: the tile waits
 // below order it.  Nor does it see a memory instruction here, so the five wait
 // states that one needs after a vector instruction has written its scalar
-// address (v_readlane) are in the text: the s_mov and four of the s_nop.
+// address (v_readlane) are in the text: the s_mov and four of the s_nop.  m0 is
+// named as overwritten, so that no value that the compiler sets up there for an
+// instruction of its own is taken to outlive these (it is warned of as a register
+// that the compiler reserves, which is what is wanted).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma_row(const char* src, int off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(src));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(src) : "m0");
 }
 __device__ __forceinline__ void dma_lanes(const char* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src) : "m0");
 }
+#pragma clang diagnostic pop
 // All but the last N of this wave's loads to LDS are done.
 template <int N>
 __device__ __forceinline__ void dma_wait() {
