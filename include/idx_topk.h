@@ -351,6 +351,10 @@ int idx_topk_decode_paged_noalloc(const uint8_t *q, const float *q_scale, const 
  *
  * A latent row is 512 latent numbers, shared by all heads as key and as value,
  * followed by 64 rotary numbers that are key only.
+ *
+ * Calls too large for one launch are IDX_EUNSUPPORTED: 2^23 tokens or sequences and more of the
+ * absorbed forms (fewer with more than 128 rows a sequence; up to 2^25 with 16 heads), max_q
+ * beyond 16776960 of the expanded one.
  */
 #define IDX_TOPK_LATENT 512
 #define IDX_TOPK_ROPE 64

@@ -678,7 +678,9 @@ static int launch(LatArgs A, const LatGeom& g, char* ws, hipStream_t stream) {
   A.plan = reinterpret_cast<int2*>(ws + g.plan);
   const int64_t grid = (int64_t)(PAGED ? 1 : A.B) * g.parts * g.row_blocks;
   const int64_t join = (int64_t)A.B * g.row_blocks * g.hg * kCols;
-  if (grid > 0x7fffffffLL || join > 0x7fffffffLL) return IDX_EUNSUPPORTED;
+  // a launch dimension takes fewer than 2^32 threads (a larger one wraps, without an error)
+  const int64_t threads = 64 * (g.hg == 8 ? 8 : 2 * g.hg);
+  if (grid * threads > 0xffffffffLL || (g.cells && join * 256 > 0xffffffffLL)) return IDX_EUNSUPPORTED;
   const dim3 n((uint32_t)grid);
   if (g.hg == 1) k_latent<T, 1, 2, PAGED><<<n, dim3(128), 0, stream>>>(A);
   else if (g.hg == 2) k_latent<T, 2, 2, PAGED><<<n, dim3(256), 0, stream>>>(A);

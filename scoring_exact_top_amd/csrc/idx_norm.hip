@@ -82,6 +82,14 @@ __device__ __forceinline__ auto load8(const E* p, int n) {
   return v;
 }
 
+// A launch dimension takes fewer than 2^32 threads (a larger one wraps, without an
+// error): workgroups of 256 beyond 2^22 go on in the second dimension.
+constexpr int64_t kGridX = 1 << 22;
+__device__ __forceinline__ int64_t workgroup() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+static dim3 grid_of(int64_t groups) {
+  return groups <= kGridX ? dim3((uint32_t)groups) : dim3((uint32_t)kGridX, (uint32_t)((groups + kGridX - 1) / kGridX));
+}
+
 // Rows in chunks of 8 numbers, one load each: TPR threads a row (16, 64
 // or 256), NC chunks a thread, h kept in registers between the passes, so
 // that every byte is moved once.  A group of 128 columns is 16 neighbouring
@@ -95,7 +103,7 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs A) {
   __shared__ float s_sum[4];
   __shared__ uint32_t s_top[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t row = (int64_t)blockIdx.x * (256 / TPR) + tid / TPR;
+  const int64_t row = workgroup() * (256 / TPR) + tid / TPR;
   const int at = tid % TPR;  // this thread's first chunk
   const int chunks = (A.width + 7) >> 3;
   const bool live = row < A.rows;
@@ -221,7 +229,7 @@ __global__ __launch_bounds__(256) void k_norm_rows(NormArgs A) {
 template <class E, bool kAny>
 static void launch_rows(const NormArgs& A, hipStream_t stream) {
   const int chunks = (A.width + 7) >> 3;
-  const auto grid = [&](int tpr) { return dim3((uint32_t)(((int64_t)A.rows * tpr + 255) / 256)); };
+  const auto grid = [&](int tpr) { return grid_of(((int64_t)A.rows * tpr + 255) / 256); };
   if (chunks <= 16) k_norm_rows<E, 16, 1, kAny><<<grid(16), dim3(256), 0, stream>>>(A);
   else if (chunks <= 64) k_norm_rows<E, 64, 1, kAny><<<grid(64), dim3(256), 0, stream>>>(A);
   else if (chunks <= 128) k_norm_rows<E, 64, 2, kAny><<<grid(64), dim3(256), 0, stream>>>(A);
@@ -261,7 +269,7 @@ struct AppendArgs {
 template <class E>
 __global__ __launch_bounds__(256) void k_append(AppendArgs A) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t t = workgroup() * 4 + (threadIdx.x >> 6);
   if (t >= A.T) return;
   const int64_t slot = A.slots[t];
   if (slot < 0 || slot >= A.num_slots) return;
@@ -319,7 +327,7 @@ int cache_append(const void* latents, int64_t latent_token, const void* index_ke
     return IDX_EINVAL;
   const AppendArgs A{static_cast<const char*>(latents), latent_token, static_cast<const char*>(index_keys), key_token,
                      slots, T, static_cast<char*>(latent_cache), k_cache, k_scale, num_slots};
-  const dim3 grid((uint32_t)(((int64_t)T + 3) / 4));
+  const dim3 grid = grid_of(((int64_t)T + 3) / 4);
   if (dtype == IDX_TOPK_BF16) k_append<__bf16><<<grid, dim3(256), 0, stream>>>(A);
   else k_append<_Float16><<<grid, dim3(256), 0, stream>>>(A);
   return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;

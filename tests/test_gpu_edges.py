@@ -251,3 +251,31 @@ def test_norm_codes_are_the_nearest(W, group):
     want = (y / scale[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
     assert torch.equal(scales.cpu(), scale)
     assert torch.equal(codes.cpu().view(R, -1, n).float(), want.float())
+
+
+# ------------------------------------------------------------------ launches of 2^32 threads and more
+
+def test_norm_of_more_rows_than_one_grid_dimension_takes():
+    import scoring_exact_top_amd as lib
+    R, far = 2 ** 28 + 37, 2 ** 28 - 3
+    x = torch.randint(-100, 100, (R, 1), generator=torch.Generator("cuda").manual_seed(1), device="cuda", dtype=torch.int8).bfloat16()
+    log("norm rows", R)
+    codes, scales, _ = lib.norm_quant(x, None, 1.0)
+    for lo, hi in ((0, 1000), (R // 2, R // 2 + 1000), (far, R)):
+        want, want_scales, _ = lib.norm_quant(x[lo:hi], None, 1.0)
+        assert torch.equal(codes[lo:hi].view(torch.uint8), want.view(torch.uint8)) and torch.equal(scales[lo:hi], want_scales)
+
+
+def test_append_of_more_tokens_than_one_grid_dimension_takes():
+    import scoring_exact_top_amd as lib
+    T = 2 ** 26 + 11
+    key = torch.randn(1, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    slots[0], slots[2 ** 26 - 1], slots[2 ** 26], slots[T - 1] = 3, 1, 60, 22
+    kc, ks = torch.zeros(64, 128, dtype=torch.uint8, device="cuda"), torch.zeros(64, device="cuda")
+    log("append tokens", T)
+    lib.cache_append(None, key.expand(T, -1), slots, None, kc, ks)
+    at = [3, 1, 60, 22]
+    want = key.float() / (key.float().abs().amax() / 448)
+    assert torch.equal(kc[at].view(torch.float8_e4m3fn).float(), want.to(torch.float8_e4m3fn).float().expand(4, -1))
+    assert int((ks != 0).sum()) == 4

@@ -1,5 +1,7 @@
 """Workspace queries and size limits of the operators around the indexer, all
 answered on the host (no GPU needed)."""
+import ctypes
+
 import pytest
 
 import scoring_exact_top_amd as st
@@ -30,3 +32,16 @@ def test_paged_workspace_is_bounded(B):
             for max_pages in (1, 3, 8, 16, 1024, 1 << 20):
                 need = st.latent_paged_workspace_bytes(B, S, H, max_pages)
                 assert 256 <= need <= 528 << 20, (B, S, H, max_pages, need)
+
+
+def test_calls_too_large_for_one_launch_are_refused():
+    """A launch dimension of 2^32 threads would wrap: refused on the host, before any HIP call."""
+    L, at, big = st.raw_library(), ctypes.c_void_p(1 << 20), 1 << 40
+    for T, H in ((1 << 23, 128), (1 << 23, 64), (1 << 24, 32), (1 << 25, 16), (1 << 25, 1)):
+        rc = L.idx_topk_latent_selected(at, 0, 0, at, 100, at, 1, T, H, 0.1, 0, at, None, at, big, None)
+        assert rc == -2, (T, H)
+        rc = L.idx_topk_latent_paged(at, 0, 0, 0, at, 100, at, 4, at, T, 1, H, 0.1, 0, at, None, at, big, None)
+        assert rc == -2, (T, H)
+    for B, S, H in ((1 << 22, 2, 128), (1 << 20, 8, 128)):
+        assert L.idx_topk_latent_paged(at, 0, 0, 0, at, 100, at, 4, at, B, S, H, 0.1, 0, at, None, at, big, None) == -2, (B, S, H)
+    assert L.idx_topk_latent_expanded(at, 0, 0, at, 0, 0, at, 0, at, at, 1, 1 << 30, 100, 16776961, 100, 128, 0.1, 1, 0, at, None, at, big, None) == -2
