@@ -347,7 +347,7 @@ int idx_topk_decode_paged_noalloc(const uint8_t *q, const float *q_scale, const 
  * for them too, with these differences: their 16-bit tensors are bfloat16 or
  * half (`dtype`), and input strides are given in numbers, non-negative
  * multiples of 8, with unit stride along the last dimension; base pointers of
- * 16-bit tensors are 16-byte aligned.
+ * 16-bit tensors are 16-byte aligned, those of 32-bit ones 4-byte aligned.
  *
  * A latent row is 512 latent numbers, shared by all heads as key and as value,
  * followed by 64 rotary numbers that are key only.

@@ -237,6 +237,7 @@ __global__ __launch_bounds__(256) void k_expanded_join(ExpArgs A, int max_q) {
 // ------------------------------------------------------------------ host
 
 static inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+static inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 static bool bad_stride(int64_t s) { return s < 0 || (s & 7) != 0; }
 
 static inline size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -276,7 +277,8 @@ int latent_expanded(const void* q, int64_t q_token, int64_t q_head, const void* 
   const int64_t blocks = ((int64_t)max_q + kXRows - 1) / kXRows * parts;
   if (blocks > 65535) return IDX_EUNSUPPORTED;
   if (!q || !out || !cu_q || !cu_k || (Tk > 0 && (!kv || !k_rope))) return IDX_EINVAL;
-  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(out)) return IDX_EINVAL;
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(out) || !aligned4(cu_q) || !aligned4(cu_k) || !aligned4(lse))
+    return IDX_EINVAL;
   if (!workspace || workspace_bytes < latent_expanded_workspace_bytes(Tq, B, max_q, max_k, H)) return IDX_EWORKSPACE;
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   char* const ws = static_cast<char*>(workspace);

@@ -590,6 +590,7 @@ __global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int hgs, bool pa
 // ------------------------------------------------------------------ host
 
 static inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+static inline bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 static inline size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // How a call is cut: 16 * hg rows a workgroup, `parts` as in LatArgs.
@@ -699,7 +700,7 @@ static int check_common(const void* q, const void* cache, const int32_t* list, i
   if (dtype != IDX_TOPK_BF16 && dtype != IDX_TOPK_F16) return IDX_EINVAL;
   if (H > kMaxHeads) return IDX_EUNSUPPORTED;
   if (rows == 0) return IDX_OK;
-  if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned16(cache)) return IDX_EINVAL;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned16(cache) || !aligned4(list) || !aligned4(lse)) return IDX_EINVAL;
   return IDX_OK;
 }
 
@@ -739,7 +740,7 @@ int latent_paged(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, 
   if (max_pages > 0x7fffffff / IDX_TOPK_PAGE) return IDX_EUNSUPPORTED;
   const int rc = check_common(q, cache, page_table, B, H, scale, dtype, out, lse);
   if (rc != IDX_OK || B == 0) return rc;
-  if (!seq_lens || (!page_table && max_pages > 0) || (!cache && num_pages > 0)) return IDX_EINVAL;
+  if (!seq_lens || !aligned4(seq_lens) || (!page_table && max_pages > 0) || (!cache && num_pages > 0)) return IDX_EINVAL;
   const LatGeom g = paged_geom(B, S, H, max_pages);
   if (!workspace || workspace_bytes < g.total) return IDX_EWORKSPACE;
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;

@@ -323,7 +323,7 @@ int cache_append(const void* latents, int64_t latent_token, const void* index_ke
   if ((!latents) != (!latent_cache) || (!index_keys) != (!k_cache) || (!k_cache) != (!k_scale)) return IDX_EINVAL;
   if (!latents && !index_keys) return IDX_OK;
   if (!slots || !aligned16(latents) || !aligned16(latent_cache) || !aligned16(index_keys) || !aligned16(k_cache) ||
-      ((uintptr_t)k_scale & 3u))
+      (((uintptr_t)k_scale | (uintptr_t)slots) & 3u))
     return IDX_EINVAL;
   const AppendArgs A{static_cast<const char*>(latents), latent_token, static_cast<const char*>(index_keys), key_token,
                      slots, T, static_cast<char*>(latent_cache), k_cache, k_scale, num_slots};

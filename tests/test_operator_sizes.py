@@ -45,3 +45,17 @@ def test_calls_too_large_for_one_launch_are_refused():
     for B, S, H in ((1 << 22, 2, 128), (1 << 20, 8, 128)):
         assert L.idx_topk_latent_paged(at, 0, 0, 0, at, 100, at, 4, at, B, S, H, 0.1, 0, at, None, at, big, None) == -2, (B, S, H)
     assert L.idx_topk_latent_expanded(at, 0, 0, at, 0, 0, at, 0, at, at, 1, 1 << 30, 100, 16776961, 100, 128, 0.1, 1, 0, at, None, at, big, None) == -2
+
+
+def test_pointers_off_their_type_are_refused():
+    """int32 and FP32 arrays off 4 bytes: a scalar load of a page id would drop the address's low bits."""
+    L, at, big = st.raw_library(), ctypes.c_void_p(1 << 20), 1 << 40
+    for off in (1, 2, 3):
+        odd = ctypes.c_void_p((1 << 20) + off)
+        for slots, lse in ((odd, None), (at, odd)):
+            assert L.idx_topk_latent_selected(at, 576, 576, at, 100, slots, 8, 2, 4, 0.1, 0, at, lse, at, big, None) == -1
+        for table, lens, lse in ((odd, at, None), (at, odd, None), (at, at, odd)):
+            assert L.idx_topk_latent_paged(at, 0, 0, 0, at, 100, table, 4, lens, 2, 1, 4, 0.1, 0, at, lse, at, big, None) == -1
+        for cu_q, cu_k, lse in ((odd, at, None), (at, odd, None), (at, at, odd)):
+            assert L.idx_topk_latent_expanded(at, 0, 0, at, 0, 0, at, 0, cu_q, cu_k, 1, 8, 8, 8, 8, 4, 0.1, 1, 0, at, lse, at, big, None) == -1
+        assert L.idx_topk_cache_append(at, 576, at, 128, odd, 4, 0, at, at, at, 100, None) == -1
