@@ -448,6 +448,13 @@ def _dtype16(t: torch.Tensor) -> int:
 # The checks below cost a few hundred nanoseconds a call in all: a decode step's
 # launches wait for them.
 
+def _int32(n: int) -> None:
+    """n: sizes of a call, or'ed together, and not all of them small ones.  The library takes them in 32 bits, of
+    which ctypes would drop the rest; negative ones it refuses itself."""
+    if n >> 31 != -1:
+        raise ValueError("a size of this call is outside 32 bits")
+
+
 def _at(t: torch.Tensor, dtype, dev) -> int:
     """Address of a contiguous tensor of this type on this device."""
     if t.dtype != dtype:
@@ -534,6 +541,8 @@ def latent_selected(q, cache, slots, scale: float, out=None, lse=None, workspace
         raise ValueError("expected q [T,H,576] and slots [T,K], got %s and %s" % (list(q.shape), list(slots.shape)))
     T, H, _ = q.shape
     K = slots.shape[1]
+    if (T | H | K) >> 31:
+        _int32(T | H | K)
     q_at = _rows_at(q, dtype, dev, (T, H, LATENT_ROW))
     q_token, q_head = _strides(q)
     cache_at, num_slots = _cache_at(cache, LATENT_ROW, dtype, dev)
@@ -559,6 +568,8 @@ def latent_paged(q, cache, page_table, seq_lens, scale: float, out=None, lse=Non
     if page_table.dim() != 2 or page_table.shape[0] != B or seq_lens.shape != (B,):
         raise ValueError("expected page_table [%d, max_pages] and seq_lens [%d]" % (B, B))
     max_pages = page_table.shape[1]
+    if (B | S | H | max_pages | cache.shape[0]) >> 31:
+        _int32(B | S | H | max_pages | cache.shape[0])
     q_at = _rows_at(q, dtype, dev, (B, S, H, LATENT_ROW))
     q_seq, q_token, q_head = _strides(q)
     cache_at, num_slots = _cache_at(cache, LATENT_ROW, dtype, dev)
@@ -592,6 +603,8 @@ def latent_expanded(q, kv, k_rope, cu_q, cu_k, max_q: int, max_k: int, scale: fl
     if cu_q.dim() != 1 or cu_q.shape != cu_k.shape or cu_q.shape[0] < 1:
         raise ValueError("expected cu_q and cu_k of shape [B+1]")
     B = cu_q.shape[0] - 1
+    if (B | Tq | Tk | H | max_q | max_k) >> 31:
+        _int32(B | Tq | Tk | H | max_q | max_k)
     out, out_at = _out(out, (Tq, H, VALUE), dtype, dev, stream)
     lse, lse_at = _out(lse, (Tq, H), torch.float32, dev, stream)
     ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_expanded_workspace(Tq, B, max_q, max_k, H), dev, stream)
@@ -615,6 +628,8 @@ def norm_quant(x, weight, eps: float, residual=None, group: int = 0, codes=None,
     if x.dim() != 2:
         raise ValueError("expected x [R,W], got %s" % list(x.shape))
     R, W = shape = x.shape
+    if (R | W | group) >> 31:
+        _int32(R | W | group)
     x_at = _rows_at(x, dtype, dev, shape)
     res_at, res_stride = None, 0
     if residual is not None:
@@ -648,6 +663,8 @@ def cache_append(latents, index_keys, slots, latent_cache, k_cache, k_scale, str
         raise ValueError("latents come with latent_cache, index_keys with k_cache and k_scale")
     if slots.shape != (T,):
         raise ValueError("expected slots of shape [%d], got %s" % (T, list(slots.shape)))
+    if T >> 31:
+        _int32(T)
     lat_at = cache_at = key_at = kc_at = ks_at = None
     lat_stride = key_stride = 0
     num = n = None

@@ -279,3 +279,28 @@ def test_append_of_more_tokens_than_one_grid_dimension_takes():
     want = key.float() / (key.float().abs().amax() / 448)
     assert torch.equal(kc[at].view(torch.float8_e4m3fn).float(), want.to(torch.float8_e4m3fn).float().expand(4, -1))
     assert int((ks != 0).sum()) == 4
+
+
+def test_sizes_outside_32_bits_are_refused():
+    """ctypes drops the bits above 32: such a size would be answered as another, and a group of 2^32 + 128 would write
+    scales that no tensor holds.  Refused before anything is allocated."""
+    import scoring_exact_top_amd as lib
+
+    def wide(rows, *shape, dtype=torch.bfloat16):
+        return torch.zeros(1, *shape, dtype=dtype, device="cuda").expand(rows, *shape)
+
+    big, i32 = 2 ** 32 + 5, torch.int32
+    x, cu = wide(4, 256).contiguous(), torch.zeros(2, dtype=i32, device="cuda")
+    q, kv, rope = wide(4, 2, 192).contiguous(), wide(4, 2, 256).contiguous(), wide(4, 64).contiguous()
+    cache, pages = wide(5, 576).contiguous(), wide(1, 64, 576)
+    for bad in (lambda: lib.norm_quant(x, None, 1e-6, group=2 ** 32 + 128), lambda: lib.norm_quant(wide(big, 1), None, 1e-6),
+                lambda: lib.norm_quant(x, None, 1e-6, group=-2 ** 32 + 128),
+                lambda: lib.latent_expanded(q, kv, rope, cu, cu, 2 ** 32 + 4, 4, SCALE),
+                lambda: lib.latent_expanded(q, kv, rope, cu, cu, 4, 2 ** 32 + 4, SCALE),
+                lambda: lib.latent_selected(wide(big, 2, 576), cache, wide(big, 8, dtype=i32), SCALE),
+                lambda: lib.latent_paged(wide(big, 1, 2, 576), pages, wide(big, 3, dtype=i32), wide(big, dtype=i32), SCALE),
+                lambda: lib.cache_append(wide(big, 576), None, wide(big, dtype=i32), cache, None, None)):
+        with pytest.raises(ValueError, match="32 bits"):
+            bad()
+    with pytest.raises(lib.IdxTopkError):
+        lib.latent_expanded(q, kv, rope, cu, cu, -1, 4, SCALE)
