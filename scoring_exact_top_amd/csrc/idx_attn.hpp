@@ -57,6 +57,7 @@ struct TBf16 {
   typedef __bf16 elem;
   typedef __bf16 v8 __attribute__((ext_vector_type(8)));
   typedef __bf16 v4 __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ elem out(float x) { return (elem)x; }
   static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
@@ -77,6 +78,11 @@ struct TF16 {
   typedef _Float16 elem;
   typedef _Float16 v8 __attribute__((ext_vector_type(8)));
   typedef _Float16 v4 __attribute__((ext_vector_type(4)));
+  // The rounded weights' sum may pass l by a factor of 1 + 2^-11, and with it an average of values at the
+  // end of half's range that end.  Infinities among the values stay what they are.
+  static __device__ __forceinline__ elem out(float x) {
+    return (elem)(fabsf(x) < INFINITY ? __builtin_amdgcn_fmed3f(x, -65504.f, 65504.f) : x);
+  }
   static __device__ __forceinline__ v16f mfma(v8 a, v8 b, v16f c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }

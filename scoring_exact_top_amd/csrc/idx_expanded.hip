@@ -195,7 +195,7 @@ __global__ __launch_bounds__(64 * kXWaves, 2) void k_expanded(ExpArgs A) {
     for (int g = 0; g < 4; ++g) {
       typename T::v4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = (typename T::elem)(o[d][4 * g + j] * inv);
+      for (int j = 0; j < 4; ++j) v[j] = T::out(o[d][4 * g + j] * inv);
       *reinterpret_cast<typename T::v4*>(out + 32 * d + 8 * g + 4 * h) = v;
     }
   if (A.lse && h == 0) A.lse[at] = row_lse(st.m, l);
@@ -228,8 +228,7 @@ __global__ __launch_bounds__(256) void k_expanded_join(ExpArgs A, int max_q) {
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   typename T::v4 v;
-  v[0] = (typename T::elem)(o.x * inv); v[1] = (typename T::elem)(o.y * inv);
-  v[2] = (typename T::elem)(o.z * inv); v[3] = (typename T::elem)(o.w * inv);
+  v[0] = T::out(o.x * inv); v[1] = T::out(o.y * inv); v[2] = T::out(o.z * inv); v[3] = T::out(o.w * inv);
   *reinterpret_cast<typename T::v4*>(reinterpret_cast<typename T::elem*>(A.out) + at * kValue + c) = v;
   if (A.lse && c == 0) A.lse[at] = row_lse(m, l);
 }

@@ -505,7 +505,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   for (int d = 0; d < kOwn; ++d) {
     typename T::v4 v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = (typename T::elem)(r[d][j] * inv);
+    for (int j = 0; j < 4; ++j) v[j] = T::out(r[d][j] * inv);
     *reinterpret_cast<typename T::v4*>(out + 16 * d) = v;
   }
   if (A.lse && g == 0 && kg == 0) A.lse[at] = row_lse(m, l);
@@ -579,8 +579,7 @@ __global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int hgs, bool pa
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   typename T::v4 v;
-  v[0] = (typename T::elem)(o.x * inv); v[1] = (typename T::elem)(o.y * inv);
-  v[2] = (typename T::elem)(o.z * inv); v[3] = (typename T::elem)(o.w * inv);
+  v[0] = T::out(o.x * inv); v[1] = T::out(o.y * inv); v[2] = T::out(o.z * inv); v[3] = T::out(o.w * inv);
   const int64_t at = (int64_t)b * A.S * A.H + row;  // rows of a sequence are its steps' heads in order
   const int column = 16 * piece + 4 * (lane >> 4);
   *reinterpret_cast<typename T::v4*>(reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + column) = v;

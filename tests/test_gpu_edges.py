@@ -304,3 +304,48 @@ def test_sizes_outside_32_bits_are_refused():
             bad()
     with pytest.raises(lib.IdxTopkError):
         lib.latent_expanded(q, kv, rope, cu, cu, -1, 4, SCALE)
+
+
+@pytest.mark.parametrize("form", ["selected", "split list", "paged", "expanded", "split keys"])
+def test_half_outputs_at_the_end_of_the_range(form):
+    """All values the largest that half has: so is the output.  The weights of all keys but each 32nd are rounded up by
+    nearly half a step, which a sum over half's weights divided by the sum of the exact ones passes on."""
+    import scoring_exact_top_amd as lib
+    n, H = 2000, 3
+    scale = -math.log(0.5 * (1 + 1.05 * 2.0 ** -11))
+    log("half range", form)
+    if form in ("expanded", "split keys"):
+        kv = torch.full((n, H, 256), 65504.0).half()
+        kv[:, 1, 128:] = -65504
+        kv[..., :128] = 0
+        rope = torch.zeros(n, 64, dtype=torch.float16)
+        rope[:, 0] = -1
+        rope[::32, 0] = 0
+        T = 1 if form == "split keys" else 256 * 30
+        q = torch.zeros(T, H, 192, dtype=torch.float16)
+        q[..., 128] = 1
+        cu_q, cu_k = torch.tensor([0, T], dtype=torch.int32), torch.tensor([0, n], dtype=torch.int32)
+        out, lse = lib.latent_expanded(q.cuda(), kv.cuda(), rope.cuda(), cu_q.cuda(), cu_k.cuda(), T, n, scale, causal=False)
+        want = kv[:1, :, 128:].float()
+    else:
+        cache = torch.full((n + 48, 576), 65504.0).half().view(-1, 64, 576)
+        flat = cache.view(-1, 576)
+        flat[:, 1::2] *= -1
+        flat[:, 512:] = 0
+        flat[:, 512] = -1
+        flat[::32, 512] = 0
+        T = {"selected": 300, "split list": 1, "paged": 1100}[form]
+        q = torch.zeros(T, H, 576, dtype=torch.float16)
+        q[..., 512] = 1
+        if form == "paged":
+            table = torch.arange(cache.shape[0], dtype=torch.int32)[None].repeat(T, 1)
+            out, lse = lib.latent_paged(q[:, None].cuda(), cache.cuda(), table.cuda(), torch.full((T,), n, dtype=torch.int32).cuda(), scale)
+            out, lse = out[:, 0], lse[:, 0]
+        else:
+            slots = torch.arange(n, dtype=torch.int32)[None].repeat(T, 1)
+            out, lse = lib.latent_selected(q.cuda(), cache.cuda(), slots.cuda(), scale)
+        want = flat[:1, None, :512].float()
+    out = out.float().cpu()
+    assert torch.isfinite(out).all()
+    assert ((out - want).abs() <= 65504 * 2 ** -10).all()
+    assert abs(float(lse[0, 0]) - math.log(63 + (n - 63) * math.exp(-scale))) < 1e-3
