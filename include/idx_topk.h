@@ -379,7 +379,9 @@ size_t idx_topk_latent_selected_workspace(int32_t T, int32_t H, int32_t K);
  * and lse = -inf.
  *   q         [T][H][576], strides q_token, q_head
  *   cache     [num_slots][576] contiguous; any number of slots (64-bit offsets)
- *   slots     [T][K] int32, K in 1..2048
+ *   slots     [T][K] int32, K in 1..2048.  idx_topk_decode_paged lists slots; idx_topk_prefill lists
+ *             keys, which are slots where the cache's rows stand in key order (over a paged cache key s
+ *             of a sequence is slot page_table[s / 64] * 64 + s % 64: the caller's mapping)
  *   H         1..128
  *   scale     finite and > 0
  *   out       [T][H][512] in `dtype`, 16-byte aligned
@@ -435,7 +437,8 @@ size_t idx_topk_latent_expanded_workspace(int32_t Tq, int32_t B, int32_t max_q, 
  *   k_rope    [Tk][64], stride rope_token
  *   cu_q      [B+1] int32 device, cu_k [B+1] int32 device: running token counts.  A prompt whose
  *             range is not within [0, Tq] or [0, Tk] is skipped (its output is not written)
- *   max_q     at least the longest prompt's query tokens (queries past it are not computed),
+ *   max_q     at least the longest prompt's query tokens (past it, queries are computed to the end of
+ *             a block of 256 and then not written),
  *   max_k     about the longest prompt's keys (only sizes the launch); B at most 65535
  *   out       [Tq][H][128], lse [Tq][H] float or NULL
  * A key's numbers must be finite if any query of its prompt sees it.

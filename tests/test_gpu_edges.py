@@ -349,3 +349,132 @@ def test_half_outputs_at_the_end_of_the_range(form):
     assert torch.isfinite(out).all()
     assert ((out - want).abs() <= 65504 * 2 ** -10).all()
     assert abs(float(lse[0, 0]) - math.log(63 + (n - 63) * math.exp(-scale))) < 1e-3
+
+
+# ------------------------------------------------------------------ views, offsets past 32 bits, what max_q leaves out
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("W,group", [(1024, 128), (1024, 0), (128, 0), (2048, 128), (4104, 0)])
+def test_norm_of_views_is_bit_identical(W, group, dtype):
+    """Rows at every alignment, read and written: the same operations in the same order as on contiguous rows."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator().manual_seed(W)
+    wide = torch.randn(40, W + 52, generator=g).to(dtype).cuda()
+    w = torch.randn(W, generator=g).to(dtype).cuda()
+    flat = torch.randn(W + 8, generator=g).to(dtype).cuda()
+    for off in (0, 8, 4, 3, 1):
+        x, res = wide[:20, off:off + W], wide[20:, off:off + W]
+        want = lib.norm_quant(x.contiguous(), w, 1e-5, residual=res.contiguous(), group=group)
+        codes = torch.zeros(20 * W + 16, dtype=torch.float8_e4m3fn, device="cuda")[off:off + 20 * W].view(20, W)
+        out = torch.zeros(20 * W + 16, dtype=dtype, device="cuda")[off:off + 20 * W].view(20, W)
+        for kw in ({}, {"codes": codes}, {"residual_out": out}, {"codes": codes, "residual_out": out}):
+            got = lib.norm_quant(x, w, 1e-5, residual=res, group=group, **kw)
+            assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)), (off, kw.keys())
+            assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2]), (off, kw.keys())
+        odd = flat[off:off + W]
+        got, want = lib.norm_quant(x, odd, 1e-5, group=group), lib.norm_quant(x.contiguous(), odd.clone(), 1e-5, group=group)
+        assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1]), off
+
+
+def test_paged_offsets_past_32_bits():
+    """A cache of more than 4 GiB: pages on both sides of 2^31 and 2^32 bytes."""
+    import scoring_exact_top_amd as lib
+    g, size = torch.Generator().manual_seed(1), 64 * 1152
+    P = 2 ** 32 // size + 9
+    cache = torch.zeros(P, 64, 576, dtype=torch.bfloat16, device="cuda")
+    pages = [0, 2 ** 31 // size, 2 ** 31 // size + 1, 2 ** 32 // size, 2 ** 32 // size + 1, P - 1]
+    rows = torch.randn(len(pages), 64, 576, generator=g).bfloat16()
+    cache[torch.tensor(pages).cuda()] = rows.cuda()
+    n, H = 64 * len(pages) - 7, 20
+    q = torch.randn(1, 1, H, 576, generator=g).bfloat16()
+    log("paged past 2^32 bytes", P)
+    out, lse = lib.latent_paged(q.cuda(), cache, torch.tensor([pages], dtype=torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda(), SCALE)
+    k = rows.view(-1, 576)[:n].double()
+    for h in (0, H - 1):
+        attn_util.check_row(out[0, 0, h], lse[0, 0, h], attn_util.attend(q[0, 0, h].double(), k, k[:, :512], SCALE), n, out.dtype, "head %d" % h)
+
+
+def test_expanded_offsets_past_32_bits():
+    """Keys, values and queries in tensors of more than 4 GiB each (wide token strides): the last tokens are past 2^32 bytes."""
+    import scoring_exact_top_amd as lib
+    g, T, H, stride = torch.Generator().manual_seed(2), 1100, 2, 2 ** 21
+    big = torch.zeros(T, stride, dtype=torch.bfloat16, device="cuda")
+    q, kv, rope = torch.randn(T, H, 192, generator=g).bfloat16(), torch.randn(T, H, 256, generator=g).bfloat16(), torch.randn(T, 64, generator=g).bfloat16()
+    big[:, :H * 256] = kv.view(T, -1).cuda()
+    big[:, 4096:4096 + 64] = rope.cuda()
+    big[:, 8192:8192 + H * 192] = q.view(T, -1).cuda()
+    cu = torch.tensor([0, T], dtype=torch.int32).cuda()
+    log("expanded past 2^32 bytes", T)
+    out, lse = lib.latent_expanded(big[:, 8192:8192 + H * 192].unflatten(1, (H, 192)), big[:, :H * 256].unflatten(1, (H, 256)),
+                                   big[:, 4096:4096 + 64], cu, cu, T, T, SCALE)
+    for i, h in ((T - 1, 0), (T - 1, 1), (T - 60, 1), (1030, 0), (3, 1)):
+        k = torch.cat([kv[:i + 1, h, :128], rope[:i + 1]], 1).double()
+        want = attn_util.attend(q[i, h].double(), k, kv[:i + 1, h, 128:].double(), SCALE)
+        attn_util.check_row(out[i, h], lse[i, h], want, i + 1, out.dtype, "query %d head %d" % (i, h))
+
+
+def test_norm_and_append_offsets_past_32_bits():
+    import scoring_exact_top_amd as lib
+    R, W = 2 ** 32 // 8192 + 3, 8192                               # more than 2^32 numbers
+    x = torch.zeros(R, W, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, W, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    log("norm past 2^32 numbers", R)
+    codes, scales, _ = lib.norm_quant(x, None, 1e-6)
+    want, want_scales, _ = lib.norm_quant(x[-3:].clone(), None, 1e-6)
+    assert torch.equal(codes[-3:].view(torch.uint8), want.view(torch.uint8)) and torch.equal(scales[-3:], want_scales)
+    assert not codes[:-3:5000].view(torch.uint8).any() and (scales[:-3] == 1).all()
+    del x, codes
+    N = 2 ** 32 // 128 + 5                                         # k_cache of more than 2^32 bytes, latent rows of 9 times as many
+    cache, kc, ks = torch.zeros(N, 576, dtype=torch.bfloat16, device="cuda"), torch.zeros(N, 128, dtype=torch.uint8, device="cuda"), torch.zeros(N, device="cuda")
+    lat, key = torch.randn(2, 576).bfloat16().cuda(), torch.randn(2, 128).bfloat16().cuda()
+    lib.cache_append(lat, key, torch.tensor([N - 1, 2 ** 32 // 1152 + 1], dtype=torch.int32).cuda(), cache, kc, ks)
+    at = torch.tensor([N - 1, 2 ** 32 // 1152 + 1]).cuda()
+    assert torch.equal(cache[at], lat) and int((ks != 0).sum()) == 2
+    assert torch.equal(kc[at].view(torch.float8_e4m3fn).float(), (key.float() / ks[at][:, None]).to(torch.float8_e4m3fn).float())
+
+
+@pytest.mark.parametrize("Lk,H", [(600, 64), (9000, 1)])
+def test_expanded_queries_past_max_q(Lk, H):
+    """max_q below the longest prompt: its first queries are right, those past the blocks that hold max_q are not written."""
+    import scoring_exact_top_amd as lib
+    g, Lq = torch.Generator().manual_seed(4), 600
+    q, kv, rope = torch.randn(Lq, H, 192, generator=g).bfloat16(), torch.randn(Lk, H, 256, generator=g).bfloat16(), torch.randn(Lk, 64, generator=g).bfloat16()
+    cu_q, cu_k = torch.tensor([0, Lq], dtype=torch.int32).cuda(), torch.tensor([0, Lk], dtype=torch.int32).cuda()
+    for max_q in (100, 256, 300):
+        out, lse = torch.full((Lq, H, 128), 7.0).bfloat16().cuda(), torch.full((Lq, H), 7.0).cuda()
+        lib.latent_expanded(q.cuda(), kv.cuda(), rope.cuda(), cu_q, cu_k, max_q, Lk, SCALE, out=out, lse=lse)
+        done = -(-max_q // 256) * 256
+        assert (out[done:] == 7).all() and (lse[done:] == 7).all()
+        for i in (0, max_q - 1):
+            seen = i + 1 + Lk - Lq
+            k = torch.cat([kv[:seen, 0, :128], rope[:seen]], 1).double()
+            want = attn_util.attend(q[i, 0].double(), k, kv[:seen, 0, 128:].double(), SCALE)
+            attn_util.check_row(out[i, 0], lse[i, 0], want, seen, out.dtype, "query %d" % i)
+
+
+def test_attention_over_the_lists_of_a_prefill():
+    """The indexer's lists are numbers of keys: slots of a cache whose rows stand in key order as they come, and of a
+    paged one through its page table."""
+    import scoring_exact_top_amd as lib
+    g, T, N, H, K = torch.Generator().manual_seed(5), 40, 700, 20, 128
+    q8, qs, _ = lib.norm_quant(torch.randn(T * 64, 128, generator=g).bfloat16().cuda(), None, 1e-6)
+    k8, ks, _ = lib.norm_quant(torch.randn(N, 128, generator=g).bfloat16().cuda(), None, 1e-6)
+    lo = torch.zeros(T, dtype=torch.int32, device="cuda")
+    hi = torch.arange(N - T + 1, N + 1, dtype=torch.int32, device="cuda")
+    lists = lib.prefill(q8.view(T, 64, 128), qs.view(T, 64), k8, ks.view(-1), torch.rand(T, 64, generator=g).cuda(), lo, hi, K)
+    rows, q = torch.randn(N, 576, generator=g).bfloat16(), torch.randn(T, H, 576, generator=g).bfloat16()
+    out, lse = lib.latent_selected(q.cuda(), rows.cuda(), lists, SCALE)
+    for t in (0, T // 2, T - 1):
+        keep = lists[t].cpu().long()
+        assert int(keep.min()) >= 0 and int(keep.max()) < int(hi[t]) and len(set(keep.tolist())) == K
+        k = rows[keep].double()
+        for h in (0, H - 1):
+            attn_util.check_row(out[t, h], lse[t, h], attn_util.attend(q[t, h].double(), k, k[:, :512], SCALE), K, out.dtype, "token %d" % t)
+    pages = (N + 63) // 64
+    table = torch.randperm(pages + 3, generator=g)[:pages]
+    cache = torch.full((pages + 3, 64, 576), math.nan).bfloat16()
+    padded = torch.cat([rows, torch.zeros(pages * 64 - N, 576).bfloat16()])
+    cache[table] = padded.view(pages, 64, 576)
+    slots = table.cuda()[lists.long() // 64] * 64 + lists.long() % 64
+    paged, paged_lse = lib.latent_selected(q.cuda(), cache.cuda(), slots.to(torch.int32), SCALE)
+    assert torch.equal(paged, out) and torch.equal(paged_lse, lse)
