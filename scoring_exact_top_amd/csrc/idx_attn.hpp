@@ -10,9 +10,10 @@
 //
 // and o', l are multiplied by 2^(m_old - m_new) where m moves.
 //
-// A wave owns 32 rows.  Both products are v_mfma_f32_32x32x16 with the keys
-// (or the values' columns) as the 32 rows of A and the 32 attention rows as
-// the columns of B:
+// Both products have the keys (or the values' columns) as the rows of A and the
+// attention rows as the columns of B.  In the expanded form a wave owns 32 rows
+// and they are v_mfma_f32_32x32x16 (in the absorbed form 16 rows and
+// v_mfma_f32_16x16x32, laid out as k_latent says):
 //
 //   logits^T [32 keys x 32 rows] = K [32 x d] . Q^T [d x 32]
 //   o'^T     [32 columns x 32 rows] += V^T [32 x keys] . P^T [keys x 32]

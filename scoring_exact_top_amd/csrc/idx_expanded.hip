@@ -8,9 +8,9 @@
 // into a ring of three in LDS.  Few queries over many keys (a chunk of a long prompt) have their
 // keys split over workgroups, joined by a second kernel.  idx_attn.hpp has the arithmetic.
 //
-// Measured: 8192 tokens x 32 heads in 642 us, 1070 TFLOP/s of useful work; the matrix cores are 56%
+// Measured: 8192 tokens x 32 heads in 632 us, 1090 TFLOP/s of useful work; the matrix cores are 55%
 // busy at 1.9 GHz (their products alone, at the 1.6 GHz that power leaves them, take 430 us).  500
-// tokens over 16384 keys, 16 heads: 103 us, 9 of them the join.  64 rows a wave (half the LDS reads, but
+// tokens over 16384 keys, 16 heads: 102 us, 9 of them the join.  64 rows a wave (half the LDS reads, but
 // one wave a SIMD) takes as long, and so does the softmax spread between the products within a wave:
 // 12% fewer clocks, 4% less time on long prompts and 5% more on short ones.
 #include "idx_attn.hpp"

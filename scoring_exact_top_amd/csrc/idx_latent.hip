@@ -17,12 +17,12 @@
 // results a second kernel joins.
 //
 // Measured, and what bounds it (a call in a loop; walk and join as traced alone):
-//   4096 tokens x 64 heads x 2048 of 32768 rows   1316 us  888 TFLOP/s; 9.7 GB of rows gathered at
-//                                                  7.3 TB/s (the gather alone reaches 8.5)
-//   16 sequences to 65536 keys, 128 heads           163 us  walk 148: 3.4 TB/s and 810 TFLOP/s at
-//                                                  once, where power holds the clock at 1.6 GHz; join 14
-//   16 tokens x 64 heads x 2048 of 262144 rows      24 us  walk 19, join 6: latency
-//   one token, 128 heads, 2048 rows                 14 us  walk 11, join 4: latency
+//   4096 tokens x 64 heads x 2048 of 32768 rows   1297 us  901 TFLOP/s; 98% of the busy clocks are LDS
+//                                                  traffic (each wave reads every tile for 16 rows)
+//   16 sequences to 65536 keys, 128 heads           162 us  walk 146: the same 98%, at the 1.6 GHz that
+//                                                  power leaves; 3.4 TB/s, 820 TFLOP/s; join 13
+//   16 tokens x 64 heads x 2048 of 262144 rows      24 us  walk 18, join 6: latency, partial results
+//   one token, 128 heads, 2048 rows                 15 us  walk 11, join 3: latency
 #include <type_traits>
 #include "idx_attn.hpp"
 #include "idx_latent.hpp"
@@ -135,7 +135,7 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
 // for 16 rows only, twice what 32 rows would; but o' is then 128 registers and
 // q 72, two waves fit a SIMD, and one wave's softmax, LDS latency and stalls on
 // loads run beside the other's products.  A tile of 128 rows takes 4650 clocks
-// (2176 of them products, 4352 of them LDS reads), with 32 rows a wave and one
+// (4352 of LDS reads and 288 of writes, 2176 of products), with 32 rows a wave and one
 // wave a SIMD 4430 at a clock that power lowers from 1.64 to 1.61 GHz: 3% of
 // time, and only with the softmax spread over the products and every register
 // chosen by hand.
@@ -390,11 +390,15 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     return max_quarters(mx) * A.c;
   };
 
-  // Rescaling o' where a row's maximum grows would take all of its registers
-  // through others that are not there.  The reference stays where the row's first
-  // live tile's maximum puts it instead: p may grow to kHeadroom octaves above 1,
-  // which costs no precision.  A workgroup that sees more walks its keys again,
-  // first for the rows' true maxima, then with those as references.
+  // o' is not rescaled where a row's maximum grows.  With 16 or 32 rows a workgroup
+  // it lies in accumulation registers and would have to pass through ordinary ones;
+  // with more it lies in ordinary ones (253 to 256 are taken), where multiplying it in
+  // place has not been tried.  The reference stays where the row's first live tile's
+  // maximum puts it: p may grow to kHeadroom octaves above 1, which costs no precision.
+  // A workgroup that sees more walks its keys again, first for the rows' true maxima,
+  // then with those as references: 560 us instead of 229 for 16 half sequences of 40000
+  // keys, 128 heads, where every row's logits (standard deviation 7) climb by more than
+  // 15 octaves; bfloat16's 64 octaves take a standard deviation of 14 to be passed.
   const float lift = T::first_lift(steps);
   __builtin_amdgcn_s_waitcnt(0x0F70);  // q is there: the waits below count tile loads only
   for (int attempt = 0;; ++attempt) {

@@ -1,8 +1,8 @@
 // Root-mean-square norm with the residual's addition to e4m3 codes and scales, and the append
 // of new tokens to the caches (gfx950).  Both are bound by memory: every input is read once and
-// every output written once.  Measured: 8192 rows of 5120 with the residual 54.9 us, 5.4 TB/s;
-// 30000 appended tokens 16.0 us, 5.0 TB/s (a large copy reaches 4.7); 1024 rows of 128 take 3 us on
-// the card, and the host sets the call's 7.2.
+// every output written once.  Measured: 8192 rows of 5120 with the residual 55.2 us, 5.3 TB/s;
+// 30000 appended tokens 16.1 us, 5.0 TB/s (a large copy reaches 4.7); 1024 rows of 128 take 3 us on
+// the card, and the host sets the call's 7.3.
 #include "idx_common.hpp"
 #include "idx_latent.hpp"
 #include "idx_norm.hpp"
@@ -25,12 +25,6 @@ struct NormArgs {
   float* scales;
   void* residual_out;
 };
-
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
-  return x;
-}
 
 // Largest magnitudes are taken over the bits of |y| as integers: these order
 // finite numbers as the numbers do, infinity above them and every NaN above
