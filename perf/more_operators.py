@@ -30,7 +30,7 @@ SCALE = 1.0 / math.sqrt(192.0)        # softmax scale
 EPS = 1e-6
 MOST_POSITIONS = 65536                # rows of the table of angles
 
-TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
 
 
 def listed():
@@ -76,7 +76,7 @@ def draw(rng):
         k = 16 * _log(rng, 1, 640)
         m = _log(rng, 1, 8192)
         n = _log(rng, 1, min(16384, 4096 * 12288 * 5120 // (m * k)))
-        return {"op": op, "dtype": rng.choice(["bf16", "bf16", "f16", "f32"]), "m": m, "n": n, "k": k, "grouped": rng.random() < 0.7}
+        return {"op": op, "dtype": dtype, "m": m, "n": n, "k": k, "grouped": rng.random() < 0.7}
     if op == "rotate":
         dim = rng.choice([64, 128, 128, 192, 576, 8 * rng.randint(8, 72)])
         heads = rng.choice([1, 8, 16, 20, 32, 40, 64, 100, 128])
@@ -205,7 +205,7 @@ def run(state):
 def _run_own(s):
     import scoring_exact_top_amd as lib
     if s["op"] == "matmul":
-        return lib.matmul_e4m3(s["x"], s["x_scale"], s["w"], s["w_scale"], out=s["out"])
+        return lib.matmul_e4m3(s["x"], s["x_scale"], s["w"], s["w_scale"], dtype=s["out"].dtype, out=s["out"])
     if s["op"] == "rotate":
         if s["quant"]:
             return lib.norm_rotate_quant(s["x"], s["positions"], s["table"], s["rope_at"], interleaved=s["interleaved"], norm=s["norm"],
@@ -291,7 +291,7 @@ def work(case):
     if case["op"] == "matmul":
         M, N, K = case["m"], case["n"], case["k"]
         blocks = -(-K // BLOCK)
-        return {"bytes": (M + N) * K + 4 * (M * (blocks if case["grouped"] else 1) + -(-N // BLOCK) * blocks) + M * N * (4 if case["dtype"] == "f32" else 2),
+        return {"bytes": (M + N) * K + 4 * (M * (blocks if case["grouped"] else 1) + -(-N // BLOCK) * blocks) + 2 * M * N,
                 "flops": 2 * M * N * K}
     if case["op"] == "rotate":
         heads = case["tokens"] * case["heads"]
