@@ -362,9 +362,21 @@ int idx_topk_decode_paged_noalloc(const uint8_t *q, const float *q_scale, const 
 #define IDX_TOPK_VALUE 128  /* expanded form: per-head value width                      */
 #define IDX_TOPK_MAX_ATTN_HEADS 128
 #define IDX_TOPK_MAX_STEPS 16
+#define IDX_TOPK_MAX_NODES 64   /* drafted tokens of a sequence's tree */
 
 #define IDX_TOPK_BF16 0
 #define IDX_TOPK_F16 1
+
+/* Norms of idx_topk_norm_rotate and idx_topk_cache_append_rotary, over a row x of n numbers:
+ *   NONE   x
+ *   RMS    x / sqrt(mean(x^2) + eps) * weight + bias
+ *   LAYER  (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight + bias
+ * weight NULL: ones, bias NULL: zeros; both NULL and eps not looked at with NONE.  A row that is zero
+ * (after the mean's subtraction) with eps = 0 counts as normed.  A NaN or an infinity in a row, or
+ * squares that leave FP32, make its numbers NaN. */
+#define IDX_TOPK_NORM_NONE 0
+#define IDX_TOPK_NORM_RMS 1
+#define IDX_TOPK_NORM_LAYER 2
 
 /* Bytes of workspace idx_topk_latent_selected needs (0 for arguments it rejects). */
 size_t idx_topk_latent_selected_workspace(int32_t T, int32_t H, int32_t K);
@@ -420,6 +432,34 @@ int idx_topk_latent_paged(const void *q, int64_t q_seq, int64_t q_token, int64_t
                           int32_t max_pages, const int32_t *seq_lens, int32_t B, int32_t S, int32_t H,
                           float scale, int32_t dtype, void *out, float *lse, void *workspace,
                           size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace idx_topk_latent_tree needs (0 for arguments it rejects): at most 552 MiB,
+ * whatever the batch. */
+size_t idx_topk_latent_tree_workspace(int32_t B, int32_t S, int32_t H, int32_t max_pages);
+
+/*
+ * Latent attention of drafted tokens (absorbed form): sequence b has prefix_lens[b] committed keys
+ * and behind them, at positions prefix_lens[b] + i, the keys of counts[b] drafted tokens, the
+ * nodes of a tree.  Node j sees every committed key, and the key of node i where bit i of
+ * masks[b,j] is set: its ancestors' and its own bit, as a rule, but any mask is taken.
+ *   q           [B][S][H][576], strides q_seq, q_token, q_head;  S in 1..64, H in 1..128
+ *   cache, page_table as in idx_topk_latent_paged
+ *   prefix_lens [B] int32 (device) >= 0
+ *   counts      [B] int32 (device), 0..S, or NULL: S each.  A sequence whose lengths lie outside their
+ *               ranges or together pass max_pages * 64 is taken as one without nodes
+ *   masks       [B][S] uint64 (device, 8-byte aligned), sequence stride mask_seq numbers (0: one tree for
+ *               all); bits at counts[b] and above are not looked at
+ *   out         [B][S][H][512], lse [B][S][H] float or NULL
+ * Rows j >= counts[b] give o = 0 and lse = -inf, as do nodes that see no key; their q is not looked
+ * at.  Keys in pages outside [0, num_pages) are skipped; cache slots behind the last node may hold
+ * anything.  The rows of all nodes of a sequence must be finite, seen or not.
+ */
+int idx_topk_latent_tree(const void *q, int64_t q_seq, int64_t q_token, int64_t q_head,
+                         const void *cache, int32_t num_pages, const int32_t *page_table,
+                         int32_t max_pages, const int32_t *prefix_lens, const int32_t *counts,
+                         const uint64_t *masks, int64_t mask_seq, int32_t B, int32_t S, int32_t H,
+                         float scale, int32_t dtype, void *out, float *lse, void *workspace,
+                         size_t workspace_bytes, void *stream);
 
 /* Bytes of workspace idx_topk_latent_expanded needs (0 for arguments it rejects). */
 size_t idx_topk_latent_expanded_workspace(int32_t Tq, int32_t B, int32_t max_q, int32_t max_k, int32_t H);
@@ -490,6 +530,82 @@ int idx_topk_cache_append(const void *latents, int64_t latent_token, const void 
                           void *latent_cache, uint8_t *k_cache, float *k_scale, int64_t num_slots,
                           void *stream);
 
+/*
+ * Norm of every head of every token and rotation of 64 of its numbers by the token's position:
+ *   y = norm(x[t,h,:])   (IDX_TOPK_NORM_*, over the D numbers)
+ *   a, b = y[i], y[j]  become  a cos - b sin, b cos + a sin     for the 32 pairs of the rotary part
+ * The rotary part is the numbers rope_at .. rope_at + 64; pair p is its numbers 2p and 2p + 1
+ * (interleaved != 0) or p and p + 32 (0), and cos, sin are table[positions[t], p] and
+ * table[positions[t], 32 + p].  All arithmetic is FP32.  One of two outputs:
+ *   out       [T][H][D] in `dtype`, strides out_token, out_head (multiples of 8, heads apart); it may be
+ *             x itself with x's strides, and must not overlap x otherwise
+ *   codes     [T][H][D] uint8 with scales [T][H]: scale = max|y| / 448 (1 for an all-zero head),
+ *             codes = nearest e4m3fn of y / scale, as q and q_scale of idx_topk_prefill and
+ *             idx_topk_decode_paged.  A head with a NaN or an infinity gets NaN codes and scale 1.
+ *   x         [T][H][D], strides x_token, x_head; D 64..1024, a multiple of 8, as rope_at is
+ *   weight, bias  [D] in `dtype` or NULL
+ *   positions [T] int32 device.  A token whose position lies outside [0, table_rows) is padding: its
+ *             outputs are not written
+ *   table     [table_rows][64] float, 16-byte aligned: 32 cosines, then 32 sines
+ * codes 16-byte aligned.  T * H at most 2^31 - 1 (IDX_EUNSUPPORTED).  No workspace.
+ */
+int idx_topk_norm_rotate(const void *x, int64_t x_token, int64_t x_head, int32_t norm,
+                         const void *weight, const void *bias, float eps, const int32_t *positions,
+                         const float *table, int32_t table_rows, int32_t rope_at, int32_t interleaved,
+                         int32_t T, int32_t H, int32_t D, int32_t dtype, void *out, int64_t out_token,
+                         int64_t out_head, uint8_t *codes, float *scales, void *stream);
+
+/*
+ * idx_topk_cache_append of tokens that are not yet normed and rotated: for every token t with
+ * slots[t] in [0, num_slots) and positions[t] in [0, table_rows)
+ *   row = latents[t, 0:512] normed (latent_norm: NONE or RMS), latents[t, 512:576] rotated
+ *   latent_cache[slots[t],:] = row,   latents_out[t,:] = row
+ *   key = index_keys[t,:] normed, then its numbers key_rope_at .. key_rope_at + 64 rotated
+ *   k_scale[slots[t]], k_cache[slots[t],:] = scale and codes of key, as in idx_topk_cache_append
+ * Norms, pairs and table as in idx_topk_norm_rotate.  Between norm, rotation and the one rounding
+ * (to `dtype`, or to codes) everything is FP32.  Other tokens are not stored and their rows of
+ * latents_out not written.  The slots of one call must be distinct.
+ *   latents       [T][576] stride latent_token; with latent_cache NULL: not stored
+ *   latent_weight [512] in `dtype` or NULL
+ *   index_keys    [T][128] stride key_token; with k_cache and k_scale NULL: not stored
+ *   key_weight, key_bias  [128] in `dtype` or NULL;  key_rope_at 0..64, a multiple of 8
+ *   latents_out   NULL or [T][576] in `dtype`, 16-byte aligned: the finished rows for
+ *                 a prompt's own attention; may be `latents` itself where its stride is 576
+ */
+int idx_topk_cache_append_rotary(const void *latents, int64_t latent_token, int32_t latent_norm,
+                                 const void *latent_weight, float latent_eps, int32_t latent_interleaved,
+                                 const void *index_keys, int64_t key_token, int32_t key_norm,
+                                 const void *key_weight, const void *key_bias, float key_eps,
+                                 int32_t key_rope_at, int32_t key_interleaved, const int32_t *slots,
+                                 const int32_t *positions, const float *table, int32_t table_rows,
+                                 int32_t T, int32_t dtype, void *latent_cache, uint8_t *k_cache,
+                                 float *k_scale, int64_t num_slots, void *latents_out, void *stream);
+
+/* Bytes of workspace idx_topk_matmul_e4m3 needs (0 for arguments it rejects). */
+size_t idx_topk_matmul_e4m3_workspace(int32_t M, int32_t N, int32_t K);
+
+/*
+ * Product of e4m3 activations and weights with block scales:
+ *   out[m,n] = sum_b xs(m,b) * w_scale[n / 128, b] * sum_{k in block b} x[m,k] * w[n,k]
+ * over blocks of 128 columns k (the last may be shorter).  x and x_scale are what
+ * idx_topk_norm_quant writes: xs(m,b) = x_scale[m,b] with x_group 128, x_scale[m] with x_group 0.
+ *   x         [M][K] uint8 e4m3fn, row stride x_row (a multiple of 16, at most 2^24); K a multiple of 16
+ *   x_scale   [M][ceil(K / 128)] float, or [M]
+ *   w         [N][K] uint8 e4m3fn, contiguous;  w_scale [ceil(N / 128)][ceil(K / 128)] float
+ *   out       [M][N] in `dtype`, row stride out_row >= N
+ * x, w and out 16-byte aligned; K at most 2^24.  A block's sum is the matrix cores': FP32 over groups of
+ * eight neighbouring columns, in which each product is cut off 13 binary places below the leading
+ * one of the largest (measured; for random numbers 1.5e-5 of the result, a hundredth of
+ * bfloat16's rounding).  It is scaled and added to the others in FP32 and the result is rounded
+ * once; sums that leave the output's type are infinities.  NaN codes
+ * (those of idx_topk_norm_quant for a row with a NaN) make the outputs they enter NaN, and no others.
+ * The result does not depend on timing.
+ */
+int idx_topk_matmul_e4m3(const uint8_t *x, int64_t x_row, const float *x_scale, int32_t x_group,
+                         const uint8_t *w, const float *w_scale, int32_t M, int32_t N, int32_t K,
+                         int32_t dtype, void *out, int64_t out_row, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
 /* Copy the counters of the last call that used `workspace` into *out.
  * Synchronises `stream`.  For tests and diagnosis, not for hot loops. */
 int idx_topk_read_stats(const void *workspace, idx_topk_stats *out, void *stream);
@@ -508,8 +624,9 @@ const char *idx_topk_strerror(int code);
  *                                  be captured: IDX_EINVAL)
  *   ... any of idx_topk_prefill, _prefill_debug (no timing events),
  *       _prefill_unfused, _rows, _decode_paged, _scan_bf16, _stream_floor,
- *       _latent_selected, _latent_paged, _latent_expanded, _norm_quant,
- *       _cache_append on `stream`, in any number and order ...
+ *       _latent_selected, _latent_paged, _latent_tree, _latent_expanded,
+ *       _norm_quant, _norm_rotate, _cache_append, _cache_append_rotary,
+ *       _matmul_e4m3 on `stream`, in any number and order ...
  *   idx_topk_graph_end(stream, &g) stops recording and instantiates the graph;
  *                                  on failure (a capture that was invalidated,
  *                                  a call that failed) returns IDX_EHIP, *g =

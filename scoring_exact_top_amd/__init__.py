@@ -422,6 +422,21 @@ _lib.idx_topk_norm_quant.restype = ctypes.c_int
 _lib.idx_topk_norm_quant.argtypes = [_vp, _i64, _vp, _i64, _vp, _f32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp]
 _lib.idx_topk_cache_append.restype = ctypes.c_int
 _lib.idx_topk_cache_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i64, _vp]
+_lib.idx_topk_latent_tree_workspace.restype = _sz
+_lib.idx_topk_latent_tree_workspace.argtypes = [_i32, _i32, _i32, _i32]
+_lib.idx_topk_latent_tree.restype = ctypes.c_int
+_lib.idx_topk_latent_tree.argtypes = [_vp, _i64, _i64, _i64, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _f32,
+                                      _i32, _vp, _vp, _vp, _sz, _vp]
+_lib.idx_topk_norm_rotate.restype = ctypes.c_int
+_lib.idx_topk_norm_rotate.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _f32, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                      _vp, _i64, _i64, _vp, _vp, _vp]
+_lib.idx_topk_cache_append_rotary.restype = ctypes.c_int
+_lib.idx_topk_cache_append_rotary.argtypes = [_vp, _i64, _i32, _vp, _f32, _i32, _vp, _i64, _i32, _vp, _vp, _f32, _i32, _i32, _vp, _vp,
+                                              _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _vp]
+_lib.idx_topk_matmul_e4m3_workspace.restype = _sz
+_lib.idx_topk_matmul_e4m3_workspace.argtypes = [_i32, _i32, _i32]
+_lib.idx_topk_matmul_e4m3.restype = ctypes.c_int
+_lib.idx_topk_matmul_e4m3.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _sz, _vp]
 
 
 def latent_selected_workspace_bytes(T: int, H: int, K: int) -> int:
@@ -430,6 +445,14 @@ def latent_selected_workspace_bytes(T: int, H: int, K: int) -> int:
 
 def latent_paged_workspace_bytes(B: int, S: int, H: int, max_pages: int) -> int:
     return int(_lib.idx_topk_latent_paged_workspace(B, S, H, max_pages))
+
+
+def latent_tree_workspace_bytes(B: int, S: int, H: int, max_pages: int) -> int:
+    return int(_lib.idx_topk_latent_tree_workspace(B, S, H, max_pages))
+
+
+def matmul_e4m3_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(_lib.idx_topk_matmul_e4m3_workspace(M, N, K))
 
 
 def latent_expanded_workspace_bytes(Tq: int, B: int, max_q: int, max_k: int, H: int) -> int:
@@ -582,6 +605,39 @@ def latent_paged(q, cache, page_table, seq_lens, scale: float, out=None, lse=Non
     return out, lse
 
 
+def latent_tree(q, cache, page_table, prefix_lens, counts, masks, scale: float, out=None, lse=None, workspace=None, stream=None):
+    """Latent attention of drafted tokens that form a tree; see idx_topk_latent_tree.
+
+    q [B,S,H,576] (strided), cache [P,64,576], page_table [B,max_pages] int32,
+    prefix_lens [B] and counts [B] (or None: S each) int32, masks int64 [B,S] or
+    [S] (one tree for all sequences): bit i of a node's mask says whether it sees
+    node i.  Returns (out [B,S,H,512], lse [B,S,H] f32).
+    """
+    dt, dev, dtype = _dtype16(q), q.get_device(), q.dtype
+    if q.dim() != 4 or cache.dim() != 3 or cache.shape[1] != PAGE:
+        raise ValueError("expected q [B,S,H,576] and a cache [pages,64,576], got %s and %s" % (list(q.shape), list(cache.shape)))
+    B, S, H, _ = q.shape
+    if page_table.dim() != 2 or page_table.shape[0] != B or prefix_lens.shape != (B,) or (counts is not None and counts.shape != (B,)):
+        raise ValueError("expected page_table [%d, max_pages], prefix_lens [%d] and counts [%d]" % (B, B, B))
+    if masks.shape != (S,) and masks.shape != (B, S):
+        raise ValueError("expected masks [%d, %d] or [%d], got %s" % (B, S, S, list(masks.shape)))
+    max_pages = page_table.shape[1]
+    if (B | S | H | max_pages | cache.shape[0]) >> 31:
+        _int32(B | S | H | max_pages | cache.shape[0])
+    q_at = _rows_at(q, dtype, dev, (B, S, H, LATENT_ROW))
+    q_seq, q_token, q_head = _strides(q)
+    cache_at, num_slots = _cache_at(cache, LATENT_ROW, dtype, dev)
+    out, out_at = _out(out, (B, S, H, LATENT), dtype, dev, stream)
+    lse, lse_at = _out(lse, (B, S, H), torch.float32, dev, stream)
+    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_latent_tree_workspace(B, S, H, max_pages), dev, stream)
+    _check(_lib.idx_topk_latent_tree(q_at, q_seq, q_token, q_head, cache_at, num_slots // PAGE, _at(page_table, torch.int32, dev),
+                                     max_pages, _at(prefix_lens, torch.int32, dev),
+                                     None if counts is None else _at(counts, torch.int32, dev), _at(masks, torch.int64, dev),
+                                     S if masks.dim() == 2 else 0, B, S, H, scale, dt, out_at, lse_at, ws_at, ws_bytes,
+                                     _on(stream, dev)))
+    return out, lse
+
+
 def latent_expanded(q, kv, k_rope, cu_q, cu_k, max_q: int, max_k: int, scale: float, causal: bool = True, out=None,
                     lse=None, workspace=None, stream=None):
     """Causal attention over packed prompts with expanded keys and values; see
@@ -681,6 +737,165 @@ def cache_append(latents, index_keys, slots, latent_cache, k_cache, k_scale, str
             raise ValueError("the caches hold different numbers of slots: %s" % [num, n, k_scale.numel()])
     _check(_lib.idx_topk_cache_append(lat_at, lat_stride, key_at, key_stride, _at(slots, torch.int32, dev), T, dt, cache_at,
                                       kc_at, ks_at, n if num is None else num, _on(stream, dev)))
+
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def _norm(name: str) -> int:
+    code = NORMS.get(name)
+    if code is None:
+        raise ValueError("expected a norm of %s, got %r" % (sorted(NORMS), name))
+    return code
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype, dev):
+    """Address of a weight or bias [n], or None."""
+    if t is None:
+        return None
+    if t.shape != (n,):
+        raise ValueError("expected a weight or bias of shape [%d], got %s" % (n, list(t.shape)))
+    return _at(t, dtype, dev)
+
+
+def _angles(positions, table, T: int, dev):
+    """Addresses of the positions and the table of angles, and the table's rows."""
+    if positions.shape != (T,):
+        raise ValueError("expected positions of shape [%d], got %s" % (T, list(positions.shape)))
+    if table.dim() != 2 or table.shape[1] != ROPE:
+        raise ValueError("expected a table [positions,%d], got %s" % (ROPE, list(table.shape)))
+    if table.shape[0] >> 31:
+        _int32(table.shape[0])
+    return _at(positions, torch.int32, dev), _at(table, torch.float32, dev), table.shape[0]
+
+
+def _head_rows(x, rope_at: int):
+    """What norm_rotate and norm_rotate_quant take of x [T,H,D]."""
+    dt, dev, dtype = _dtype16(x), x.get_device(), x.dtype
+    if x.dim() != 3:
+        raise ValueError("expected x [T,H,D], got %s" % list(x.shape))
+    T, H, D = shape = x.shape
+    if (T | H | D | rope_at) >> 31:
+        _int32(T | H | D | rope_at)
+    return dt, dev, dtype, T, H, D, _rows_at(x, dtype, dev, shape), _strides(x)
+
+
+def norm_rotate(x, positions, table, rope_at: int, interleaved: bool = False, norm: str = "none", weight=None, bias=None,
+                eps: float = 1e-6, out=None, stream=None):
+    """Norm of each head and rotation of its numbers rope_at .. rope_at + 64; see
+    idx_topk_norm_rotate.
+
+    x [T,H,D] bf16 or f16 (strided), positions [T] int32 (outside the table:
+    padding, not written), table [P,64] f32 (32 cosines, 32 sines a
+    position), norm "none", "rms" or "layer" with weight and bias [D] or None.
+    Returns out [T,H,D]: a new tensor, or the caller's (strided; may be x).
+    """
+    dt, dev, dtype, T, H, D, x_at, x_strides = _head_rows(x, rope_at)
+    if out is None:
+        out = _empty((T, H, D), dtype, dev, stream)
+    out_at = _rows_at(out, dtype, dev, (T, H, D))
+    pos_at, table_at, P = _angles(positions, table, T, dev)
+    _check(_lib.idx_topk_norm_rotate(x_at, *x_strides, _norm(norm), _vector(weight, D, dtype, dev), _vector(bias, D, dtype, dev), eps,
+                                     pos_at, table_at, P, rope_at, 1 if interleaved else 0, T, H, D, dt, out_at, *_strides(out), None,
+                                     None, _on(stream, dev)))
+    return out
+
+
+def norm_rotate_quant(x, positions, table, rope_at: int, interleaved: bool = False, norm: str = "none", weight=None, bias=None,
+                      eps: float = 1e-6, codes=None, scales=None, stream=None):
+    """norm_rotate to e4m3 codes with one scale a head: the indexer's queries from
+    projected ones.  Returns (codes [T,H,D] float8_e4m3fn, scales [T,H] f32).
+    """
+    dt, dev, dtype, T, H, D, x_at, x_strides = _head_rows(x, rope_at)
+    codes, codes_at = _out(codes, (T, H, D), torch.float8_e4m3fn, dev, stream)
+    scales, scales_at = _out(scales, (T, H), torch.float32, dev, stream)
+    pos_at, table_at, P = _angles(positions, table, T, dev)
+    _check(_lib.idx_topk_norm_rotate(x_at, *x_strides, _norm(norm), _vector(weight, D, dtype, dev), _vector(bias, D, dtype, dev), eps,
+                                     pos_at, table_at, P, rope_at, 1 if interleaved else 0, T, H, D, dt, None, 0, 0, codes_at,
+                                     scales_at, _on(stream, dev)))
+    return codes, scales
+
+
+def cache_append_rotary(latents, index_keys, slots, positions, table, latent_cache, k_cache, k_scale, latent_norm: str = "rms",
+                        latent_weight=None, latent_eps: float = 1e-6, latent_interleaved: bool = True, key_norm: str = "layer",
+                        key_weight=None, key_bias=None, key_eps: float = 1e-6, key_rope_at: int = 0, key_interleaved: bool = False,
+                        latents_out=None, stream=None):
+    """Norm, rotate and store new tokens in the caches; see idx_topk_cache_append_rotary.
+
+    As cache_append, with positions [T] int32 and table [P,64] f32 as in
+    norm_rotate.  latents_out [T,576] (or None) also receives the finished
+    latent rows of the tokens that are stored.
+    """
+    one = latents if latents is not None else index_keys
+    if one is None:
+        raise ValueError("expected latents, index_keys or both")
+    dt, dev, dtype, T = _dtype16(one), one.get_device(), one.dtype, one.shape[0]
+    if (latents is None) != (latent_cache is None) or (index_keys is None) != (k_cache is None) or (k_cache is None) != (k_scale is None):
+        raise ValueError("latents come with latent_cache, index_keys with k_cache and k_scale")
+    if slots.shape != (T,):
+        raise ValueError("expected slots of shape [%d], got %s" % (T, list(slots.shape)))
+    if (T | key_rope_at) >> 31:
+        _int32(T | key_rope_at)
+    lat_at = cache_at = out_at = key_at = kc_at = ks_at = None
+    lat_stride = key_stride = 0
+    num = n = None
+    if latents is not None:
+        lat_at = _rows_at(latents, dtype, dev, (T, LATENT_ROW))
+        lat_stride, = _strides(latents)
+        cache_at, num = _cache_at(latent_cache, LATENT_ROW, dtype, dev)
+    if latents_out is not None:
+        _, out_at = _out(latents_out, (T, LATENT_ROW), dtype, dev, stream)
+    if index_keys is not None:
+        key_at = _rows_at(index_keys, dtype, dev, (T, DIM))
+        key_stride, = _strides(index_keys)
+        kc_at, n = _cache_at(k_cache, DIM, torch.float8_e4m3fn if k_cache.dtype == torch.float8_e4m3fn else torch.uint8, dev)
+        ks_at = _at(k_scale, torch.float32, dev)
+        if k_scale.numel() != n or (num is not None and num != n):
+            raise ValueError("the caches hold different numbers of slots: %s" % [num, n, k_scale.numel()])
+    pos_at, table_at, P = _angles(positions, table, T, dev)
+    _check(_lib.idx_topk_cache_append_rotary(lat_at, lat_stride, _norm(latent_norm), _vector(latent_weight, LATENT, dtype, dev), latent_eps,
+                                             1 if latent_interleaved else 0, key_at, key_stride, _norm(key_norm),
+                                             _vector(key_weight, DIM, dtype, dev), _vector(key_bias, DIM, dtype, dev), key_eps,
+                                             key_rope_at, 1 if key_interleaved else 0, _at(slots, torch.int32, dev), pos_at, table_at,
+                                             P, T, dt, cache_at, kc_at, ks_at, n if num is None else num, out_at, _on(stream, dev)))
+
+
+def matmul_e4m3(x, x_scale, w, w_scale, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+    """Product x @ w.T of e4m3 operands with block scales; see idx_topk_matmul_e4m3.
+
+    x [M,K] float8_e4m3fn or uint8 (strided rows) with x_scale [M,ceil(K/128)]
+    or [M,1] f32, as norm_quant returns them; w [N,K] with w_scale
+    [ceil(N/128),ceil(K/128)] f32.  Returns out [M,N] in `dtype` (bf16 or f16): a
+    new tensor, or the caller's (strided rows).
+    """
+    if not x.is_cuda:
+        raise ValueError("expected a device tensor")
+    dev = x.get_device()
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError("expected x [M,K] and w [N,K], got %s and %s" % (list(x.shape), list(w.shape)))
+    M, K = x.shape
+    N = w.shape[0]
+    if (M | N | K) >> 31:
+        _int32(M | N | K)
+    for t in (x, w):
+        if t.dtype != torch.float8_e4m3fn and t.dtype != torch.uint8:
+            raise ValueError("expected float8_e4m3fn or uint8, got %s" % t.dtype)
+    blocks = (K + 127) // 128
+    if x_scale.shape != (M, blocks) and x_scale.shape != (M, 1):
+        raise ValueError("expected x_scale [%d,%d] or [%d,1], got %s" % (M, blocks, M, list(x_scale.shape)))
+    if w_scale.shape != ((N + 127) // 128, blocks):
+        raise ValueError("expected w_scale [%d,%d], got %s" % ((N + 127) // 128, blocks, list(w_scale.shape)))
+    kind = _DTYPES.get(dtype)
+    if kind is None:
+        raise ValueError("expected an output of bfloat16 or float16, got %s" % dtype)
+    if out is None:
+        out = _empty((M, N), dtype, dev, stream)
+    x_at, out_at = _rows_at(x, x.dtype, dev, (M, K)), _rows_at(out, dtype, dev, (M, N))
+    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_matmul_e4m3_workspace(M, N, K), dev, stream)
+    _check(_lib.idx_topk_matmul_e4m3(x_at, *_strides(x), _at(x_scale, torch.float32, dev), 128 if x_scale.shape[1] == blocks else 0,
+                                     _at(w, w.dtype, dev), _at(w_scale, torch.float32, dev), M, N, K, kind, out_at, *_strides(out),
+                                     ws_at, ws_bytes, _on(stream, dev)))
+    return out
 
 
 NOALLOC_SCRATCH_BYTES = 16 << 20

@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["csrc/idx_api.hip", "csrc/idx_prefill.hip", "csrc/idx_decode.hip", "csrc/idx_rows.hip", "csrc/idx_scan.hip"]
 # sources whose masked places may hold NaN: compiled without -fno-honor-nans
-NAN_SOURCES = ["csrc/idx_latent.hip", "csrc/idx_expanded.hip", "csrc/idx_norm.hip"]
+NAN_SOURCES = ["csrc/idx_latent.hip", "csrc/idx_expanded.hip", "csrc/idx_norm.hip",
+               "csrc/idx_rotate.hip", "csrc/idx_matmul.hip"]
 LIB = os.path.join(HERE, "libidxtopk.so")
 
 HIPCC_FLAGS = [

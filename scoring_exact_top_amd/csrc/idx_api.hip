@@ -5,7 +5,9 @@
 #include "idx_internal.hpp"
 #include "idx_decode.hpp"
 #include "idx_latent.hpp"
+#include "idx_matmul.hpp"
 #include "idx_norm.hpp"
+#include "idx_rotate.hpp"
 #include "idx_rows.hpp"
 #include "idx_scan.hpp"
 
@@ -268,6 +270,20 @@ extern "C" int idx_topk_latent_paged(const void* q, int64_t q_seq, int64_t q_tok
                       dtype, out, lse, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
+extern "C" size_t idx_topk_latent_tree_workspace(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
+  return latent_tree_workspace_bytes(B, S, H, max_pages);
+}
+
+extern "C" int idx_topk_latent_tree(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, const void* cache,
+                                    int32_t num_pages, const int32_t* page_table, int32_t max_pages,
+                                    const int32_t* prefix_lens, const int32_t* counts, const uint64_t* masks,
+                                    int64_t mask_seq, int32_t B, int32_t S, int32_t H, float scale, int32_t dtype,
+                                    void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return latent_tree(q, q_seq, q_token, q_head, cache, num_pages, page_table, max_pages, prefix_lens, counts, masks,
+                     mask_seq, B, S, H, scale, dtype, out, lse, workspace, workspace_bytes,
+                     static_cast<hipStream_t>(stream));
+}
+
 extern "C" size_t idx_topk_latent_expanded_workspace(int32_t Tq, int32_t B, int32_t max_q, int32_t max_k, int32_t H) {
   return latent_expanded_workspace_bytes(Tq, B, max_q, max_k, H);
 }
@@ -296,6 +312,41 @@ extern "C" int idx_topk_cache_append(const void* latents, int64_t latent_token, 
                                      void* stream) {
   return cache_append(latents, latent_token, index_keys, key_token, slots, T, dtype, latent_cache, k_cache, k_scale,
                       num_slots, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int idx_topk_cache_append_rotary(const void* latents, int64_t latent_token, int32_t latent_norm,
+                                            const void* latent_weight, float latent_eps, int32_t latent_interleaved,
+                                            const void* index_keys, int64_t key_token, int32_t key_norm,
+                                            const void* key_weight, const void* key_bias, float key_eps,
+                                            int32_t key_rope_at, int32_t key_interleaved, const int32_t* slots,
+                                            const int32_t* positions, const float* table, int32_t table_rows, int32_t T,
+                                            int32_t dtype, void* latent_cache, uint8_t* k_cache, float* k_scale,
+                                            int64_t num_slots, void* latents_out, void* stream) {
+  return cache_append_rotary(latents, latent_token, latent_norm, latent_weight, latent_eps, latent_interleaved, index_keys,
+                             key_token, key_norm, key_weight, key_bias, key_eps, key_rope_at, key_interleaved, slots,
+                             positions, table, table_rows, T, dtype, latent_cache, k_cache, k_scale, num_slots,
+                             latents_out, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int idx_topk_norm_rotate(const void* x, int64_t x_token, int64_t x_head, int32_t norm, const void* weight,
+                                    const void* bias, float eps, const int32_t* positions, const float* table,
+                                    int32_t table_rows, int32_t rope_at, int32_t interleaved, int32_t T, int32_t H,
+                                    int32_t D, int32_t dtype, void* out, int64_t out_token, int64_t out_head,
+                                    uint8_t* codes, float* scales, void* stream) {
+  return norm_rotate(x, x_token, x_head, norm, weight, bias, eps, positions, table, table_rows, rope_at, interleaved, T, H,
+                     D, dtype, out, out_token, out_head, codes, scales, static_cast<hipStream_t>(stream));
+}
+
+extern "C" size_t idx_topk_matmul_e4m3_workspace(int32_t M, int32_t N, int32_t K) {
+  return matmul_e4m3_workspace_bytes(M, N, K);
+}
+
+extern "C" int idx_topk_matmul_e4m3(const uint8_t* x, int64_t x_row, const float* x_scale, int32_t x_group,
+                                    const uint8_t* w, const float* w_scale, int32_t M, int32_t N, int32_t K,
+                                    int32_t dtype, void* out, int64_t out_row, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  return matmul_e4m3(x, x_row, x_scale, x_group, w, w_scale, M, N, K, dtype, out, out_row, workspace, workspace_bytes,
+                     static_cast<hipStream_t>(stream));
 }
 
 extern "C" int idx_topk_read_stats(const void* workspace, idx_topk_stats* out, void* stream) {

@@ -3,8 +3,9 @@
 //
 //   x[h,i] = scale * q[h,:] . row_i[0:576],  o[h,:] = sum_i softmax_i(x[h,:]) row_i[0:512]
 //
-// over the rows that a list names (latent_selected: the indexer's output) or over all of a paged
-// sequence (latent_paged).  A key costs 2*(576+512) operations a head and 1152 bytes: with 64
+// over the rows that a list names (latent_selected: the indexer's output), over all of a paged
+// sequence (latent_paged), or over its committed part and a drafted token's ancestors
+// (latent_tree).  A key costs 2*(576+512) operations a head and 1152 bytes: with 64
 // heads 121 operations a byte, so that up to 128 heads a key's bytes cost more than its products
 // where they are read once (16 sequences of up to 65536 keys, 128 heads: 107 us of memory, 76 of
 // products), and less where thousands of tokens list the keys of one cache.
@@ -42,13 +43,19 @@ constexpr int kMaxList = IDX_TOPK_KMAX;
 constexpr int kPlanBatch = 1024;          // larger batches take one workgroup a sequence
 constexpr int kUnits = 256;               // compute units: one workgroup each
 
+// Which keys a call's rows see.
+enum { kListed, kPaged, kTree };
+
 struct LatArgs {
   const char* q;
   int64_t q_seq, q_token, q_head;  // in numbers
   const char* cache;
   int64_t num_slots;
   const int32_t* list;             // slots [B][K], or page ids [B][K]
-  const int32_t* lens;             // paged: [B]
+  const int32_t* lens;             // paged: [B]; tree: committed keys [B]
+  const int32_t* counts;           // tree: drafted tokens [B], NULL: S each
+  const uint64_t* masks;           // tree: [B or 1][S]
+  int64_t mask_seq;
   int32_t K, B, S, H;
   int32_t row_blocks;
   int32_t parts;                   // listed: workgroups a token's list is split over; paged: workgroups in all
@@ -91,16 +98,29 @@ __device__ __forceinline__ int wave_incl_scan(int x, int lane) {
   return x;
 }
 
+// Drafted tokens of a tree's sequence (0 for a sequence that is not one).
+__device__ __forceinline__ int tree_nodes(const LatArgs& A, int b) {
+  const int p = A.lens[b], n = A.counts ? A.counts[b] : A.S;
+  return p < 0 || n < 0 || n > A.S || (int64_t)p + n > (int64_t)A.K * IDX_TOPK_PAGE ? 0 : n;
+}
+
+// Keys of a sequence: of a tree's, committed and drafted (none without drafted tokens, which alone see them).
+template <int MODE>
 __device__ __forceinline__ int seq_len(const LatArgs& A, int b) {
+  if (MODE == kTree) {
+    const int n = tree_nodes(A, b);
+    return n ? A.lens[b] + n : 0;
+  }
   const int n = A.lens[b];
   return n < 0 || (int64_t)n > (int64_t)A.K * IDX_TOPK_PAGE ? 0 : n;
 }
 
+template <int MODE>
 __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   if (A.parts == A.B) return Part{wg, 0, 1, 0};
   int64_t total = 0;
   for (int b0 = 0; b0 < A.B; b0 += 64) {
-    const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    const int n = b0 + lane < A.B ? (seq_len<MODE>(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
     total += __shfl(wave_incl_scan(n, lane), 63, 64);
   }
   // sum of max(1, ceil(n / unit)) <= total / unit + B <= parts
@@ -108,7 +128,7 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   unit = unit < kMinPages ? kMinPages : unit;
   int base = 0;  // sums over the sequences before: parts, and 2^16 x parts with a cell (2^11 at most each)
   for (int b0 = 0; b0 < A.B; b0 += 64) {
-    const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    const int n = b0 + lane < A.B ? (seq_len<MODE>(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
     const int parts = b0 + lane < A.B ? max(1, (n + unit - 1) / unit) : 0;
     const int both = parts > 1 ? parts << 16 | parts : parts;
     const int end = base + wave_incl_scan(both, lane);
@@ -139,8 +159,9 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
 // wave a SIMD 4430 at a clock that power lowers from 1.64 to 1.61 GHz: 3% of
 // time, and only with the softmax spread over the products and every register
 // chosen by hand.
-template <class T, int HG, int KG, bool PAGED>
+template <class T, int HG, int KG, int MODE>
 __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(LatArgs A) {
+  constexpr bool PAGED = MODE != kListed;
   constexpr int kAhead = 5;      // LDS reads of operands run this many products ahead (as registers allow)
   constexpr int kRing = kBuffers / KG;           // tiles of a key group in LDS
   constexpr int kRows = kTileKeys / HG;          // rows of a tile that one wave loads
@@ -150,6 +171,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   __shared__ __attribute__((aligned(1024))) char s_tile[kBuffers * kTileBytes];
   __shared__ int32_t s_again;
   __shared__ int32_t s_list[PAGED ? 4 : kMaxList + kTileKeys];
+  __shared__ uint64_t s_mask[MODE == kTree ? HG * kRowsWave : 1];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hg = wave % HG, kg = wave / HG;
   const int g = lane >> 4, col = lane & 15;
@@ -162,7 +184,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   int len, tile0, tile1;  // keys of the sequence or list, this workgroup's tiles
   if (PAGED) {
     if (wave == 0) {
-      part = plan_part(A, wg, lane);
+      part = plan_part<MODE>(A, wg, lane);
       if (lane == 0) {
         s_list[0] = part.b; s_list[1] = part.part; s_list[2] = part.parts; s_list[3] = part.cell;
         if (A.parts > A.B && rb == 0 && part.b >= 0 && part.part == 0) A.plan[part.b] = make_int2(part.cell, part.parts);
@@ -173,7 +195,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     part.part = __builtin_amdgcn_readfirstlane(s_list[1]);
     part.parts = __builtin_amdgcn_readfirstlane(s_list[2]);
     if (part.b < 0) return;
-    len = __builtin_amdgcn_readfirstlane(seq_len(A, part.b));
+    len = __builtin_amdgcn_readfirstlane(seq_len<MODE>(A, part.b));
     const int pages = (len + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE;
     tile0 = 2 * (int)((int64_t)pages * part.part / part.parts);
     tile1 = min(2 * (int)((int64_t)pages * (part.part + 1) / part.parts), (len + kTileKeys - 1) / kTileKeys);
@@ -188,8 +210,20 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   const int row = (rb * HG + hg) * kRowsWave + col;
   const bool have = row < A.S * A.H;
   const int step = have ? row / A.H : 0, head = have ? row % A.H : 0;
-  int limit = PAGED ? len - A.S + 1 + step : len;  // this lane's row sees keys below
-  const int limit_min = PAGED ? len - A.S + 1 : len;     // every row does
+  int limit = MODE == kPaged ? len - A.S + 1 + step : len;  // this lane's row sees keys below
+  int limit_min = MODE == kPaged ? len - A.S + 1 : len;     // every row does
+  bool none = false;  // tree: this lane's row is no drafted token's, whatever it computes
+  if (MODE == kTree) {
+    const int nodes = __builtin_amdgcn_readfirstlane(tree_nodes(A, b));
+    limit_min = len - nodes;
+    none = step >= nodes;
+    // a row's mask, its bits behind the last drafted token cleared
+    if (tid < HG * kRowsWave) {
+      const int r = rb * HG * kRowsWave + tid, node = r < A.S * A.H ? r / A.H : A.S;
+      s_mask[tid] = node < nodes ? A.masks[b * A.mask_seq + node] & (~0ull >> (64 - nodes)) : 0;
+    }
+    if (rb * HG * kRowsWave >= nodes * A.H) tile1 = tile0;  // no row of this workgroup is one
+  }
 
   // The first memory the wave waits for: this range's slots (-1 for what is not
   // to be read) go to LDS behind q's loads, which are under way meanwhile.
@@ -201,7 +235,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   int slot = PAGED ? -1 : listed(tid);
   typename T::v8 q[kSteps];  // a row past the last repeats the first: its results are dropped
   {
-    const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + step * A.q_token +
+    const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + (MODE == kTree && none ? 0 : step) * A.q_token +
                                 head * A.q_head + 8 * g;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 32 * s);
@@ -364,7 +398,14 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     const int key0 = (mine + i * KG) * kTileKeys;
     if (live[0] != ~0u || key0 + kTileKeys > limit_min) {
       const int g4 = own_lane() >> 4 << 2;
-      const uint32_t live_g = live[0] >> g4;
+      uint32_t live_g = live[0] >> g4;
+      if (MODE == kTree) {
+        // keys of the tile that the row sees: committed ones, then those of its mask
+        const int past = limit_min - key0;  // committed keys from here on, below 32 where there are drafted ones
+        const uint64_t m = s_mask[hg * kRowsWave + (own_lane() & 15)];
+        const uint64_t seen = past >= kTileKeys ? ~0ull : past >= 0 ? m << past | ((1ull << past) - 1) : m >> min(-past, 63);
+        live_g &= (uint32_t)seen >> g4;
+      }
       const int limit_g = limit - key0 - g4;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
@@ -458,6 +499,12 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     load_first();
   }
   float l = sum_quarters(st.l), m = st.m;
+  if (MODE == kTree && none) {
+    l = 0.f;
+    m = -INFINITY;
+#pragma unroll
+    for (int d = 0; d < kCols; ++d) o[d] = w4f{};
+  }
 
   // Key groups are joined through LDS (nothing is in flight there any more): each hands the other m, l and
   // half of o', 16 bytes a lane at a time, and goes on with its own half of the columns.
@@ -673,24 +720,24 @@ static LatGeom paged_geom(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
   return layout(g, g.cells ? B : 0);
 }
 
-template <class T, bool PAGED>
+template <class T, int MODE>
 static int launch(LatArgs A, const LatGeom& g, char* ws, hipStream_t stream) {
   A.row_blocks = g.row_blocks;
   A.parts = g.parts;
   A.part_o = reinterpret_cast<float*>(ws + g.o);
   A.part_ml = reinterpret_cast<float2*>(ws + g.ml);
   A.plan = reinterpret_cast<int2*>(ws + g.plan);
-  const int64_t grid = (int64_t)(PAGED ? 1 : A.B) * g.parts * g.row_blocks;
+  const int64_t grid = (int64_t)(MODE != kListed ? 1 : A.B) * g.parts * g.row_blocks;
   const int64_t join = (int64_t)A.B * g.row_blocks * g.hg * kCols;
   // a launch dimension takes fewer than 2^32 threads (a larger one wraps, without an error)
   const int64_t threads = 64 * (g.hg == 8 ? 8 : 2 * g.hg);
   if (grid * threads > 0xffffffffLL || (g.cells && join * 256 > 0xffffffffLL)) return IDX_EUNSUPPORTED;
   const dim3 n((uint32_t)grid);
-  if (g.hg == 1) k_latent<T, 1, 2, PAGED><<<n, dim3(128), 0, stream>>>(A);
-  else if (g.hg == 2) k_latent<T, 2, 2, PAGED><<<n, dim3(256), 0, stream>>>(A);
-  else if (g.hg == 4) k_latent<T, 4, 2, PAGED><<<n, dim3(512), 0, stream>>>(A);
-  else k_latent<T, 8, 1, PAGED><<<n, dim3(512), 0, stream>>>(A);
-  if (g.cells) k_latent_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, g.hg, PAGED);
+  if (g.hg == 1) k_latent<T, 1, 2, MODE><<<n, dim3(128), 0, stream>>>(A);
+  else if (g.hg == 2) k_latent<T, 2, 2, MODE><<<n, dim3(256), 0, stream>>>(A);
+  else if (g.hg == 4) k_latent<T, 4, 2, MODE><<<n, dim3(512), 0, stream>>>(A);
+  else k_latent<T, 8, 1, MODE><<<n, dim3(512), 0, stream>>>(A);
+  if (g.cells) k_latent_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, g.hg, MODE != kListed);
   return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
 
@@ -723,9 +770,9 @@ int latent_selected(const void* q, int64_t q_token, int64_t q_head, const void* 
   if (!workspace || workspace_bytes < g.total) return IDX_EWORKSPACE;
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   LatArgs A{static_cast<const char*>(q), q_token, 0, q_head, static_cast<const char*>(cache), num_slots, slots,
-            nullptr, K, T, 1, H, 0, 0, scale * kLog2e, static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
+            nullptr, nullptr, nullptr, 0, K, T, 1, H, 0, 0, scale * kLog2e, static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
   char* const ws = static_cast<char*>(workspace);
-  return dtype == IDX_TOPK_BF16 ? launch<TBf16, false>(A, g, ws, stream) : launch<TF16, false>(A, g, ws, stream);
+  return dtype == IDX_TOPK_BF16 ? launch<TBf16, kListed>(A, g, ws, stream) : launch<TF16, kListed>(A, g, ws, stream);
 }
 
 size_t latent_paged_workspace_bytes(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
@@ -748,10 +795,38 @@ int latent_paged(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, 
   if (!workspace || workspace_bytes < g.total) return IDX_EWORKSPACE;
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   LatArgs A{static_cast<const char*>(q), q_seq, q_token, q_head, static_cast<const char*>(cache),
-            (int64_t)num_pages * IDX_TOPK_PAGE, page_table, seq_lens, max_pages, B, S, H, 0, 0, scale * kLog2e,
+            (int64_t)num_pages * IDX_TOPK_PAGE, page_table, seq_lens, nullptr, nullptr, 0, max_pages, B, S, H, 0, 0, scale * kLog2e,
             static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
   char* const ws = static_cast<char*>(workspace);
-  return dtype == IDX_TOPK_BF16 ? launch<TBf16, true>(A, g, ws, stream) : launch<TF16, true>(A, g, ws, stream);
+  return dtype == IDX_TOPK_BF16 ? launch<TBf16, kPaged>(A, g, ws, stream) : launch<TF16, kPaged>(A, g, ws, stream);
+}
+
+size_t latent_tree_workspace_bytes(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
+  if (B < 0 || S < 1 || S > IDX_TOPK_MAX_NODES || H < 1 || H > kMaxHeads || max_pages < 0) return 0;
+  return paged_geom(B, S, H, max_pages).total;
+}
+
+int latent_tree(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, const void* cache, int32_t num_pages,
+                const int32_t* page_table, int32_t max_pages, const int32_t* prefix_lens, const int32_t* counts,
+                const uint64_t* masks, int64_t mask_seq, int32_t B, int32_t S, int32_t H, float scale, int32_t dtype,
+                void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (S < 1 || S > IDX_TOPK_MAX_NODES || max_pages < 0 || num_pages < 0 || bad_stride(q_seq) || bad_stride(q_token) ||
+      bad_stride(q_head) || mask_seq < 0)
+    return IDX_EINVAL;
+  if (max_pages > 0x7fffffff / IDX_TOPK_PAGE) return IDX_EUNSUPPORTED;
+  const int rc = check_common(q, cache, page_table, B, H, scale, dtype, out, lse);
+  if (rc != IDX_OK || B == 0) return rc;
+  if (!prefix_lens || !aligned4(prefix_lens) || !aligned4(counts) || !masks || ((uintptr_t)masks & 7u) != 0 ||
+      (!page_table && max_pages > 0) || (!cache && num_pages > 0))
+    return IDX_EINVAL;
+  const LatGeom g = paged_geom(B, S, H, max_pages);
+  if (!workspace || workspace_bytes < g.total) return IDX_EWORKSPACE;
+  if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
+  LatArgs A{static_cast<const char*>(q), q_seq, q_token, q_head, static_cast<const char*>(cache),
+            (int64_t)num_pages * IDX_TOPK_PAGE, page_table, prefix_lens, counts, masks, mask_seq, max_pages, B, S, H, 0, 0,
+            scale * kLog2e, static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
+  char* const ws = static_cast<char*>(workspace);
+  return dtype == IDX_TOPK_BF16 ? launch<TBf16, kTree>(A, g, ws, stream) : launch<TF16, kTree>(A, g, ws, stream);
 }
 
 }  // namespace idxk

@@ -27,6 +27,12 @@ int latent_paged(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, 
                  int32_t S, int32_t H, float scale, int32_t dtype, void* out, float* lse, void* workspace,
                  size_t workspace_bytes, hipStream_t stream);
 
+size_t latent_tree_workspace_bytes(int32_t B, int32_t S, int32_t H, int32_t max_pages);
+int latent_tree(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, const void* cache, int32_t num_pages,
+                const int32_t* page_table, int32_t max_pages, const int32_t* prefix_lens, const int32_t* counts,
+                const uint64_t* masks, int64_t mask_seq, int32_t B, int32_t S, int32_t H, float scale, int32_t dtype,
+                void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 size_t latent_expanded_workspace_bytes(int32_t Tq, int32_t B, int32_t max_q, int32_t max_k, int32_t H);
 int latent_expanded(const void* q, int64_t q_token, int64_t q_head, const void* kv, int64_t kv_token,
                     int64_t kv_head, const void* k_rope, int64_t rope_token, const int32_t* cu_q,

@@ -1,0 +1,191 @@
+"""Latent attention of drafted trees on MI355X against its definition in 64 bits
+(bounds in attn_util.py)."""
+import math
+
+import pytest
+import torch
+
+from attn_util import attend, check_row
+from gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 1 / math.sqrt(192)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    import scoring_exact_top_amd  # noqa: F401
+
+
+def _signed(m):
+    """A 64-bit mask as the int64 that holds its bits."""
+    return m - (1 << 64) if m >> 63 else m
+
+
+def _tree(S, g):
+    """A node's ancestors and itself: parents are earlier nodes, or none."""
+    masks = []
+    for j in range(S):
+        parent = int(torch.randint(-1, j, (1,), generator=g)) if j else -1
+        masks.append((masks[parent] if parent >= 0 else 0) | 1 << j)
+    return masks
+
+
+def _case(prefix, counts, S, H, dtype, seed, masks=None):
+    g = torch.Generator().manual_seed(seed)
+    B = len(prefix)
+    pages = [-(-(p + n) // 64) for p, n in zip(prefix, counts)]
+    most = max(max(pages), 1)
+    P = sum(pages) + 2
+    cache = torch.randn(P, 64, 576, generator=g).to(dtype)
+    perm = torch.randperm(P, generator=g)
+    table = torch.full((B, most), -1, dtype=torch.int32)
+    at = 0
+    for b in range(B):
+        table[b, :pages[b]] = perm[at:at + pages[b]].int()
+        at += pages[b]
+    q = torch.randn(B, S, H, 576, generator=g).to(dtype)
+    masks = masks if masks is not None else [_tree(S, g) for _ in range(B)]
+    return q, cache, table, masks
+
+
+def _call(q, cache, table, prefix, counts, masks, **k):
+    import scoring_exact_top_amd as lib
+    i32 = lambda n: torch.tensor(n, dtype=torch.int32).cuda()  # noqa: E731
+    m = torch.tensor([[_signed(v) for v in row] for row in masks]).cuda()
+    return lib.latent_tree(q.cuda(), cache.cuda(), table.cuda(), i32(prefix), None if counts is None else i32(counts), m, SCALE, **k)
+
+
+def _check(out, lse, q, cache, table, prefix, counts, masks, nodes=None, where=""):
+    B, S, H, _ = q.shape
+    out, lse = out.cpu(), lse.cpu()
+    for b in range(B):
+        p, n = prefix[b], counts[b]
+        slots = [int(table[b, i // 64]) * 64 + i % 64 for i in range(p + n)]
+        rows = cache.view(-1, 576)[torch.tensor(slots, dtype=torch.long)].double()
+        for j in range(S) if nodes is None else nodes:
+            if j >= n:
+                assert (out[b, j] == 0).all() and (lse[b, j] == -math.inf).all(), "%s: padding %d,%d" % (where, b, j)
+                continue
+            seen = list(range(p)) + [p + i for i in range(n) if masks[b][j] >> i & 1]
+            k = rows[seen]
+            for h in {0, H // 2, H - 1}:
+                check_row(out[b, j, h], lse[b, j, h], attend(q[b, j, h].double(), k, k[:, :512], SCALE), len(seen), q.dtype,
+                          "%s: sequence %d node %d head %d" % (where, b, j, h))
+
+
+CASES = [
+    # prefix, counts, S, H
+    ([0], [1], 1, 1),
+    ([5], [3], 3, 4),
+    ([63, 64, 65, 0], [2, 5, 1, 5], 5, 16),
+    ([31, 32, 33, 127, 1], [7, 7, 7, 7, 7], 7, 20),
+    ([700, 0, 12], [64, 64, 40], 64, 3),
+    ([200, 90], [33, 63], 64, 16),
+    ([1000, 3, 450], [0, 17, 32], 33, 33),
+    ([2000], [12], 12, 128),
+    ([3000, 100, 900, 64], [16, 0, 9, 1], 16, 64),
+    ([40, 500], [64, 50], 64, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", range(len(CASES)))
+def test_tree(n, dtype):
+    """Ragged trees at every offset in a tile, sequences without a draft or without committed keys, rows by the
+    thousand, one to 64 nodes."""
+    prefix, counts, S, H = CASES[n]
+    log("tree", prefix, counts, S, H, dtype)
+    q, cache, table, masks = _case(prefix, counts, S, H, dtype, n)
+    out, lse = _call(q, cache, table, prefix, counts, masks)
+    _check(out, lse, q, cache, table, prefix, counts, masks, where="case %d" % n)
+
+
+def test_tree_any_mask():
+    """Masks that are no tree's: none (committed keys only, or nothing at all), all, a later node, bits behind the count."""
+    S, H = 6, 5
+    masks = [0, (1 << 64) - 1, 1 << 5, 0b101010, 1 << 63, 0b11]
+    prefix, counts = [70, 0, 30], [6, 6, 4]
+    q, cache, table, _ = _case(prefix, counts, S, H, torch.bfloat16, 3)
+    for form in ([masks] * 3, masks):
+        if form is masks:                                   # one tree for all sequences
+            import scoring_exact_top_amd as lib
+            i32 = lambda n: torch.tensor(n, dtype=torch.int32).cuda()  # noqa: E731
+            out, lse = lib.latent_tree(q.cuda(), cache.cuda(), table.cuda(), i32(prefix), i32(counts),
+                                       torch.tensor([_signed(v) for v in masks]).cuda(), SCALE)
+        else:
+            out, lse = _call(q, cache, table, prefix, counts, form)
+        _check(out, lse, q, cache, table, prefix, counts, [masks] * 3, where="any")
+    assert (out[1, 0] == 0).all() and (lse[1, 0] == -math.inf).all()
+
+
+def test_tree_chain_is_paged():
+    """A chain of drafted tokens: latent_paged's result for the same tokens, bit for bit."""
+    import scoring_exact_top_amd as lib
+    for S, H, prefix in ((4, 20, [1000, 37, 0]), (1, 128, [5000, 64, 1]), (16, 64, [300, 1200, 2])):
+        q, cache, table, _ = _case(prefix, [S] * 3, S, H, torch.bfloat16, S)
+        chain = [[(2 << j) - 1 for j in range(S)]] * 3
+        a = _call(q, cache, table, prefix, None, chain)
+        lens = torch.tensor([p + S for p in prefix], dtype=torch.int32).cuda()
+        b = lib.latent_paged(q.cuda(), cache.cuda(), table.cuda(), lens, SCALE)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), (S, H)
+
+
+def test_tree_ignores_what_is_not_there():
+    """Slots behind the last node, queries of padding rows and table entries past a sequence may hold anything;
+    pages outside the cache are skipped; bad lengths are sequences without nodes."""
+    S, H = 5, 16
+    prefix, counts = [100, 40, 64, 10, 10, 10, 10], [3, 5, 0, 5, 5, 5, 5]
+    q, cache, table, masks = _case(prefix, counts, S, H, torch.bfloat16, 4)
+    want, want_lse = _call(q, cache, table, prefix, counts, masks)
+    for b in range(2):
+        end = prefix[b] + counts[b]
+        cache[table[b, end // 64].item(), end % 64:] = float("nan")
+    q[0, 3:] = float("nan")
+    q[2] = float("inf")
+    bad_prefix, bad_counts = list(prefix), list(counts)
+    bad_prefix[3], bad_counts[4], bad_counts[5], bad_prefix[6] = -1, 6, -1, 2 ** 31 - 1
+    out, lse = _call(q, cache, table, bad_prefix, bad_counts, masks)
+    assert torch.equal(out[:3], want[:3]) and torch.equal(lse[:3], want_lse[:3])
+    assert (out[3:] == 0).all() and (lse[3:] == -math.inf).all()
+    gone = table.clone()
+    gone[0, 0], gone[1, 0] = cache.shape[0], -5             # the first page of each: 64 committed keys, all of the second's
+    out, lse = _call(q, cache, gone, prefix, counts, masks)
+    o, l = out.cpu(), lse.cpu()
+    rows = cache[table[0, 1].item()].double()
+    for j in range(3):
+        seen = list(range(100 - 64)) + [100 - 64 + i for i in range(3) if masks[0][j] >> i & 1]
+        check_row(o[0, j, 1], l[0, j, 1], attend(q[0, j, 1].double(), rows[seen], rows[seen][:, :512], SCALE), len(seen), q.dtype, "page gone")
+    assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+
+
+def test_tree_peaked_rows():
+    """Logits that climb far along the keys, so that workgroups walk them again; half precision as well."""
+    prefix, counts, S, H = [900], [9], 9, 16
+    for dtype in (torch.bfloat16, torch.float16):
+        q, cache, table, masks = _case(prefix, counts, S, H, dtype, 6)
+        q *= 8
+        slots = [int(table[0, i // 64]) * 64 + i % 64 for i in range(909)]
+        cache.view(-1, 576)[torch.tensor(slots)] *= torch.linspace(0.1, 1.5, 909)[:, None].to(dtype)
+        out, lse = _call(q, cache, table, prefix, counts, masks)
+        _check(out, lse, q, cache, table, prefix, counts, masks, where="peaked")
+
+
+def test_tree_views_streams_and_given_buffers():
+    import scoring_exact_top_amd as lib
+    prefix, counts, S, H = [300, 7], [6, 4], 6, 20
+    q, cache, table, masks = _case(prefix, counts, S, H, torch.bfloat16, 7)
+    want, want_lse = _call(q, cache, table, prefix, counts, masks)
+    wide = torch.randn(2, S, H + 2, 640).to(torch.bfloat16)
+    wide[:, :, 1:1 + H, 64:] = q
+    need = lib.latent_tree_workspace_bytes(2, S, H, table.shape[1])
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # NaN patterns in the partial results
+    out, lse = torch.empty(2, S, H, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(2, S, H, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = _call(wide.cuda()[:, :, 1:1 + H, 64:], cache, table, prefix, counts, masks, out=out, lse=lse, workspace=ws, stream=s)
+    s.synchronize()
+    assert got[0] is out and got[1] is lse and torch.equal(out, want) and torch.equal(lse, want_lse)
