@@ -433,7 +433,7 @@ int idx_topk_latent_paged(const void *q, int64_t q_seq, int64_t q_token, int64_t
                           float scale, int32_t dtype, void *out, float *lse, void *workspace,
                           size_t workspace_bytes, void *stream);
 
-/* Bytes of workspace idx_topk_latent_tree needs (0 for arguments it rejects): at most 552 MiB,
+/* Bytes of workspace idx_topk_latent_tree needs (0 for arguments it rejects): at most 132 MiB,
  * whatever the batch. */
 size_t idx_topk_latent_tree_workspace(int32_t B, int32_t S, int32_t H, int32_t max_pages);
 

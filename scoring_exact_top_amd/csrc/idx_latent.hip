@@ -42,6 +42,7 @@ constexpr int kBuffers = 4;               // tiles in LDS: 144 of the 160 KiB
 constexpr int kMaxList = IDX_TOPK_KMAX;
 constexpr int kPlanBatch = 1024;          // larger batches take one workgroup a sequence
 constexpr int kUnits = 256;               // compute units: one workgroup each
+static_assert(kUnits % 64 == 0, "");
 
 // Which keys a call's rows see.
 enum { kListed, kPaged, kTree };
@@ -58,13 +59,16 @@ struct LatArgs {
   int64_t mask_seq;
   int32_t K, B, S, H;
   int32_t row_blocks;
-  int32_t parts;                   // listed: workgroups a token's list is split over; paged: workgroups in all
+  int32_t parts;                   // listed: workgroups a token's list is split over; paged: workgroups in all;
+                                   // tree: workgroups that share the work, 0: one for each block of rows
   float c;                         // scale * log2(e)
   char* out;
   float* lse;
   float* part_o;                   // [(cell * row_blocks + block) * HG + group] 16 rows x 512 columns
   float2* part_ml;                 // ... of 16 rows
   int2* plan;                      // paged: [B] first cell and number of parts
+  int4* split;                     // tree: for each workgroup the block that begins in its work and goes on in
+                                   // other ones': sequence, block, number of parts (0: none), nodes
 };
 
 // A row of zeros for keys that a tile does not have: they are masked, and
@@ -115,12 +119,11 @@ __device__ __forceinline__ int seq_len(const LatArgs& A, int b) {
   return n < 0 || (int64_t)n > (int64_t)A.K * IDX_TOPK_PAGE ? 0 : n;
 }
 
-template <int MODE>
 __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   if (A.parts == A.B) return Part{wg, 0, 1, 0};
   int64_t total = 0;
   for (int b0 = 0; b0 < A.B; b0 += 64) {
-    const int n = b0 + lane < A.B ? (seq_len<MODE>(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    const int n = b0 + lane < A.B ? (seq_len<kPaged>(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
     total += __shfl(wave_incl_scan(n, lane), 63, 64);
   }
   // sum of max(1, ceil(n / unit)) <= total / unit + B <= parts
@@ -128,7 +131,7 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   unit = unit < kMinPages ? kMinPages : unit;
   int base = 0;  // sums over the sequences before: parts, and 2^16 x parts with a cell (2^11 at most each)
   for (int b0 = 0; b0 < A.B; b0 += 64) {
-    const int n = b0 + lane < A.B ? (seq_len<MODE>(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    const int n = b0 + lane < A.B ? (seq_len<kPaged>(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
     const int parts = b0 + lane < A.B ? max(1, (n + unit - 1) / unit) : 0;
     const int both = parts > 1 ? parts << 16 | parts : parts;
     const int end = base + wave_incl_scan(both, lane);
@@ -142,6 +145,119 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
     base = __shfl(end, 63, 64);
   }
   return Part{-1, 0, 0, 0};  // a spare workgroup
+}
+
+// A tree call's work is one page for one block of rows after another: the pages of a sequence's first
+// block, then those of its next, and so on through the sequences.  Few blocks are cut into equal parts of
+// at most `unit` pages, one a workgroup.  Where that would leave the longest part far above the mean (many
+// blocks of ragged trees and lengths), workgroup i takes the pages total * i / shares and on, whatever
+// sequences and blocks they are of: 20 nodes x 128 heads on 16 sequences to 32768 keys take 740 us instead of
+// 1360 with a part a workgroup.  Beginning a block costs a workgroup about kBegin pages (q, the first
+// tiles, what is written for the join).  A block that several workgroups share is joined from their partial
+// results: the first's (workgroup i) is cell 2 i + 1, those of the following ones j cells 2 j.
+constexpr int kBegin = 3;
+
+struct TreeSeq {
+  int nodes, pages, blocks;
+  __device__ __forceinline__ TreeSeq(const LatArgs& A, int b, int rows) {
+    nodes = b < A.B ? tree_nodes(A, b) : 0;
+    pages = nodes ? (A.lens[b] + nodes + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    blocks = (nodes * A.H + rows - 1) / rows;
+  }
+};
+
+// a / b of numbers that are not negative.  Those past 32 bits are below 2^53, and so is b * (a / b): the quotient
+// in FP64 cannot round up to a whole number then (it is 1 / b below one at least), and is a tenth of a 64-bit
+// division's instructions.
+__device__ __forceinline__ int32_t quotient(int32_t a, int32_t b) { return (int32_t)((uint32_t)a / (uint32_t)b); }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) { return (int64_t)((double)a / (double)b); }
+
+// Where a workgroup begins and how far it goes.  parts > 0: of so many parts of the block, all with one workgroup
+// each; else its share of the stream ends at page `end` of `total` over `shares`.
+struct TreeStart {
+  int b, block, first, parts;
+  int64_t pages, end, total;
+  int shares, wg;
+};
+
+template <class N>
+__device__ __forceinline__ N wave_sum_before(N x, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const N y = __shfl_up((std::conditional_t<sizeof(N) == 8, long long, int>)x, d, 64);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// N: 32 bits where the work is below 2^22 pages (a plan takes a workgroup 2 us then, in 64 bits 5).
+template <int HG, class N>
+__device__ __forceinline__ TreeStart plan_tree_in(const LatArgs& A, int wg, int lane, N total, N blocks) {
+  TreeStart at{-1, 0, 0, 0, 0, 0, (int64_t)total, 1, wg};
+  const N shares = A.parts;
+  // sum of ceil(pages / unit) <= total / unit + blocks <= parts
+  N unit = blocks < shares ? quotient(total + shares - blocks - 1, shares - blocks) : total + kBegin + 1;
+  const bool cut = unit <= quotient(total, shares) + kBegin;
+  unit = unit < kMinPages ? kMinPages : unit;
+  N from = wg;
+  if (!cut) {
+    const N most = (total + kMinPages - 1) / kMinPages, n = most < 1 ? 1 : most < shares ? most : shares;
+    at.shares = (int)n;
+    from = wg < n ? quotient(total * wg, n) : total;
+    at.end = wg < n ? quotient(total * (wg + 1), n) : total;
+    at.pages = at.end - from;
+  }
+  N base = 0;
+#pragma nounroll
+  for (int b0 = 0; b0 < A.B; b0 += 64) {
+    const TreeSeq t(A, b0 + lane, 16 * HG);
+    const N parts = cut ? quotient((N)t.pages + unit - 1, unit) : t.pages;
+    const N w = (N)t.blocks * parts, end = base + wave_sum_before(w, lane), begin = end - w;
+    const uint64_t found = __ballot(from >= begin && from < end);
+    if (found) {
+      const int l = __ffsll((unsigned long long)found) - 1;
+      const auto of = [&](N x) { return (N)__shfl((std::conditional_t<sizeof(N) == 8, long long, int>)x, l, 64); };
+      const N into = from - of(begin), n = of(parts), pages = of(t.pages), block = quotient(into, n), part = into - block * n;
+      at.b = b0 + l;
+      at.block = (int)block;
+      at.first = (int)part;
+      if (cut) {
+        const N first = quotient(pages * part, n);
+        at.first = (int)first;
+        at.pages = quotient(pages * (part + 1), n) - first;
+        at.parts = (int)n;
+      }
+      break;
+    }
+    base = (N)__shfl((std::conditional_t<sizeof(N) == 8, long long, int>)end, 63, 64);
+  }
+  return at;
+}
+
+template <int HG>
+__device__ __forceinline__ TreeStart plan_tree(const LatArgs& A, int wg, int lane) {
+  int64_t total = 0;
+  int blocks = 0;
+#pragma nounroll
+  for (int b0 = 0; b0 < A.B; b0 += 64) {
+    const TreeSeq t(A, b0 + lane, 16 * HG);
+    int64_t w = (int64_t)t.blocks * t.pages;
+    int n = t.blocks;
+    if (A.B == 1) {
+      w = __shfl((long long)w, 0, 64);
+      n = __shfl(n, 0, 64);
+    } else {
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) {
+        w += __shfl_xor((long long)w, d, 64);
+        n += __shfl_xor(n, d, 64);
+      }
+    }
+    total += w;
+    blocks += n;
+  }
+  if (total < 1 << 22) return plan_tree_in<HG, int32_t>(A, wg, lane, (int32_t)total, blocks);
+  return plan_tree_in<HG, int64_t>(A, wg, lane, total, blocks);
 }
 
 // HG row groups of 16 (one wave each) x KG key groups: wave (kg, hg) walks
@@ -160,7 +276,8 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
 // time, and only with the softmax spread over the products and every register
 // chosen by hand.
 template <class T, int HG, int KG, int MODE>
-__global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(LatArgs A) {
+__global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(LatArgs args) {
+  const LatArgs& A = args;
   constexpr bool PAGED = MODE != kListed;
   constexpr int kAhead = 5;      // LDS reads of operands run this many products ahead (as registers allow)
   constexpr int kRing = kBuffers / KG;           // tiles of a key group in LDS
@@ -172,19 +289,28 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   __shared__ int32_t s_again;
   __shared__ int32_t s_list[PAGED ? 4 : kMaxList + kTileKeys];
   __shared__ uint64_t s_mask[MODE == kTree ? HG * kRowsWave : 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int hg = wave % HG, kg = wave / HG;
-  const int g = lane >> 4, col = lane & 15;
+  __shared__ TreeStart s_at;
+  int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // workgroups of one chiplet (every eighth) take neighbouring work
   const int total = gridDim.x, per = total >> 3, extra = total & 7, x8 = blockIdx.x & 7, i8 = blockIdx.x >> 3;
   const int work = x8 * per + min(x8, extra) + i8;
-  const int wg = work / A.row_blocks, rb = work % A.row_blocks;
+  const int wg = work / A.row_blocks;
 
   Part part;
+  int rb = work % A.row_blocks;
   int len, tile0, tile1;  // keys of the sequence or list, this workgroup's tiles
-  if (PAGED) {
+  if (MODE == kTree) {
     if (wave == 0) {
-      part = plan_part<MODE>(A, wg, lane);
+      const TreeStart at = A.parts ? plan_tree<HG>(A, work, lane) : TreeStart{wg, rb, 0, 0, INT64_MAX, 0, 0, 0, work};
+      if (lane == 0) {
+        s_at = at;
+        if (A.parts) A.split[work] = make_int4(0, 0, 0, 0);
+      }
+    }
+    __syncthreads();
+  } else if (PAGED) {
+    if (wave == 0) {
+      part = plan_part(A, wg, lane);
       if (lane == 0) {
         s_list[0] = part.b; s_list[1] = part.part; s_list[2] = part.parts; s_list[3] = part.cell;
         if (A.parts > A.B && rb == 0 && part.b >= 0 && part.part == 0) A.plan[part.b] = make_int2(part.cell, part.parts);
@@ -206,17 +332,46 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     tile0 = tiles * part.part / A.parts;
     tile1 = tiles * (part.part + 1) / A.parts;
   }
+  // Tree: the pieces of work of this workgroup's share, one after another; once otherwise.  What leads from one to
+  // the next stays in LDS, and the arguments are read again for each and nothing else is kept, so that the walk has the registers.
+  for (;;) {
+  LatArgs A = args;
+  if (MODE == kTree) {
+    auto at = (const __attribute__((address_space(4))) LatArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+    A = *(const LatArgs*)at;
+    asm volatile("" : "+v"(tid));
+    lane = tid & 63;
+    wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    part.b = __builtin_amdgcn_readfirstlane(s_at.b);
+    rb = __builtin_amdgcn_readfirstlane(s_at.block);
+    if (part.b < 0) return;
+    const int first = __builtin_amdgcn_readfirstlane(s_at.first);
+    len = __builtin_amdgcn_readfirstlane(seq_len<MODE>(A, part.b));
+    const int pages = (len + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE;
+    const int last = s_at.pages < pages - first ? first + __builtin_amdgcn_readfirstlane((int)s_at.pages) : pages;
+    tile0 = 2 * first;
+    tile1 = min(2 * last, (len + kTileKeys - 1) / kTileKeys);
+    part.parts = first == 0 && last == pages ? 1 : 2;
+    if (tid == 0 && first == 0 && last < pages) {
+      const int64_t to = s_at.end - last + pages;  // the stream's page behind the block
+      const int n = s_at.parts ? s_at.parts : (int)quotient(to * s_at.shares - 1, s_at.total) - s_at.wg + 1;
+      A.split[s_at.wg] = make_int4(part.b, rb, n, tree_nodes(A, part.b));
+    }
+  }
+  const int hg = wave % HG, kg = wave / HG;
+  const int g = lane >> 4, col = lane & 15;
   const int b = part.b;
-  const int row = (rb * HG + hg) * kRowsWave + col;
-  const bool have = row < A.S * A.H;
-  const int step = have ? row / A.H : 0, head = have ? row % A.H : 0;
+  int row = (rb * HG + hg) * kRowsWave + col;
+  bool have = row < A.S * A.H;
+  int step = have ? row / A.H : 0, head = have ? row % A.H : 0;
   int limit = MODE == kPaged ? len - A.S + 1 + step : len;  // this lane's row sees keys below
   int limit_min = MODE == kPaged ? len - A.S + 1 : len;     // every row does
-  bool none = false;  // tree: this lane's row is no drafted token's, whatever it computes
+  int q_step = step, nodes = 0;
   if (MODE == kTree) {
-    const int nodes = __builtin_amdgcn_readfirstlane(tree_nodes(A, b));
+    nodes = __builtin_amdgcn_readfirstlane(tree_nodes(A, b));
     limit_min = len - nodes;
-    none = step >= nodes;
+    q_step = step < nodes ? step : 0;  // a row of no drafted token repeats the first one's, and is dropped
     // a row's mask, its bits behind the last drafted token cleared
     if (tid < HG * kRowsWave) {
       const int r = rb * HG * kRowsWave + tid, node = r < A.S * A.H ? r / A.H : A.S;
@@ -235,7 +390,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   int slot = PAGED ? -1 : listed(tid);
   typename T::v8 q[kSteps];  // a row past the last repeats the first: its results are dropped
   {
-    const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + (MODE == kTree && none ? 0 : step) * A.q_token +
+    const typename T::elem* p = reinterpret_cast<const typename T::elem*>(A.q) + b * A.q_seq + q_step * A.q_token +
                                 head * A.q_head + 8 * g;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 32 * s);
@@ -410,7 +565,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         const int key = (r & 3) + 16 * (r >> 2);
-        if (!(live_g >> key & 1) || key >= limit_g) x[r >> 2][r & 3] = -INFINITY;
+        if (!(live_g >> key & 1) || (MODE != kTree && key >= limit_g)) x[r >> 2][r & 3] = -INFINITY;
       }
     }
   };
@@ -499,11 +654,19 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     load_first();
   }
   float l = sum_quarters(st.l), m = st.m;
-  if (MODE == kTree && none) {
-    l = 0.f;
-    m = -INFINITY;
+  if (MODE == kTree) {
+    // worked out again, not kept over the walk
+    row = (__builtin_amdgcn_readfirstlane(s_at.block) * HG + hg) * kRowsWave + (own_lane() & 15);
+    step = row / A.H;
+    head = row % A.H;
+    have = step < (A.parts ? nodes : A.S);
+    if (step >= nodes) {
+      // without a plan there is no second kernel that writes the zeros of rows of no drafted token
+      l = 0.f;
+      m = -INFINITY;
 #pragma unroll
-    for (int d = 0; d < kCols; ++d) o[d] = w4f{};
+      for (int d = 0; d < kCols; ++d) o[d] = w4f{};
+    }
   }
 
   // Key groups are joined through LDS (nothing is in flight there any more): each hands the other m, l and
@@ -540,15 +703,13 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   }
   if (part.parts > 1) {
     // in the order of the registers: whole lines, and the join adds them in that order too
-    const int of = PAGED ? __builtin_amdgcn_readfirstlane(s_list[3]) + part.part : wg;
-    const int64_t cell = ((int64_t)of * A.row_blocks + rb) * HG + hg;
+    const int of = MODE == kPaged ? __builtin_amdgcn_readfirstlane(s_list[3]) + part.part : wg;
+    const int64_t cell = MODE == kTree ? (int64_t)(2 * s_at.wg + (s_at.first == 0 ? 1 : 0)) * HG + hg : ((int64_t)of * A.row_blocks + rb) * HG + hg;
     float* po = A.part_o + cell * (kRowsWave * kLatent) + kg * kOwn * 256 + lane * 4;
 #pragma unroll
     for (int d = 0; d < kOwn; ++d) *reinterpret_cast<w4f*>(po + d * 256) = r[d];
     if (g == 0 && kg == 0) A.part_ml[cell * kRowsWave + col] = make_float2(m, l);
-    return;
-  }
-  if (!have) return;
+  } else if (have) {
   const int64_t at = ((int64_t)b * A.S + step) * A.H + head;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   typename T::elem* out = reinterpret_cast<typename T::elem*>(A.out) + at * kLatent + 16 * kg * kOwn + 4 * g;
@@ -560,6 +721,26 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     *reinterpret_cast<typename T::v4*>(out + 16 * d) = v;
   }
   if (A.lse && g == 0 && kg == 0) A.lse[at] = row_lse(m, l);
+  }
+  if (MODE != kTree || !A.parts || s_at.parts) return;
+  __syncthreads();  // masks, tiles and state are read
+  if (tid == 0) {
+    const TreeSeq t(A, s_at.b, 16 * HG);
+    const int64_t left = s_at.pages - (t.pages - s_at.first);  // a share that goes on took the block to its end
+    int next = left > 0 ? s_at.b : -1, block = s_at.block + 1;
+    if (next >= 0 && block >= t.blocks) {
+      block = 0;
+      do ++next;
+      while (next < A.B && TreeSeq(A, next, 16 * HG).blocks == 0);
+      if (next >= A.B) next = -1;
+    }
+    s_at.b = next;
+    s_at.block = block;
+    s_at.first = 0;
+    s_at.pages = left;
+  }
+  __syncthreads();
+  }
 }
 
 // Joins the parts of a row: o = sum_p 2^(m_p - m) o'_p / sum_p 2^(m_p - m) l_p.
@@ -637,6 +818,98 @@ __global__ __launch_bounds__(256) void k_latent_join(LatArgs A, int hgs, bool pa
   if (A.lse && column == 0) A.lse[at] = row_lse(top, l);
 }
 
+// Joins the blocks of a tree call that several workgroups worked on and writes the rows of no drafted token.  A
+// wave takes 256 of a cell's numbers at a time (two or three parts as a rule, so that its waves do not divide
+// them); how many blocks there are stands in `split`, and the waves of a fixed grid go through them.
+constexpr int kTreeJoin = 1024;  // workgroups
+
+template <class T>
+__global__ __launch_bounds__(256) void k_tree_join(LatArgs A, int hgs) {
+  constexpr int kSlots = kUnits / 64;
+  const int lane = threadIdx.x & 63, waves = gridDim.x * 4, self = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int pieces = hgs * kCols;
+  typename T::elem* const out = reinterpret_cast<typename T::elem*>(A.out);
+  int4 split[kSlots];
+  uint64_t some[kSlots];
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) split[i] = A.split[64 * i + lane];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    some[i] = __ballot(split[i].z != 0);
+    count += __popcll(some[i]);
+  }
+  for (int item = self; item < count * pieces; item += waves) {
+    int k = item / pieces, wg = 0;
+    int4 block = {};
+    const int hg = item % pieces / kCols, piece = item % kCols;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {  // the k-th workgroup with a block
+      uint64_t bits = some[i];
+      const int here = __popcll(bits);
+      if (k >= 0 && k < here) {
+        for (; k > 0; --k) bits &= bits - 1;
+        const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)bits) - 1);
+        wg = 64 * i + l;
+        block.x = __builtin_amdgcn_readlane(split[i].x, l);
+        block.y = __builtin_amdgcn_readlane(split[i].y, l);
+        block.z = __builtin_amdgcn_readlane(split[i].z, l);
+        block.w = __builtin_amdgcn_readlane(split[i].w, l);
+      }
+      k -= here;
+    }
+    const int b = block.x, n = block.z, row = (block.y * hgs + hg) * kRowsWave + (lane & 15);
+    const auto cell = [&](int p) { return (int64_t)(p == 0 ? 2 * wg + 1 : 2 * (wg + p)) * hgs + hg; };
+    const float2* ml = A.part_ml + (lane & 15);
+    const float4* po = reinterpret_cast<const float4*>(A.part_o) + piece * 64 + lane;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto add = [&](auto batch) __attribute__((always_inline)) {
+      constexpr int kBatch = decltype(batch)::value;
+      for (int p0 = 0; p0 < n; p0 += kBatch) {
+        float2 s[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int64_t c = cell(min(p0 + u, n - 1));
+          s[u] = ml[c * kRowsWave];
+          v[u] = po[c * (kRowsWave * kLatent / 4)];
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) top = fmaxf(top, s[u].x);
+        const float t0 = top == -INFINITY ? 0.f : top, old = __builtin_amdgcn_exp2f(m - t0);
+        m = top;
+        l *= old; o.x *= old; o.y *= old; o.z *= old; o.w *= old;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const float f = p0 + u < n ? __builtin_amdgcn_exp2f(s[u].x - t0) : 0.f;
+          l = fmaf(s[u].y, f, l);
+          o.x = fmaf(v[u].x, f, o.x); o.y = fmaf(v[u].y, f, o.y); o.z = fmaf(v[u].z, f, o.z); o.w = fmaf(v[u].w, f, o.w);
+        }
+      }
+    };
+    if (n <= 3) add(std::integral_constant<int, 3>{});
+    else add(std::integral_constant<int, 8>{});
+    if (row >= block.w * A.H) continue;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    typename T::v4 v;
+    v[0] = T::out(o.x * inv); v[1] = T::out(o.y * inv); v[2] = T::out(o.z * inv); v[3] = T::out(o.w * inv);
+    const int64_t to = (int64_t)b * A.S * A.H + row;
+    const int column = 16 * piece + 4 * (lane >> 4);
+    *reinterpret_cast<typename T::v4*>(out + to * kLatent + column) = v;
+    if (A.lse && column == 0) A.lse[to] = row_lse(m, l);
+  }
+  for (int item = self; item < A.B * A.S; item += waves) {
+    const int b = item / A.S, node = item % A.S;
+    if (node < tree_nodes(A, b)) continue;
+    const int64_t row = (int64_t)item * A.H;
+    for (int h = 0; h < A.H; ++h) *reinterpret_cast<uint4*>(out + (row + h) * kLatent + 8 * lane) = make_uint4(0, 0, 0, 0);
+    if (A.lse)
+      for (int h = lane; h < A.H; h += 64) A.lse[row + h] = -INFINITY;
+  }
+}
+
 // ------------------------------------------------------------------ host
 
 static inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -671,6 +944,7 @@ static LatGeom layout(LatGeom g, int64_t B) {
 // where parts would be short the rows are halved first: 16 tokens x 64 heads x
 // 2048 keys take 24 us as 8 parts of 32 rows against 28 us as 16 parts of 64.
 constexpr int kManyParts = 8;     // listed: more parts a token than these are short
+constexpr int64_t kFewPages = 4;  // tree: pages a compute unit
 constexpr int kShortKeys = 512;   // paged: keys a part at most, where the table says so
 
 // A paged call has B parts and `extra` more, and no part has more pages than
@@ -720,6 +994,22 @@ static LatGeom paged_geom(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
   return layout(g, g.cells ? B : 0);
 }
 
+// A tree call's rows are cut into blocks of 128, or of 64 where those leave fewer waves idle (a wave of either
+// takes about as long over a tile, 4640 against 2 x 2464 clocks) or where the card's share of the work would be
+// a few pages a unit, and the calls' time the walk of one of them.
+static LatGeom tree_geom(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
+  LatGeom g{};
+  const int rows = S * H;
+  const auto blocks = [&](int hg) { return (int64_t)(rows + kRowsWave * hg - 1) / (kRowsWave * hg); };
+  g.hg = row_groups(rows);
+  if (g.hg == 8 && (blocks(4) * 17 < blocks(8) * 32 || B * blocks(8) * max_pages < kFewPages * kUnits)) g.hg = 4;
+  g.row_blocks = (int)blocks(g.hg);
+  if (B == 0 || B > kPlanBatch) return layout(g, 0);
+  g.parts = kUnits;
+  g.cells = 2 * kUnits;
+  return layout(g, 2 * kUnits);
+}
+
 template <class T, int MODE>
 static int launch(LatArgs A, const LatGeom& g, char* ws, hipStream_t stream) {
   A.row_blocks = g.row_blocks;
@@ -727,8 +1017,10 @@ static int launch(LatArgs A, const LatGeom& g, char* ws, hipStream_t stream) {
   A.part_o = reinterpret_cast<float*>(ws + g.o);
   A.part_ml = reinterpret_cast<float2*>(ws + g.ml);
   A.plan = reinterpret_cast<int2*>(ws + g.plan);
-  const int64_t grid = (int64_t)(MODE != kListed ? 1 : A.B) * g.parts * g.row_blocks;
-  const int64_t join = (int64_t)A.B * g.row_blocks * g.hg * kCols;
+  A.split = reinterpret_cast<int4*>(ws + g.plan);
+  const int64_t grid = MODE == kTree ? (g.parts ? g.parts : (int64_t)A.B * g.row_blocks)
+                                     : (int64_t)(MODE == kPaged ? 1 : A.B) * g.parts * g.row_blocks;
+  const int64_t join = MODE == kTree ? kTreeJoin : (int64_t)A.B * g.row_blocks * g.hg * kCols;
   // a launch dimension takes fewer than 2^32 threads (a larger one wraps, without an error)
   const int64_t threads = 64 * (g.hg == 8 ? 8 : 2 * g.hg);
   if (grid * threads > 0xffffffffLL || (g.cells && join * 256 > 0xffffffffLL)) return IDX_EUNSUPPORTED;
@@ -737,7 +1029,11 @@ static int launch(LatArgs A, const LatGeom& g, char* ws, hipStream_t stream) {
   else if (g.hg == 2) k_latent<T, 2, 2, MODE><<<n, dim3(256), 0, stream>>>(A);
   else if (g.hg == 4) k_latent<T, 4, 2, MODE><<<n, dim3(512), 0, stream>>>(A);
   else k_latent<T, 8, 1, MODE><<<n, dim3(512), 0, stream>>>(A);
-  if (g.cells) k_latent_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, g.hg, MODE != kListed);
+  if (MODE == kTree) {
+    if (g.cells) k_tree_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, g.hg);
+  } else if (g.cells) {
+    k_latent_join<T><<<dim3((uint32_t)join), dim3(256), 0, stream>>>(A, g.hg, MODE == kPaged);
+  }
   return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
 
@@ -770,7 +1066,7 @@ int latent_selected(const void* q, int64_t q_token, int64_t q_head, const void* 
   if (!workspace || workspace_bytes < g.total) return IDX_EWORKSPACE;
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   LatArgs A{static_cast<const char*>(q), q_token, 0, q_head, static_cast<const char*>(cache), num_slots, slots,
-            nullptr, nullptr, nullptr, 0, K, T, 1, H, 0, 0, scale * kLog2e, static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
+            nullptr, nullptr, nullptr, 0, K, T, 1, H, 0, 0, scale * kLog2e, static_cast<char*>(out), lse, nullptr, nullptr, nullptr, nullptr};
   char* const ws = static_cast<char*>(workspace);
   return dtype == IDX_TOPK_BF16 ? launch<TBf16, kListed>(A, g, ws, stream) : launch<TF16, kListed>(A, g, ws, stream);
 }
@@ -796,14 +1092,14 @@ int latent_paged(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, 
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   LatArgs A{static_cast<const char*>(q), q_seq, q_token, q_head, static_cast<const char*>(cache),
             (int64_t)num_pages * IDX_TOPK_PAGE, page_table, seq_lens, nullptr, nullptr, 0, max_pages, B, S, H, 0, 0, scale * kLog2e,
-            static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
+            static_cast<char*>(out), lse, nullptr, nullptr, nullptr, nullptr};
   char* const ws = static_cast<char*>(workspace);
   return dtype == IDX_TOPK_BF16 ? launch<TBf16, kPaged>(A, g, ws, stream) : launch<TF16, kPaged>(A, g, ws, stream);
 }
 
 size_t latent_tree_workspace_bytes(int32_t B, int32_t S, int32_t H, int32_t max_pages) {
   if (B < 0 || S < 1 || S > IDX_TOPK_MAX_NODES || H < 1 || H > kMaxHeads || max_pages < 0) return 0;
-  return paged_geom(B, S, H, max_pages).total;
+  return tree_geom(B, S, H, max_pages).total;
 }
 
 int latent_tree(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, const void* cache, int32_t num_pages,
@@ -819,12 +1115,12 @@ int latent_tree(const void* q, int64_t q_seq, int64_t q_token, int64_t q_head, c
   if (!prefix_lens || !aligned4(prefix_lens) || !aligned4(counts) || !masks || ((uintptr_t)masks & 7u) != 0 ||
       (!page_table && max_pages > 0) || (!cache && num_pages > 0))
     return IDX_EINVAL;
-  const LatGeom g = paged_geom(B, S, H, max_pages);
+  const LatGeom g = tree_geom(B, S, H, max_pages);
   if (!workspace || workspace_bytes < g.total) return IDX_EWORKSPACE;
   if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   LatArgs A{static_cast<const char*>(q), q_seq, q_token, q_head, static_cast<const char*>(cache),
             (int64_t)num_pages * IDX_TOPK_PAGE, page_table, prefix_lens, counts, masks, mask_seq, max_pages, B, S, H, 0, 0,
-            scale * kLog2e, static_cast<char*>(out), lse, nullptr, nullptr, nullptr};
+            scale * kLog2e, static_cast<char*>(out), lse, nullptr, nullptr, nullptr, nullptr};
   char* const ws = static_cast<char*>(workspace);
   return dtype == IDX_TOPK_BF16 ? launch<TBf16, kTree>(A, g, ws, stream) : launch<TF16, kTree>(A, g, ws, stream);
 }

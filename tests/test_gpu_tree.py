@@ -123,15 +123,15 @@ def test_tree_any_mask():
 
 
 def test_tree_chain_is_paged():
-    """A chain of drafted tokens: latent_paged's result for the same tokens, bit for bit."""
+    """A chain of drafted tokens: latent_paged's keys for the same tokens.  The two cut the keys in different places,
+    so that each is held to the bounds, not to the other's bits."""
     import scoring_exact_top_amd as lib
     for S, H, prefix in ((4, 20, [1000, 37, 0]), (1, 128, [5000, 64, 1]), (16, 64, [300, 1200, 2])):
         q, cache, table, _ = _case(prefix, [S] * 3, S, H, torch.bfloat16, S)
         chain = [[(2 << j) - 1 for j in range(S)]] * 3
-        a = _call(q, cache, table, prefix, None, chain)
         lens = torch.tensor([p + S for p in prefix], dtype=torch.int32).cuda()
-        b = lib.latent_paged(q.cuda(), cache.cuda(), table.cuda(), lens, SCALE)
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), (S, H)
+        for out, lse in (_call(q, cache, table, prefix, None, chain), lib.latent_paged(q.cuda(), cache.cuda(), table.cuda(), lens, SCALE)):
+            _check(out, lse, q, cache, table, prefix, [S] * 3, chain, where="chain")
 
 
 def test_tree_ignores_what_is_not_there():

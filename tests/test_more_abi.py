@@ -98,4 +98,4 @@ def test_tree_workspace_is_bounded():
             for H in (1, 16, 20, 33, 64, 100, 113, 128):
                 for max_pages in (0, 1, 3, 16, 1024, 1 << 20):
                     need = st.latent_tree_workspace_bytes(B, S, H, max_pages)
-                    assert 256 <= need <= 552 << 20, (B, S, H, max_pages, need)
+                    assert 256 <= need <= 132 << 20, (B, S, H, max_pages, need)
