@@ -581,9 +581,6 @@ int idx_topk_cache_append_rotary(const void *latents, int64_t latent_token, int3
                                  int32_t T, int32_t dtype, void *latent_cache, uint8_t *k_cache,
                                  float *k_scale, int64_t num_slots, void *latents_out, void *stream);
 
-/* Bytes of workspace idx_topk_matmul_e4m3 needs (0 for arguments it rejects). */
-size_t idx_topk_matmul_e4m3_workspace(int32_t M, int32_t N, int32_t K);
-
 /*
  * Product of e4m3 activations and weights with block scales:
  *   out[m,n] = sum_b xs(m,b) * w_scale[n / 128, b] * sum_{k in block b} x[m,k] * w[n,k]
@@ -599,12 +596,11 @@ size_t idx_topk_matmul_e4m3_workspace(int32_t M, int32_t N, int32_t K);
  * bfloat16's rounding).  It is scaled and added to the others in FP32 and the result is rounded
  * once; sums that leave the output's type are infinities.  NaN codes
  * (those of idx_topk_norm_quant for a row with a NaN) make the outputs they enter NaN, and no others.
- * The result does not depend on timing.
+ * The result does not depend on timing.  Calls of 2^23 tiles of 16 x 16 and more are IDX_EUNSUPPORTED.  No workspace.
  */
 int idx_topk_matmul_e4m3(const uint8_t *x, int64_t x_row, const float *x_scale, int32_t x_group,
                          const uint8_t *w, const float *w_scale, int32_t M, int32_t N, int32_t K,
-                         int32_t dtype, void *out, int64_t out_row, void *workspace,
-                         size_t workspace_bytes, void *stream);
+                         int32_t dtype, void *out, int64_t out_row, void *stream);
 
 /* Copy the counters of the last call that used `workspace` into *out.
  * Synchronises `stream`.  For tests and diagnosis, not for hot loops. */

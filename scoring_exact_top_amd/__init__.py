@@ -433,10 +433,8 @@ _lib.idx_topk_norm_rotate.argtypes = [_vp, _i64, _i64, _i32, _vp, _vp, _f32, _vp
 _lib.idx_topk_cache_append_rotary.restype = ctypes.c_int
 _lib.idx_topk_cache_append_rotary.argtypes = [_vp, _i64, _i32, _vp, _f32, _i32, _vp, _i64, _i32, _vp, _vp, _f32, _i32, _i32, _vp, _vp,
                                               _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _vp]
-_lib.idx_topk_matmul_e4m3_workspace.restype = _sz
-_lib.idx_topk_matmul_e4m3_workspace.argtypes = [_i32, _i32, _i32]
 _lib.idx_topk_matmul_e4m3.restype = ctypes.c_int
-_lib.idx_topk_matmul_e4m3.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _sz, _vp]
+_lib.idx_topk_matmul_e4m3.argtypes = [_vp, _i64, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i64, _vp]
 
 
 def latent_selected_workspace_bytes(T: int, H: int, K: int) -> int:
@@ -449,10 +447,6 @@ def latent_paged_workspace_bytes(B: int, S: int, H: int, max_pages: int) -> int:
 
 def latent_tree_workspace_bytes(B: int, S: int, H: int, max_pages: int) -> int:
     return int(_lib.idx_topk_latent_tree_workspace(B, S, H, max_pages))
-
-
-def matmul_e4m3_workspace_bytes(M: int, N: int, K: int) -> int:
-    return int(_lib.idx_topk_matmul_e4m3_workspace(M, N, K))
 
 
 def latent_expanded_workspace_bytes(Tq: int, B: int, max_q: int, max_k: int, H: int) -> int:
@@ -860,7 +854,7 @@ def cache_append_rotary(latents, index_keys, slots, positions, table, latent_cac
                                              P, T, dt, cache_at, kc_at, ks_at, n if num is None else num, out_at, _on(stream, dev)))
 
 
-def matmul_e4m3(x, x_scale, w, w_scale, dtype=torch.bfloat16, out=None, workspace=None, stream=None):
+def matmul_e4m3(x, x_scale, w, w_scale, dtype=torch.bfloat16, out=None, stream=None):
     """Product x @ w.T of e4m3 operands with block scales; see idx_topk_matmul_e4m3.
 
     x [M,K] float8_e4m3fn or uint8 (strided rows) with x_scale [M,ceil(K/128)]
@@ -891,10 +885,9 @@ def matmul_e4m3(x, x_scale, w, w_scale, dtype=torch.bfloat16, out=None, workspac
     if out is None:
         out = _empty((M, N), dtype, dev, stream)
     x_at, out_at = _rows_at(x, x.dtype, dev, (M, K)), _rows_at(out, dtype, dev, (M, N))
-    ws_at, ws_bytes, ws = _scratch(workspace, _lib.idx_topk_matmul_e4m3_workspace(M, N, K), dev, stream)
     _check(_lib.idx_topk_matmul_e4m3(x_at, *_strides(x), _at(x_scale, torch.float32, dev), 128 if x_scale.shape[1] == blocks else 0,
                                      _at(w, w.dtype, dev), _at(w_scale, torch.float32, dev), M, N, K, kind, out_at, *_strides(out),
-                                     ws_at, ws_bytes, _on(stream, dev)))
+                                     _on(stream, dev)))
     return out
 
 

@@ -337,15 +337,10 @@ extern "C" int idx_topk_norm_rotate(const void* x, int64_t x_token, int64_t x_he
                      D, dtype, out, out_token, out_head, codes, scales, static_cast<hipStream_t>(stream));
 }
 
-extern "C" size_t idx_topk_matmul_e4m3_workspace(int32_t M, int32_t N, int32_t K) {
-  return matmul_e4m3_workspace_bytes(M, N, K);
-}
-
 extern "C" int idx_topk_matmul_e4m3(const uint8_t* x, int64_t x_row, const float* x_scale, int32_t x_group,
                                     const uint8_t* w, const float* w_scale, int32_t M, int32_t N, int32_t K,
-                                    int32_t dtype, void* out, int64_t out_row, void* workspace,
-                                    size_t workspace_bytes, void* stream) {
-  return matmul_e4m3(x, x_row, x_scale, x_group, w, w_scale, M, N, K, dtype, out, out_row, workspace, workspace_bytes,
+                                    int32_t dtype, void* out, int64_t out_row, void* stream) {
+  return matmul_e4m3(x, x_row, x_scale, x_group, w, w_scale, M, N, K, dtype, out, out_row,
                      static_cast<hipStream_t>(stream));
 }
 

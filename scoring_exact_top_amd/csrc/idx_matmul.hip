@@ -11,12 +11,15 @@
 // 16x16x32 form does the same.  The weights' rows are the rows of A and the activations' those of B, so that a lane
 // holds four neighbouring columns n of one row m: one scale a lane, and outputs that are stored
 // together.  Both operands are laid out alike (lane l has bytes 32 (l / 16) .. + 32 of row l % 16).
+#include <type_traits>
+#include "idx_attn.hpp"
 #include "idx_common.hpp"
 #include "idx_matmul.hpp"
 
 namespace idxk {
 
 constexpr int kBlock = 128;
+constexpr int kUnits = 256;        // compute units
 constexpr int kMaxRow = 1 << 24;  // bytes of an operand's row: 256 rows on, offsets take 32 bits
 
 struct MatArgs {
@@ -29,17 +32,7 @@ struct MatArgs {
   int32_t M, N, K, blocks;
   void* out;
   int64_t out_row;
-  float* part;               // split: [splits][M][N]
-  int32_t splits;
 };
-
-// 32 bytes of a row from p on, of which `have` (a multiple of 16, maybe negative) are in the row; zeros for the others.
-__device__ __forceinline__ v8i load_some(const uint8_t* p, int have) {
-  uint4 a = make_uint4(0, 0, 0, 0), b = a;
-  if (have > 0) a = *reinterpret_cast<const uint4*>(p);
-  if (have > 16) b = *reinterpret_cast<const uint4*>(p + 16);
-  return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-}
 
 // Four neighbouring columns of a row; `n` of them are there.
 template <class E>
@@ -53,61 +46,312 @@ __device__ __forceinline__ void store4(E* p, v4f v, int n) {
       if (j < n) p[j] = y[j];
 }
 
-// Few rows: a workgroup of 8 waves takes 16 NF columns and 16 MF rows, each wave every eighth
-// block of them straight from memory; the waves' sums are added through LDS in a fixed order.
-template <class E, int NF, int MF>
-__global__ __launch_bounds__(512) void k_matmul_few(MatArgs A) {
-  __shared__ v4f s_sum[8][NF * MF][64];
+// 64 lanes x 4 bytes from a lane's own address to 256 bytes of LDS in lane order, as dma_lanes.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma_words(const void* src, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(src) : "m0");
+}
+#pragma clang diagnostic pop
+
+// An image of a block in LDS: rows of 8 16-byte chunks, chunk c of row r at c ^ (r / 2 & 7), so that 16 rows at one
+// chunk cover all banks once.  Lane 16g + r of a product takes chunks g and g + 4 of row r of both operands.  It is
+// loaded 8 rows at a time without registers; loads of a fragment straight into the lanes would cost the address
+// unit four times as much (neighbouring lanes are different rows).
+__device__ const uint4 kZeroChunk = {};
+
+// Few rows or few tiles: a workgroup of W waves takes 16 NF columns and 16 MF rows, each wave every W-th block of
+// them through a ring of D images of its own, without a barrier; the waves' sums are added through LDS in a
+// fixed order.  For few rows it is bound by memory (up to 150 KB on their way to a unit), beyond that by the loads
+// of a unit: 64 bytes a clock, so that a 64 x 64 tile's block takes 256 clocks of them and 128 of products.
+template <class E, int NF, int MF, int W, int D>
+__global__ __launch_bounds__(64 * W, W / 4) void k_matmul_few(MatArgs A) {
+  constexpr int kSlot = (NF + MF) * 16 * kBlock + 64 * 4;
+  constexpr int kLoads = 2 * (NF + MF) + 1;
+  constexpr int kRing = W * D * kSlot, kSums = W * NF * MF * 1024;
+  __shared__ __attribute__((aligned(1024))) char s_ring[kRing > kSums ? kRing : kSums];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, r = lane & 15;
-  const int n0 = blockIdx.x * 16 * NF, m0 = blockIdx.y * 16 * MF, split = blockIdx.z;
-  const int b0 = (int)((int64_t)A.blocks * split / A.splits), b1 = (int)((int64_t)A.blocks * (split + 1) / A.splits);
-  const uint8_t* wp[NF];
-  const uint8_t* xp[MF];
-  const float* sp[MF];
+  // workgroups of one chiplet (every eighth) take neighbouring tiles: the rows of a column together
+  const int tiles_m = (A.M + 16 * MF - 1) / (16 * MF);
+  const int total = gridDim.x, per = total >> 3, extra = total & 7, x8 = blockIdx.x & 7, i8 = blockIdx.x >> 3;
+  const int work = x8 * per + min(x8, extra) + i8;
+  const int n0 = work / tiles_m * (16 * NF), m0 = work % tiles_m * (16 * MF);
+  const char* const w_tile = reinterpret_cast<const char*>(A.w) + (int64_t)n0 * A.K;
+  const char* const x_tile = reinterpret_cast<const char*>(A.x) + (int64_t)m0 * A.x_row;
+  // a load takes 8 rows; rows past the last repeat it, what comes of them is dropped
+  const int l8 = lane >> 3, chunk = ((lane & 7) ^ (l8 >> 1)) << 4;
+  uint32_t at_w[2 * NF], at_x[2 * MF];
 #pragma unroll
-  for (int i = 0; i < NF; ++i) wp[i] = A.w + (int64_t)min(n0 + 16 * i + r, A.N - 1) * A.K + 32 * g;
+  for (int i = 0; i < 2 * NF; ++i) at_w[i] = (uint32_t)min(8 * i + l8, A.N - 1 - n0) * (uint32_t)A.K + (chunk ^ (i & 1) << 6);
 #pragma unroll
-  for (int j = 0; j < MF; ++j) {
-    const int64_t m = min(m0 + 16 * j + r, A.M - 1);
-    xp[j] = A.x + m * A.x_row + 32 * g;
-    sp[j] = A.xs + m * A.xs_row;
-  }
-  const float* ws = A.ws + (int64_t)(n0 / kBlock) * A.blocks;
+  for (int i = 0; i < 2 * MF; ++i) at_x[i] = (uint32_t)min(8 * i + l8, A.M - 1 - m0) * (uint32_t)A.x_row + (chunk ^ (i & 1) << 6);
+  const float* const xs = A.xs + (int64_t)min(m0 + lane, A.M - 1) * A.xs_row;
+  // columns whose number does not divide 128 may lie in two blocks of the weights' scales: a fragment lies in one
+  constexpr int kWs = kBlock % (16 * NF) == 0 ? 1 : NF;
+  const auto* const ws = reinterpret_cast<const __attribute__((address_space(4))) float*>((uintptr_t)A.ws);
+  int64_t ws_at[kWs];
+#pragma unroll
+  for (int i = 0; i < kWs; ++i) ws_at[i] = (int64_t)(min(n0 + 16 * i, A.N - 1) / kBlock) * A.blocks;
+  char* const ring = s_ring + wave * (D * kSlot);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)ring);
+  const auto load = [&](int b, int slot) __attribute__((always_inline)) {
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(lds0 + slot * kSlot);
+    const char *wb = w_tile + (int64_t)b * kBlock, *xb = x_tile + (int64_t)b * kBlock;
+    if ((b + 1) * kBlock <= A.K) {
+#pragma unroll
+      for (int i = 0; i < 2 * NF; ++i) dma_row(wb, (int)at_w[i], dst + i * 1024);
+#pragma unroll
+      for (int i = 0; i < 2 * MF; ++i) dma_row(xb, (int)at_x[i], dst + (2 * NF + i) * 1024);
+    } else {  // a short last block: zeros behind its end
+      const int have = A.K - b * kBlock;
+      const char* const zero = reinterpret_cast<const char*>(&kZeroChunk);
+#pragma unroll
+      for (int i = 0; i < 2 * NF; ++i) dma_lanes((chunk ^ (i & 1) << 6) < have ? wb + at_w[i] : zero, dst + i * 1024);
+#pragma unroll
+      for (int i = 0; i < 2 * MF; ++i) dma_lanes((chunk ^ (i & 1) << 6) < have ? xb + at_x[i] : zero, dst + (2 * NF + i) * 1024);
+    }
+    dma_words(xs + (int64_t)b * A.xs_block, dst + (NF + MF) * 16 * kBlock);
+  };
   v4f acc[NF * MF];
 #pragma unroll
   for (int i = 0; i < NF * MF; ++i) acc[i] = v4f{};
-  for (int b = b0 + wave; b < b1; b += 8) {
-    v8i a[NF], c[MF];
-    float s[MF];
-    const int have = A.K - b * kBlock - 32 * g;
+  const int count = A.blocks > wave ? (A.blocks - wave + W - 1) / W : 0;  // blocks of this wave
 #pragma unroll
-    for (int i = 0; i < NF; ++i) a[i] = load_some(wp[i] + (int64_t)b * kBlock, have);
+  for (int t = 0; t < D; ++t)
+    if (t < count) load(wave + W * t, t);
+  const int at = r * kBlock + ((g ^ (r >> 1 & 7)) << 4);
+  int slot = 0;
+  for (int t = 0; t < count; ++t) {
+    // what a wait leaves outstanding are the loads of later blocks
+    const int later = min(count - 1 - t, D - 1);
+    if (later == 3) dma_wait<(D > 3 ? 3 : 0) * kLoads>();
+    else if (later == 2) dma_wait<(D > 2 ? 2 : 0) * kLoads>();
+    else if (later == 1) dma_wait<(D > 1 ? 1 : 0) * kLoads>();
+    else dma_wait<0>();
+    const int b = wave + W * t;
+    const char *p = ring + slot * kSlot + at, *q = ring + slot * kSlot + (at ^ 64);
+    const float* const scales = reinterpret_cast<const float*>(ring + slot * kSlot + (NF + MF) * 16 * kBlock);
+    v8i a[NF], c[MF];
+    float s[MF], wsb[kWs];
+#pragma unroll
+    for (int i = 0; i < kWs; ++i) wsb[i] = ws[ws_at[i] + b];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) a[i] = cat8(lds_read<v4i>(p + i * 2048), lds_read<v4i>(q + i * 2048));
 #pragma unroll
     for (int j = 0; j < MF; ++j) {
-      c[j] = load_some(xp[j] + (int64_t)b * kBlock, have);
-      s[j] = sp[j][b * A.xs_block] * ws[b];
+      c[j] = cat8(lds_read<v4i>(p + (NF + j) * 2048), lds_read<v4i>(q + (NF + j) * 2048));
+      s[j] = scales[16 * j + r];
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the image is read: the next block of its place may come
+    if (t + D < count) load(b + W * D, slot);
+    slot = slot + 1 == D ? 0 : slot + 1;
 #pragma unroll
     for (int i = 0; i < NF; ++i)
 #pragma unroll
       for (int j = 0; j < MF; ++j) {
+        const float f = s[j] * wsb[kWs > 1 ? i : 0];
         const v4f p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[i], c[j], v4f{}, 0, 0, 0, 0, 0, 0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) acc[i * MF + j][u] = fmaf(s[j], p[u], acc[i * MF + j][u]);
+        for (int u = 0; u < 4; ++u) acc[i * MF + j][u] = fmaf(f, p[u], acc[i * MF + j][u]);
       }
   }
-#pragma unroll
-  for (int i = 0; i < NF * MF; ++i) s_sum[wave][i][lane] = acc[i];
   __syncthreads();
-  for (int f = wave; f < NF * MF; f += 8) {
-    v4f sum = s_sum[0][f][lane];
+  v4f* const sums = reinterpret_cast<v4f*>(s_ring);
 #pragma unroll
-    for (int w = 1; w < 8; ++w) sum += s_sum[w][f][lane];
+  for (int i = 0; i < NF * MF; ++i) sums[(wave * (NF * MF) + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  for (int f = wave; f < NF * MF; f += W) {
+    v4f sum = sums[f * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum += sums[(w * (NF * MF) + f) * 64 + lane];
     const int m = m0 + 16 * (f % MF) + r, n = n0 + 16 * (f / MF) + 4 * g;
-    if (m >= A.M || n >= A.N) continue;
-    if (A.splits > 1) store4(A.part + ((int64_t)split * A.M + m) * A.N + n, sum, A.N - n);
-    else store4(static_cast<E*>(A.out) + m * A.out_row + n, sum, A.N - n);
+    if (m < A.M && n < A.N) store4(static_cast<E*>(A.out) + (int64_t)m * A.out_row + n, sum, A.N - n);
+  }
+}
+
+// Many rows: a workgroup of WN x WM waves takes 16 NF WN columns and 16 MF WM rows, a wave 16 NF x 16 MF of them.  A
+// step is one block of 128 k.  Its rows of both operands come from memory straight into one of two LDS images; a wave
+// holds its MF fragments of x for the whole step and takes those of w one after another.  The sums of a fragment
+// are scaled and added between the products of the next one.
+//
+// Two barriers a step.  At the first (before the second half of w's fragments) every wave has read x and the first
+// half of w: that part of the image takes the block after the next.  At the second (before the last fragment's
+// products) every wave has read the rest, and the next block's first part is there: its fragments are read beside
+// the last products.  So a load has a step and a half to arrive with two images (a step, with one barrier: 13% more time).
+constexpr int kScaleSteps = 4;  // steps whose scales of x are loaded together
+
+template <class E, int NF, int MF, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM, 2) void k_matmul_tiles(MatArgs A) {
+  constexpr int kWaves = WN * WM, TN = 16 * NF * WN, TM = 16 * MF * WM;
+  constexpr int kImage = (TN + TM) * kBlock;
+  constexpr int kLoadsX = TM / 8 / kWaves, kLoadsW = TN / 16 / kWaves;  // of 8 rows, a wave: x, half of w
+  constexpr int kFirst = kLoadsX + kLoadsW, kLoads = kFirst + kLoadsW;  // the part that comes first, a block
+  constexpr int kScaleLoads = kScaleSteps * TM / 64 / kWaves;
+  static_assert(NF % 4 == 0 && kLoadsX % 2 == 0 && kLoadsW % 2 == 0 && kScaleLoads >= 1 && kLoadsW <= MF && kFirst <= 2 * MF, "");
+  __shared__ __attribute__((aligned(1024))) char s_tile[2 * kImage];
+  __shared__ float s_xs[2][kScaleSteps][TM];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave % WN, wm = wave / WN, g = lane >> 4, r = lane & 15;
+  // workgroups of one chiplet (every eighth) take neighbouring tiles: 4 rows of tiles together, column by column
+  const int tiles_n = (A.N + TN - 1) / TN, tiles_m = (A.M + TM - 1) / TM;
+  const int total = gridDim.x, per = total >> 3, extra = total & 7, x8 = blockIdx.x & 7, i8 = blockIdx.x >> 3;
+  const int work = x8 * per + min(x8, extra) + i8;
+  const int band = work / (4 * tiles_n), in_band = work % (4 * tiles_n), high = min(4, tiles_m - 4 * band);
+  const int m0 = (4 * band + in_band % high) * TM, n0 = in_band / high * TN;
+
+  const char* const w_tile = reinterpret_cast<const char*>(A.w) + (int64_t)n0 * A.K;
+  const char* const x_tile = reinterpret_cast<const char*>(A.x) + (int64_t)m0 * A.x_row;
+  // a load takes 8 rows, a lane's chunk of them is 64 bytes further in odd loads
+  const int l8 = lane >> 3, chunk = ((lane & 7) ^ (l8 >> 1)) << 4;
+  const int at_w[2] = {l8 * A.K + chunk, l8 * A.K + (chunk ^ 64)};
+  const int at_x[2] = {l8 * (int)A.x_row + chunk, l8 * (int)A.x_row + (chunk ^ 64)};
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)s_tile;
+  // first of the 8 rows of load i of a block: x's, the first half of each wave column's rows of w, the second halves
+  const auto row_of = [&](int i) __attribute__((always_inline)) {
+    if (i < kLoadsX) return 8 * (wave * kLoadsX + i);
+    constexpr int kHalf = NF;  // loads of a half: 16 NF / 2 rows
+    const int u = wave * kLoadsW + (i < kFirst ? i - kLoadsX : i - kFirst);
+    return u / kHalf * (16 * NF) + (i < kFirst ? 0 : 8 * NF) + u % kHalf * 8;
+  };
+  const auto image = [&](int b, int i) __attribute__((always_inline)) {
+    return __builtin_amdgcn_readfirstlane(lds0 + (b & 1) * kImage + ((i < kLoadsX ? TN : 0) + row_of(i)) * kBlock);
+  };
+  const auto load = [&](int b, int i) __attribute__((always_inline)) {
+    const bool of_x = i < kLoadsX;
+    dma_row((of_x ? x_tile : w_tile) + (int64_t)b * kBlock + (int64_t)row_of(i) * (of_x ? A.x_row : A.K), (of_x ? at_x : at_w)[i & 1], image(b, i));
+  };
+  // ... of a block that may be the last and shorter (zeros behind its end), in a tile that may pass the last row (which
+  // is repeated, what comes of it is dropped)
+  const auto load_any = [&](int b, int i) __attribute__((always_inline)) {
+    const bool of_x = i < kLoadsX;
+    const int row = min(row_of(i) + l8, of_x ? A.M - 1 - m0 : A.N - 1 - n0);
+    const int k = b * kBlock + (chunk ^ (i & 1) << 6);
+    dma_lanes(k < A.K ? (of_x ? x_tile : w_tile) + (int64_t)row * (of_x ? A.x_row : A.K) + k : reinterpret_cast<const char*>(&kZeroChunk), image(b, i));
+  };
+  // scales of x for the steps from b on
+  const auto load_scales = [&](int b) __attribute__((always_inline)) {
+    const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)s_xs + (b / kScaleSteps & 1) * (kScaleSteps * TM * 4);
+#pragma unroll
+    for (int u = 0; u < kScaleLoads; ++u) {
+      const int piece = wave * kScaleLoads + u, step = piece / (TM / 64), row = piece % (TM / 64) * 64;
+      dma_words(A.xs + (int64_t)min(m0 + row + lane, A.M - 1) * A.xs_row + (int64_t)min(b + step, A.blocks - 1) * A.xs_block,
+                __builtin_amdgcn_readfirstlane(at + (step * TM + row) * 4));
+    }
+  };
+  const auto* const ws = reinterpret_cast<const __attribute__((address_space(4))) float*>((uintptr_t)A.ws) +
+                         (int64_t)(min(n0 + 16 * NF * wn, A.N - 1) / kBlock) * A.blocks;
+
+  v4f acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) acc[i][j] = v4f{};
+
+  const int full = A.K / kBlock;  // blocks that are whole
+  // which way a block's loads are made: there is none, whole blocks, any block
+  enum { kNone, kWhole, kAny };
+  const auto load_step = [&](auto kind, int b, int i) __attribute__((always_inline)) {
+    if constexpr (kind == kWhole) load(b, i);
+    else if constexpr (kind == kAny) load_any(b, i);
+  };
+  load_scales(0);
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) load_any(0, i);
+  if (A.blocks > 1) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load_any(1, i);
+    dma_wait<kLoads>();
+  } else {
+    dma_wait<0>();
+  }
+  tile_barrier();
+  const int at = r * kBlock + ((g ^ (r >> 1 & 7)) << 4);
+  const char* tw = s_tile + wn * (16 * NF * kBlock) + at;
+  const char* tx = s_tile + TN * kBlock + wm * (16 * MF * kBlock) + at;
+  const auto read = [&](const char* tile, int u) __attribute__((always_inline)) {
+    const char* const other = s_tile + ((uint32_t)(tile - s_tile) ^ 64u);
+    return cat8(lds_read<v4i>(tile + u * 2048), lds_read<v4i>(other + u * 2048));
+  };
+  v8i fx[MF], fw[2];
+  float s[2][MF];  // scales of this step and the last one's
+  v4f p[MF];
+#pragma unroll
+  for (int j = 0; j < MF; ++j) {
+    fx[j] = read(tx, j);
+    p[j] = v4f{};
+    s[0][j] = 0.f;
+  }
+  fw[0] = read(tw, 0);
+  const auto step = [&](auto next, auto after, int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < MF; ++j) s[1][j] = s[0][j];
+    // no branch between products: the compiler would move sums behind it and keep every product until then
+    if (b % kScaleSteps == 0 && b + kScaleSteps < A.blocks) load_scales(b + kScaleSteps);
+    const float wsb = ws[b];
+#pragma unroll
+    for (int j = 0; j < MF; ++j) s[0][j] = s_xs[b / kScaleSteps & 1][b % kScaleSteps][16 * MF * wm + 16 * j + r] * wsb;
+    constexpr int kMiddle = NF / 2 - 1, kLast = NF - 1;
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      // what a wait leaves outstanding are the loads that were made after the ones it is for
+      if (i == kMiddle) {
+        dma_wait<next != kNone ? kLoads : 0>();
+        tile_barrier();
+      }
+      if (i < kLast) {
+        fw[(i + 1) & 1] = read(tw, i + 1);
+      } else if constexpr (next != kNone) {
+        dma_wait<after != kNone ? kLoads : kLoadsW>();
+        tile_barrier();
+        tw = s_tile + ((uint32_t)(tw - s_tile) ^ (uint32_t)kImage);
+        tx = s_tile + ((uint32_t)(tx - s_tile) ^ (uint32_t)kImage);
+        fw[0] = read(tw, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < MF; ++j) {
+        __builtin_amdgcn_sched_barrier(0);
+        v4f& sum = acc[i > 0 ? i - 1 : kLast][j];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum[u] = fmaf(s[i > 0 ? 0 : 1][j], p[j][u], sum[u]);
+        __builtin_amdgcn_sched_barrier(0);
+        p[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw[i & 1], fx[j], v4f{}, 0, 0, 0, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i == kLast) {
+          if constexpr (next != kNone) fx[j] = read(tx, j);
+          if (j < kLoadsW) load_step(after, b + 2, kFirst + j);
+        } else if (i >= kMiddle && (i - kMiddle) * MF + j < kFirst) {
+          load_step(after, b + 2, (i - kMiddle) * MF + j);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const std::integral_constant<int, kWhole> whole;
+  const std::integral_constant<int, kAny> any;
+  const std::integral_constant<int, kNone> none;
+  int b = 0;
+  if (n0 + TN <= A.N && m0 + TM <= A.M)
+    for (; b + 2 < full; ++b) step(whole, whole, b);
+  for (; b + 2 < A.blocks; ++b) step(any, any, b);
+  if (b + 1 < A.blocks) step(any, none, b++);
+  step(none, none, b);
+#pragma unroll
+  for (int j = 0; j < MF; ++j)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc[NF - 1][j][u] = fmaf(s[0][j], p[j][u], acc[NF - 1][j][u]);
+
+#pragma unroll
+  for (int j = 0; j < MF; ++j) {
+    const int m = m0 + 16 * MF * wm + 16 * j + r;
+    if (m >= A.M) continue;
+    E* const row = static_cast<E*>(A.out) + (int64_t)m * A.out_row;
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      const int n = n0 + 16 * NF * wn + 16 * i + 4 * g;
+      store4(row + n, acc[i][j], A.N - n);
+    }
   }
 }
 
@@ -115,21 +359,47 @@ __global__ __launch_bounds__(512) void k_matmul_few(MatArgs A) {
 
 static inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-size_t matmul_e4m3_workspace_bytes(int32_t M, int32_t N, int32_t K) {
-  if (M < 0 || N < 1 || K < 1 || (K & 15)) return 0;
-  return 256;
+template <class E, int NF, int MF, int W, int D>
+static void launch_few(const MatArgs& A, hipStream_t stream) {
+  const int64_t grid = (int64_t)((A.N + 16 * NF - 1) / (16 * NF)) * ((A.M + 16 * MF - 1) / (16 * MF));
+  k_matmul_few<E, NF, MF, W, D><<<dim3((uint32_t)grid), dim3(64 * W), 0, stream>>>(A);
+}
+template <class E, int NF, int MF, int WN, int WM>
+static void launch_tiles(const MatArgs& A, hipStream_t stream) {
+  constexpr int TN = 16 * NF * WN, TM = 16 * MF * WM;
+  const int64_t grid = (int64_t)((A.N + TN - 1) / TN) * ((A.M + TM - 1) / TM);
+  k_matmul_tiles<E, NF, MF, WN, WM><<<dim3((uint32_t)grid), dim3(64 * WN * WM), 0, stream>>>(A);
 }
 
+// Up to 32 rows the weights are streamed: as many columns a workgroup as leave one to a unit.  Beyond that the tile is
+// the one whose rounds over the chip take the least: a block of a round takes about 0.28 us of a unit with 64 x 64,
+// 0.64 with 128 x 128 and 2.0 with 256 x 256 (1024 x 4096 x 5120: 57, 31 and 68 us; 777 x 768 x 5120: 16, 27 and 65;
+// 4096 x 12288 x 5120: 660, 302 and 254).
 template <class E>
 static int launch_matmul(const MatArgs& A, hipStream_t stream) {
-  const dim3 grid((A.N + 63) / 64, (A.M + 63) / 64, A.splits);
-  k_matmul_few<E, 4, 4><<<grid, dim3(512), 0, stream>>>(A);
+  const auto tiles = [&](int64_t n, int64_t m) { return ((A.N + n - 1) / n) * ((A.M + m - 1) / m); };
+  const auto cost = [&](int64_t size, int64_t of_round) { return (tiles(size, size) + kUnits - 1) / kUnits * of_round; };
+  if (tiles(16, 16) > 0x7fffff) return IDX_EUNSUPPORTED;  // a launch dimension takes fewer than 2^32 threads
+  if (A.M <= 16) {
+    if (A.N <= 16 * kUnits) launch_few<E, 1, 1, 8, 4>(A, stream);
+    else if (A.N <= 32 * kUnits) launch_few<E, 2, 1, 8, 3>(A, stream);
+    else launch_few<E, 3, 1, 4, 4>(A, stream);
+  } else if (A.M <= 32) {
+    if (A.N <= 32 * kUnits) launch_few<E, 2, 2, 8, 2>(A, stream);
+    else launch_few<E, 4, 2, 4, 3>(A, stream);
+  } else if (cost(64, 28) <= cost(128, 64)) {
+    launch_few<E, 4, 4, 4, 2>(A, stream);
+  } else if (cost(128, 64) <= cost(256, 200)) {
+    launch_tiles<E, 4, 4, 2, 2>(A, stream);
+  } else {
+    launch_tiles<E, 8, 4, 2, 4>(A, stream);
+  }
   return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
 
 int matmul_e4m3(const uint8_t* x, int64_t x_row, const float* x_scale, int32_t x_group, const uint8_t* w,
                 const float* w_scale, int32_t M, int32_t N, int32_t K, int32_t dtype, void* out, int64_t out_row,
-                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                hipStream_t stream) {
   if (M < 0 || N < 1 || K < 1 || (K & 15) || x_row < 0 || (x_row & 15) || out_row < 0) return IDX_EINVAL;
   if (dtype != IDX_TOPK_BF16 && dtype != IDX_TOPK_F16) return IDX_EINVAL;
   if (x_group != 0 && x_group != kBlock) return IDX_EUNSUPPORTED;
@@ -139,11 +409,8 @@ int matmul_e4m3(const uint8_t* x, int64_t x_row, const float* x_scale, int32_t x
   if (!x || !x_scale || !w || !w_scale || !out || !aligned16(x) || !aligned16(w) || !aligned16(out) ||
       (((uintptr_t)x_scale | (uintptr_t)w_scale) & 3u))
     return IDX_EINVAL;
-  const size_t need = matmul_e4m3_workspace_bytes(M, N, K);
-  if (!workspace || workspace_bytes < need) return IDX_EWORKSPACE;
-  if (((uintptr_t)workspace & 255u) != 0) return IDX_EINVAL;
   const int32_t blocks = (K + kBlock - 1) / kBlock;
-  const MatArgs A{x, x_row, x_scale, x_group ? blocks : 1, x_group ? 1 : 0, w, w_scale, M, N, K, blocks, out, out_row, nullptr, 1};
+  const MatArgs A{x, x_row, x_scale, x_group ? blocks : 1, x_group ? 1 : 0, w, w_scale, M, N, K, blocks, out, out_row};
   return dtype == IDX_TOPK_BF16 ? launch_matmul<__bf16>(A, stream) : launch_matmul<_Float16>(A, stream);
 }
 

@@ -9,9 +9,8 @@
 
 namespace idxk {
 
-size_t matmul_e4m3_workspace_bytes(int32_t M, int32_t N, int32_t K);
 int matmul_e4m3(const uint8_t* x, int64_t x_row, const float* x_scale, int32_t x_group, const uint8_t* w,
                 const float* w_scale, int32_t M, int32_t N, int32_t K, int32_t dtype, void* out, int64_t out_row,
-                void* workspace, size_t workspace_bytes, hipStream_t stream);
+                hipStream_t stream);
 
 }  // namespace idxk
