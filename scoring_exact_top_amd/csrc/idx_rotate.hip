@@ -12,6 +12,7 @@
 // (interleaved) or p, p + 32 (halves).  The angles' cosines and sines come from a table in
 // FP32, which the caller computes in 64 bits: in FP32 the angle itself would be off by 2^-8 at
 // position 65536.
+#include "idx_attn.hpp"
 #include "idx_latent.hpp"
 #include "idx_quant.hpp"
 #include "idx_rotate.hpp"
@@ -20,6 +21,7 @@ namespace idxk {
 
 constexpr int kRopeChunks = kRope / 8;  // a rotary part's chunks of 8 numbers
 constexpr int kMaxHead = 1024;          // numbers of a head at most
+constexpr int64_t kManyRows = 1 << 14;  // heads a lane group takes four of
 
 struct RotArgs {
   const void* x;
@@ -30,55 +32,79 @@ struct RotArgs {
   const int32_t* positions;
   const float* table;
   int32_t table_rows, rope_at, interleaved;
-  int32_t rows, H, D;
+  int32_t T, H, D;
+  float inv_d;
+  int64_t units;  // groups of lanes with heads of one token each
   void* out;
   int64_t out_token, out_head;
   uint8_t* codes;
   float* scales;
 };
 
+// The value of the lane that `CTRL` names: l ^ 1 and l ^ 2 (quad permutations), 7 - l of 8 and 15 - l of 16.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;
+template <int CTRL>
+__device__ __forceinline__ uint32_t lane_move(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xf, 0xf, true);
+}
+// Sum and largest over N = 8, 16 or 64 neighbouring lanes, the same bits in all of them.
 template <int N>
 __device__ __forceinline__ float sum_lanes(float x) {
-#pragma unroll
-  for (int d = 1; d < N; d <<= 1) x += __shfl_xor(x, d, 64);
+  const auto f = [](uint32_t u) { return __uint_as_float(u); };
+  x += f(lane_move<kXor1>(__float_as_uint(x)));
+  x += f(lane_move<kXor2>(__float_as_uint(x)));
+  x += f(lane_move<kMirror8>(__float_as_uint(x)));
+  if (N >= 16) x += f(lane_move<kMirror16>(__float_as_uint(x)));
+  return N == 64 ? sum_quarters(x) : x;
+}
+template <int N>
+__device__ __forceinline__ uint32_t max_lanes(uint32_t x) {
+  x = max(x, lane_move<kXor1>(x));
+  x = max(x, lane_move<kXor2>(x));
+  x = max(x, lane_move<kMirror8>(x));
+  if (N >= 16) x = max(x, lane_move<kMirror16>(x));
+  if (N == 64) {
+    const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = max(h[0], h[1]);
+    const auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = max(q[0], q[1]);
+  }
   return x;
 }
 
-// 1 / sqrt(mean square): NaN for a row with a NaN or an infinity, or whose squares leave FP32.
-__device__ __forceinline__ float rstd_of(float ms) { return ms < INFINITY ? 1.f / sqrtf(ms) : NAN; }
-// ... and 0 without eps: zeros stay zeros, and numbers whose squares are lost have no norm.
-__device__ __forceinline__ float unnormed(float x) { return x == 0.f ? 0.f : INFINITY; }
-
-// A row's part of a lane, to its norm: y = (x - mean) * rstd * weight + bias.
+// A row's norm: y = (x - mean) * (rstd * weight) + bias.
 struct Norm {
   float mean, rstd;
-  bool lost;  // mean square 0
-  template <class E>
-  __device__ __forceinline__ float operator()(float x, E w, bool has_w, E b, bool has_b) const {
+  // rstd from the mean square: NaN for a row with a NaN or an infinity, or whose squares leave FP32.  The
+  // instruction is within one unit of the last place and takes no subnormal numbers.
+  __device__ __forceinline__ Norm(float mean, float ms)
+      : mean(mean), rstd(ms < INFINITY ? (ms > 0x1p-100f ? __builtin_amdgcn_rsqf(ms) : 1.f / sqrtf(ms)) : NAN) {}
+  // Mean square 0 (without eps): zeros stay zeros, and numbers whose squares are lost have no norm.
+  __device__ __forceinline__ float operator()(float x, float w, float b) const {
     x -= mean;
-    float y = (lost ? unnormed(x) : x) * rstd;
-    if (has_w) y *= (float)w;
-    if (has_b) y += (float)b;
-    return y;
+    const float y = fmaf(x, rstd * w, b);
+    return rstd < INFINITY || rstd != rstd ? y : fmaf(x == 0.f ? 0.f : INFINITY, w, b);
   }
 };
 
 // Rows (a head of a token) in chunks of 8 numbers, one 16-byte load each: LPR lanes a row, NC
-// chunks a lane.  At most one of a lane's chunks lies in the rotary part, which is 8 chunks
-// long.  Where its pairs are halves, the chunk that holds the partners is 4 chunks away, in
-// another lane or another register: it is loaded a second time (from the cache) and normed as
-// well, which is cheaper than an exchange at any offset.  All lanes of a row are in one wave and
-// have read it before one writes, so that out may be x.
-template <class E, int LPR, int NC, bool QUANT>
+// chunks a lane, HP heads of one token one after another, which share position and angles.  At
+// most one of a lane's chunks lies in the rotary part, which is 8 chunks long.  Where its pairs are
+// halves, the chunk that holds the partners is 4 chunks away, in another lane or another
+// register: it is loaded a second time (from the cache) and normed as well, which is cheaper than
+// an exchange at any offset.  All lanes of a row are in one wave and have read it before one
+// writes, so that out may be x.
+template <class E, int LPR, int NC, int HP, bool QUANT>
 __global__ __launch_bounds__(256) void k_norm_rotate(RotArgs A) {
   typedef E v8 __attribute__((ext_vector_type(8)));
   const int tid = threadIdx.x, at = tid % LPR;
-  const int64_t row = workgroup() * (256 / LPR) + tid / LPR;
-  const bool in = row < A.rows;
-  const uint32_t t = in ? (uint32_t)row / (uint32_t)A.H : 0, head = in ? (uint32_t)row % (uint32_t)A.H : 0;
+  const int64_t unit = workgroup() * (256 / LPR) + tid / LPR;
+  const uint32_t per = (uint32_t)(A.H + HP - 1) / HP;  // units of a token
+  const bool in = unit < A.units;
+  const uint32_t t = in ? (uint32_t)unit / per : 0, head0 = in ? (uint32_t)unit % per * HP : 0;
   const int chunks = A.D >> 3, r0 = A.rope_at >> 3;
   const int pos = in ? A.positions[t] : -1;
-  const E* x = static_cast<const E*>(A.x) + (int64_t)t * A.x_token + (int64_t)head * A.x_head;
+  const E* x = static_cast<const E*>(A.x) + (int64_t)t * A.x_token + (int64_t)head0 * A.x_head;
   const E *w = static_cast<const E*>(A.weight), *b = static_cast<const E*>(A.bias);
 
   const int turn = at >= r0 ? at : at + (r0 - at + LPR - 1) / LPR * LPR;  // this lane's chunk of the rotary part
@@ -87,130 +113,156 @@ __global__ __launch_bounds__(256) void k_norm_rotate(RotArgs A) {
   const bool halves = !A.interleaved;
   const int other = turn + (ci < 4 ? 4 : -4);
 
-  float h[NC][8], p[8];
-  {
-    v8 xv[NC], pv = {};
+  v8 xv[HP][NC], pv[HP];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) xv[c] = in && at + c * LPR < chunks ? *reinterpret_cast<const v8*>(x + 8 * (at + c * LPR)) : v8{};
-    if (turns && halves) pv = *reinterpret_cast<const v8*>(x + 8 * other);
+  for (int k = 0; k < HP; ++k) {
+    const bool there = in && (int)head0 + k < A.H;
+    const E* xk = x + k * A.x_head;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[c][j] = (float)xv[c][j];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = (float)pv[j];
+    for (int c = 0; c < NC; ++c) xv[k][c] = there && at + c * LPR < chunks ? *reinterpret_cast<const v8*>(xk + 8 * (at + c * LPR)) : v8{};
+    pv[k] = there && turns && halves ? *reinterpret_cast<const v8*>(xk + 8 * other) : v8{};
   }
   const bool live = pos >= 0 && pos < A.table_rows;
-  float cs[8], sn[8];  // halves: the chunk's 8 angles; interleaved: its 4
+  // halves: the chunk's 8 angles, interleaved: its 4; a lane that does not turn has angle 0
+  float cs[8], sn[8];
   {
     const float* angle = A.table + (int64_t)(live ? pos : 0) * kRope + (turns ? (halves ? 8 * (ci & 3) : 4 * ci) : 0);
     const bool need = turns && live;
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 c0 = need ? *reinterpret_cast<const float4*>(angle) : zero;
-    const float4 s0 = need ? *reinterpret_cast<const float4*>(angle + kRope / 2) : zero;
-    const float4 c1 = need && halves ? *reinterpret_cast<const float4*>(angle + 4) : zero;
-    const float4 s1 = need && halves ? *reinterpret_cast<const float4*>(angle + kRope / 2 + 4) : zero;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f), one = make_float4(1.f, 1.f, 1.f, 1.f);
+    float4 c0 = one, c1 = one, s0 = zero, s1 = zero;
+    if (need) {
+      c0 = *reinterpret_cast<const float4*>(angle);
+      s0 = *reinterpret_cast<const float4*>(angle + kRope / 2);
+      if (halves) {
+        c1 = *reinterpret_cast<const float4*>(angle + 4);
+        s1 = *reinterpret_cast<const float4*>(angle + kRope / 2 + 4);
+      }
+    }
+    const float sign = halves && ci < 4 ? -1.f : 1.f;  // a cos - b sin, b cos + a sin
     cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w; cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
-    sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
+    sn[0] = s0.x * sign; sn[1] = s0.y * sign; sn[2] = s0.z * sign; sn[3] = s0.w * sign;
+    sn[4] = s1.x * sign; sn[5] = s1.y * sign; sn[6] = s1.z * sign; sn[7] = s1.w * sign;
   }
-  if (A.norm != IDX_TOPK_NORM_NONE) {
-    Norm norm{0.f, 1.f, false};
-    float sum = 0.f;
-    if (A.norm == IDX_TOPK_NORM_LAYER) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += h[c][j];
-      norm.mean = sum_lanes<LPR>(sum) / (float)A.D;
-    }
-    sum = 0.f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = at + c * LPR < chunks ? h[c][j] - norm.mean : 0.f;
-        sum = fmaf(d, d, sum);
-      }
-    const float ms = sum_lanes<LPR>(sum) / (float)A.D + A.eps;
-    norm.lost = ms == 0.f;
-    norm.rstd = norm.lost ? 1.f : rstd_of(ms);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int i = at + c * LPR;
-      v8 wv = {}, bv = {};
-      if (w && i < chunks) wv = *reinterpret_cast<const v8*>(w + 8 * i);
-      if (b && i < chunks) bv = *reinterpret_cast<const v8*>(b + 8 * i);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[c][j] = i < chunks ? norm(h[c][j], (E)wv[j], w != nullptr, (E)bv[j], b != nullptr) : 0.f;
-    }
-    if (turns && halves) {
-      v8 wv = {}, bv = {};
-      if (w) wv = *reinterpret_cast<const v8*>(w + 8 * other);
-      if (b) bv = *reinterpret_cast<const v8*>(b + 8 * other);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = norm(p[j], (E)wv[j], w != nullptr, (E)bv[j], b != nullptr);
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    if (!turns || at + c * LPR != turn) continue;
-    if (halves) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[c][j] = fmaf(h[c][j], cs[j], ci < 4 ? -(p[j] * sn[j]) : p[j] * sn[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float u = h[c][2 * j], v = h[c][2 * j + 1];
-        h[c][2 * j] = fmaf(u, cs[j], -(v * sn[j]));
-        h[c][2 * j + 1] = fmaf(v, cs[j], u * sn[j]);
-      }
-    }
-  }
-  uint32_t top = 0;
-  if (QUANT) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = max(top, magnitude(h[c][j]));
-#pragma unroll
-    for (int d = 1; d < LPR; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d, 64));
-  }
-  if (!live) return;
-  const float scale = scale_of(top);
-  const Scaler to(scale);
-  E* out = static_cast<E*>(A.out) + (int64_t)t * A.out_token + (int64_t)head * A.out_head;
+  const v8 ones = {(E)1.f, (E)1.f, (E)1.f, (E)1.f, (E)1.f, (E)1.f, (E)1.f, (E)1.f};
+  v8 wv[NC], bv[NC], pw = ones, pb = {};  // weight and bias of this lane's chunks and of its partners
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int i = at + c * LPR;
-    if (i >= chunks) break;
-    if (QUANT) {
-      uint2 v;
-      v.x = e4m3x2_enc(to(h[c][0]), to(h[c][1])) | e4m3x2_enc(to(h[c][2]), to(h[c][3])) << 16;
-      v.y = e4m3x2_enc(to(h[c][4]), to(h[c][5])) | e4m3x2_enc(to(h[c][6]), to(h[c][7])) << 16;
-      if (!finite(top)) v.x = v.y = kNanCodes;
-      *reinterpret_cast<uint2*>(A.codes + row * A.D + 8 * i) = v;
-      if (i == 0) A.scales[row] = scale;
-    } else {
-      v8 v;
+    wv[c] = w && i < chunks ? *reinterpret_cast<const v8*>(w + 8 * i) : ones;
+    bv[c] = b && i < chunks ? *reinterpret_cast<const v8*>(b + 8 * i) : v8{};
+  }
+  if (w && turns && halves) pw = *reinterpret_cast<const v8*>(w + 8 * other);
+  if (b && turns && halves) pb = *reinterpret_cast<const v8*>(b + 8 * other);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (E)h[c][j];
-      *reinterpret_cast<v8*>(out + 8 * i) = v;
+  for (int k = 0; k < HP; ++k) {
+    float h[NC][8], p[8];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[c][j] = (float)xv[k][c][j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = (float)pv[k][j];
+    if (A.norm != IDX_TOPK_NORM_NONE) {
+      float sum = 0.f, mean = 0.f;
+      if (A.norm == IDX_TOPK_NORM_LAYER) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum += h[c][j];
+        mean = sum_lanes<LPR>(sum) * A.inv_d;
+      }
+      sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = at + c * LPR < chunks ? h[c][j] - mean : 0.f;
+          sum = fmaf(d, d, sum);
+        }
+      const Norm norm(mean, fmaf(sum_lanes<LPR>(sum), A.inv_d, A.eps));
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int i = at + c * LPR;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[c][j] = i < chunks ? norm(h[c][j], (float)wv[c][j], (float)bv[c][j]) : 0.f;
+      }
+      if (turns && halves) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = norm(p[j], (float)pw[j], (float)pb[j]);
+      }
+    }
+    if (turns) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        if (NC > 1 && at + c * LPR != turn) continue;
+        if (halves) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[c][j] = fmaf(h[c][j], cs[j], p[j] * sn[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float u = h[c][2 * j], v = h[c][2 * j + 1];
+            h[c][2 * j] = fmaf(u, cs[j], -(v * sn[j]));
+            h[c][2 * j + 1] = fmaf(v, cs[j], u * sn[j]);
+          }
+        }
+      }
+    }
+    uint32_t top = 0;
+    if (QUANT) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, magnitude(h[c][j]));
+      top = max_lanes<LPR>(top);
+    }
+    if (!live || (int)head0 + k >= A.H) continue;
+    const int64_t row = (int64_t)t * A.H + head0 + k;
+    const float scale = scale_of(top);
+    const Scaler to(scale);
+    E* out = static_cast<E*>(A.out) + (int64_t)t * A.out_token + (int64_t)(head0 + k) * A.out_head;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int i = at + c * LPR;
+      if (i >= chunks) break;
+      if (QUANT) {
+        uint2 v;
+        v.x = e4m3x2_enc(to(h[c][0]), to(h[c][1])) | e4m3x2_enc(to(h[c][2]), to(h[c][3])) << 16;
+        v.y = e4m3x2_enc(to(h[c][4]), to(h[c][5])) | e4m3x2_enc(to(h[c][6]), to(h[c][7])) << 16;
+        if (!finite(top)) v.x = v.y = kNanCodes;
+        *reinterpret_cast<uint2*>(A.codes + row * A.D + 8 * i) = v;
+        if (i == 0) A.scales[row] = scale;
+      } else {
+        v8 v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (E)h[c][j];
+        *reinterpret_cast<v8*>(out + 8 * i) = v;
+      }
     }
   }
 }
 
-// Lanes a row and chunks a lane: the fewest idle lanes among shapes that keep a row in 16 lanes.
+// Lanes a row and chunks a lane: the fewest idle lanes among shapes that keep a row in 16 lanes.  Four
+// heads a lane where there are enough rows to fill the chip so (2^14 rows: one wave a SIMD).
 template <class E, bool QUANT>
-static void launch_rotate(const RotArgs& A, hipStream_t stream) {
+static void launch_rotate(RotArgs A, hipStream_t stream) {
   const int chunks = A.D >> 3;
-  const auto grid = [&](int lpr) { return grid_of(((int64_t)A.rows * lpr + 255) / 256); };
-  if (chunks <= 8) k_norm_rotate<E, 8, 1, QUANT><<<grid(8), dim3(256), 0, stream>>>(A);
-  else if (chunks <= 16) k_norm_rotate<E, 16, 1, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
-  else if (chunks <= 24) k_norm_rotate<E, 8, 3, QUANT><<<grid(8), dim3(256), 0, stream>>>(A);
-  else if (chunks <= 32) k_norm_rotate<E, 16, 2, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
-  else if (chunks <= 48) k_norm_rotate<E, 16, 3, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
-  else if (chunks <= 80) k_norm_rotate<E, 16, 5, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
-  else k_norm_rotate<E, 16, 8, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
+  const bool many = (int64_t)A.T * A.H >= kManyRows && A.H >= 4;
+  A.units = (int64_t)A.T * (many && chunks <= 24 ? (A.H + 3) / 4 : A.H);
+  const auto grid = [&](int lpr) { return grid_of((A.units * lpr + 255) / 256); };
+  if (chunks <= 8) {
+    if (many) k_norm_rotate<E, 8, 1, 4, QUANT><<<grid(8), dim3(256), 0, stream>>>(A);
+    else k_norm_rotate<E, 8, 1, 1, QUANT><<<grid(8), dim3(256), 0, stream>>>(A);
+  } else if (chunks <= 16) {
+    if (many) k_norm_rotate<E, 16, 1, 4, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
+    else k_norm_rotate<E, 16, 1, 1, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
+  } else if (chunks <= 24) {
+    if (many) k_norm_rotate<E, 8, 3, 4, QUANT><<<grid(8), dim3(256), 0, stream>>>(A);
+    else k_norm_rotate<E, 8, 3, 1, QUANT><<<grid(8), dim3(256), 0, stream>>>(A);
+  } else if (chunks <= 32) k_norm_rotate<E, 16, 2, 1, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 48) k_norm_rotate<E, 16, 3, 1, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
+  else if (chunks <= 80) k_norm_rotate<E, 16, 5, 1, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
+  else k_norm_rotate<E, 16, 8, 1, QUANT><<<grid(16), dim3(256), 0, stream>>>(A);
 }
 
 struct AppendRotArgs {
@@ -295,11 +347,9 @@ __global__ __launch_bounds__(256) void k_append_rotary(AppendRotArgs A) {
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum = fmaf((float)xv[j], (float)xv[j], sum);
-      const float ms = sum_lanes<64>(sum) / (float)kLatent + A.latent_eps;
-      const bool lost = ms == 0.f;
-      const Norm norm{0.f, lost ? 1.f : rstd_of(ms), lost};
+      const Norm norm(0.f, fmaf(sum_lanes<64>(sum), 1.f / kLatent, A.latent_eps));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xv[j] = (E)norm((float)xv[j], (E)wv[j], A.latent_weight != nullptr, (E)0.f, false);
+      for (int j = 0; j < 8; ++j) xv[j] = (E)norm((float)xv[j], A.latent_weight ? (float)wv[j] : 1.f, 0.f);
     }
     dst[lane] = xv;
     if (out) out[lane] = xv;
@@ -307,12 +357,10 @@ __global__ __launch_bounds__(256) void k_append_rotary(AppendRotArgs A) {
   if (A.k_cache) {
     float a = (float)kv[0], b = (float)kv[1];
     if (A.key_norm != IDX_TOPK_NORM_NONE) {
-      const float mean = A.key_norm == IDX_TOPK_NORM_LAYER ? sum_lanes<64>(a + b) / (float)kD : 0.f;
-      const float ms = sum_lanes<64>(fmaf(a - mean, a - mean, (b - mean) * (b - mean))) / (float)kD + A.key_eps;
-      const bool lost = ms == 0.f;
-      const Norm norm{mean, lost ? 1.f : rstd_of(ms), lost};
-      a = norm(a, (E)kw[0], A.key_weight != nullptr, (E)kb[0], A.key_bias != nullptr);
-      b = norm(b, (E)kw[1], A.key_weight != nullptr, (E)kb[1], A.key_bias != nullptr);
+      const float mean = A.key_norm == IDX_TOPK_NORM_LAYER ? sum_lanes<64>(a + b) * (1.f / kD) : 0.f;
+      const Norm norm(mean, fmaf(sum_lanes<64>(fmaf(a - mean, a - mean, (b - mean) * (b - mean))), 1.f / kD, A.key_eps));
+      a = norm(a, A.key_weight ? (float)kw[0] : 1.f, (float)kb[0]);
+      b = norm(b, A.key_weight ? (float)kw[1] : 1.f, (float)kb[1]);
     }
     const int c = lane - A.key_rope_at / 2;  // this lane's two numbers of the rotary part
     const bool turns = c >= 0 && c < kRope / 2;
@@ -330,7 +378,7 @@ __global__ __launch_bounds__(256) void k_append_rotary(AppendRotArgs A) {
         b = fmaf(b, cs.y, c < 16 ? -(pb * sn.y) : pb * sn.y);
       }
     }
-    const uint32_t top = wave_max(max(magnitude(a), magnitude(b)));
+    const uint32_t top = max_lanes<64>(max(magnitude(a), magnitude(b)));
     const float scale = scale_of(top);
     const Scaler to(scale);
     reinterpret_cast<uint16_t*>(A.k_cache + slot * kD)[lane] = (uint16_t)(finite(top) ? e4m3x2_enc(to(a), to(b)) : kNanCodes);
@@ -370,7 +418,7 @@ int norm_rotate(const void* x, int64_t x_token, int64_t x_head, int32_t norm, co
   const bool apart = (T > 1 && x_token != out_token) || (H > 1 && x_head != out_head);
   if (out == x && apart) return IDX_EINVAL;
   const RotArgs A{x, x_token, x_head, weight, bias, eps, norm, positions, table, table_rows, rope_at, interleaved ? 1 : 0,
-                  T * H, H, D, out, out_token, out_head, codes, scales};
+                  T, H, D, 1.f / (float)D, 0, out, out_token, out_head, codes, scales};
   if (dtype == IDX_TOPK_BF16) {
     if (codes) launch_rotate<__bf16, true>(A, stream);
     else launch_rotate<__bf16, false>(A, stream);
