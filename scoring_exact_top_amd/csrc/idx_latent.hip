@@ -108,13 +108,7 @@ __device__ __forceinline__ int tree_nodes(const LatArgs& A, int b) {
   return p < 0 || n < 0 || n > A.S || (int64_t)p + n > (int64_t)A.K * IDX_TOPK_PAGE ? 0 : n;
 }
 
-// Keys of a sequence: of a tree's, committed and drafted (none without drafted tokens, which alone see them).
-template <int MODE>
 __device__ __forceinline__ int seq_len(const LatArgs& A, int b) {
-  if (MODE == kTree) {
-    const int n = tree_nodes(A, b);
-    return n ? A.lens[b] + n : 0;
-  }
   const int n = A.lens[b];
   return n < 0 || (int64_t)n > (int64_t)A.K * IDX_TOPK_PAGE ? 0 : n;
 }
@@ -123,7 +117,7 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   if (A.parts == A.B) return Part{wg, 0, 1, 0};
   int64_t total = 0;
   for (int b0 = 0; b0 < A.B; b0 += 64) {
-    const int n = b0 + lane < A.B ? (seq_len<kPaged>(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
     total += __shfl(wave_incl_scan(n, lane), 63, 64);
   }
   // sum of max(1, ceil(n / unit)) <= total / unit + B <= parts
@@ -131,7 +125,7 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   unit = unit < kMinPages ? kMinPages : unit;
   int base = 0;  // sums over the sequences before: parts, and 2^16 x parts with a cell (2^11 at most each)
   for (int b0 = 0; b0 < A.B; b0 += 64) {
-    const int n = b0 + lane < A.B ? (seq_len<kPaged>(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
     const int parts = b0 + lane < A.B ? max(1, (n + unit - 1) / unit) : 0;
     const int both = parts > 1 ? parts << 16 | parts : parts;
     const int end = base + wave_incl_scan(both, lane);
@@ -158,10 +152,11 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
 constexpr int kBegin = 3;
 
 struct TreeSeq {
-  int nodes, pages, blocks;
+  int nodes, keys, pages, blocks;
   __device__ __forceinline__ TreeSeq(const LatArgs& A, int b, int rows) {
     nodes = b < A.B ? tree_nodes(A, b) : 0;
-    pages = nodes ? (A.lens[b] + nodes + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
+    keys = nodes ? A.lens[b] + nodes : 0;  // of a sequence without drafted tokens nothing is seen
+    pages = (keys + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE;
     blocks = (nodes * A.H + rows - 1) / rows;
   }
 };
@@ -177,7 +172,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) { return (int6
 struct TreeStart {
   int b, block, first, parts;
   int64_t pages, end, total;
-  int shares, wg;
+  int shares, wg, nodes, keys;  // of the sequence
 };
 
 template <class N>
@@ -193,12 +188,21 @@ __device__ __forceinline__ N wave_sum_before(N x, int lane) {  // inclusive
 // N: 32 bits where the work is below 2^22 pages (a plan takes a workgroup 2 us then, in 64 bits 5).
 template <int HG, class N>
 __device__ __forceinline__ TreeStart plan_tree_in(const LatArgs& A, int wg, int lane, N total, N blocks) {
-  TreeStart at{-1, 0, 0, 0, 0, 0, (int64_t)total, 1, wg};
+  TreeStart at{-1, 0, 0, 0, 0, 0, (int64_t)total, 1, wg, 0, 0};
   const N shares = A.parts;
   // sum of ceil(pages / unit) <= total / unit + blocks <= parts
   N unit = blocks < shares ? quotient(total + shares - blocks - 1, shares - blocks) : total + kBegin + 1;
   const bool cut = unit <= quotient(total, shares) + kBegin;
   unit = unit < kMinPages ? kMinPages : unit;
+  if (cut && A.B <= 64) {
+    // that bound is for lengths that just pass a multiple of the unit; a smaller one often fits
+    const TreeSeq t(A, lane, 16 * HG);
+    N u = quotient(total + shares - 1, shares);
+    for (u = u < kMinPages ? kMinPages : u; u < unit; ++u) {
+      const N all = wave_sum_before((N)t.blocks * quotient((N)t.pages + u - 1, u), lane);
+      if (__shfl((std::conditional_t<sizeof(N) == 8, long long, int>)all, 63, 64) <= shares) unit = u;
+    }
+  }
   N from = wg;
   if (!cut) {
     const N most = (total + kMinPages - 1) / kMinPages, n = most < 1 ? 1 : most < shares ? most : shares;
@@ -219,6 +223,8 @@ __device__ __forceinline__ TreeStart plan_tree_in(const LatArgs& A, int wg, int 
       const auto of = [&](N x) { return (N)__shfl((std::conditional_t<sizeof(N) == 8, long long, int>)x, l, 64); };
       const N into = from - of(begin), n = of(parts), pages = of(t.pages), block = quotient(into, n), part = into - block * n;
       at.b = b0 + l;
+      at.nodes = __shfl(t.nodes, l, 64);
+      at.keys = __shfl(t.keys, l, 64);
       at.block = (int)block;
       at.first = (int)part;
       if (cut) {
@@ -301,7 +307,13 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   int len, tile0, tile1;  // keys of the sequence or list, this workgroup's tiles
   if (MODE == kTree) {
     if (wave == 0) {
-      const TreeStart at = A.parts ? plan_tree<HG>(A, work, lane) : TreeStart{wg, rb, 0, 0, INT64_MAX, 0, 0, 0, work};
+      TreeStart at;
+      if (A.parts) {
+        at = plan_tree<HG>(A, work, lane);
+      } else {
+        const TreeSeq t(A, wg, 16 * HG);
+        at = TreeStart{wg, rb, 0, 0, INT64_MAX, 0, 0, 0, work, t.nodes, t.keys};
+      }
       if (lane == 0) {
         s_at = at;
         if (A.parts) A.split[work] = make_int4(0, 0, 0, 0);
@@ -321,7 +333,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     part.part = __builtin_amdgcn_readfirstlane(s_list[1]);
     part.parts = __builtin_amdgcn_readfirstlane(s_list[2]);
     if (part.b < 0) return;
-    len = __builtin_amdgcn_readfirstlane(seq_len<MODE>(A, part.b));
+    len = __builtin_amdgcn_readfirstlane(seq_len(A, part.b));
     const int pages = (len + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE;
     tile0 = 2 * (int)((int64_t)pages * part.part / part.parts);
     tile1 = min(2 * (int)((int64_t)pages * (part.part + 1) / part.parts), (len + kTileKeys - 1) / kTileKeys);
@@ -347,7 +359,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     rb = __builtin_amdgcn_readfirstlane(s_at.block);
     if (part.b < 0) return;
     const int first = __builtin_amdgcn_readfirstlane(s_at.first);
-    len = __builtin_amdgcn_readfirstlane(seq_len<MODE>(A, part.b));
+    len = __builtin_amdgcn_readfirstlane(s_at.keys);
     const int pages = (len + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE;
     const int last = s_at.pages < pages - first ? first + __builtin_amdgcn_readfirstlane((int)s_at.pages) : pages;
     tile0 = 2 * first;
@@ -356,7 +368,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     if (tid == 0 && first == 0 && last < pages) {
       const int64_t to = s_at.end - last + pages;  // the stream's page behind the block
       const int n = s_at.parts ? s_at.parts : (int)quotient(to * s_at.shares - 1, s_at.total) - s_at.wg + 1;
-      A.split[s_at.wg] = make_int4(part.b, rb, n, tree_nodes(A, part.b));
+      A.split[s_at.wg] = make_int4(part.b, rb, n, s_at.nodes);
     }
   }
   const int hg = wave % HG, kg = wave / HG;
@@ -368,14 +380,15 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   int limit = MODE == kPaged ? len - A.S + 1 + step : len;  // this lane's row sees keys below
   int limit_min = MODE == kPaged ? len - A.S + 1 : len;     // every row does
   int q_step = step, nodes = 0;
+  uint64_t mask = 0;
   if (MODE == kTree) {
-    nodes = __builtin_amdgcn_readfirstlane(tree_nodes(A, b));
+    nodes = __builtin_amdgcn_readfirstlane(s_at.nodes);
     limit_min = len - nodes;
     q_step = step < nodes ? step : 0;  // a row of no drafted token repeats the first one's, and is dropped
     // a row's mask, its bits behind the last drafted token cleared
     if (tid < HG * kRowsWave) {
       const int r = rb * HG * kRowsWave + tid, node = r < A.S * A.H ? r / A.H : A.S;
-      s_mask[tid] = node < nodes ? A.masks[b * A.mask_seq + node] & (~0ull >> (64 - nodes)) : 0;
+      mask = node < nodes ? A.masks[b * A.mask_seq + node] & (~0ull >> (64 - nodes)) : 0;
     }
     if (rb * HG * kRowsWave >= nodes * A.H) tile1 = tile0;  // no row of this workgroup is one
   }
@@ -395,6 +408,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 32 * s);
   }
+  if (MODE == kTree && tid < HG * kRowsWave) s_mask[tid] = mask;  // before the barriers of the walk
   if (!PAGED) {
     for (int i = tid; i < n_list; i += 64 * HG * KG) {
       s_list[i] = slot >= 0 && slot < A.num_slots ? slot : -1;
@@ -436,7 +450,14 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     uint32_t dst, live;
     uint32_t lo, hi, rlo[kRope4], rhi[kRope4];
   };
-  const auto source = [&](int t) __attribute__((always_inline)) {
+  // A tile's page id; page 0 of the table stands in for tiles past the end.  A scalar load: vector loads would queue
+  // behind the tile loads.
+  const auto page_of = [&](int t) __attribute__((always_inline)) {
+    const auto* table = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)A.list) + (int64_t)b * A.K;
+    const int key0 = (mine + t * KG) * kTileKeys;
+    return table[t < steps && key0 < len ? key0 / IDX_TOPK_PAGE : 0];
+  };
+  const auto source_at = [&](int t, int pg) __attribute__((always_inline)) {
     Source f;
     f.dst = __builtin_amdgcn_readfirstlane(lds0 + (kg * kRing + t % kRing) * kTileBytes);
     asm volatile("" : "+s"(f.dst));  // the loads' addresses are made from it, not kept in registers
@@ -447,12 +468,8 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     uint64_t page = 0;
     int rows = 0;  // paged: rows of the tile that are there
     if (PAGED) {
-      const int key0 = (mine + t * KG) * kTileKeys;
-      // a scalar load: vector loads would queue behind the tile loads.  A tile
-      // lies in one page; page 0 of the table stands in for tiles past the end
-      const auto* table = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)A.list) + (int64_t)b * A.K;
+      const int key0 = (mine + t * KG) * kTileKeys;  // a tile lies in one page
       const bool some = in && key0 < len;
-      const int pg = table[some ? key0 / IDX_TOPK_PAGE : 0];
       rows = some && pg >= 0 && (int64_t)pg * IDX_TOPK_PAGE < A.num_slots ? min(kTileKeys, len - key0) : 0;
       page = cache + ((int64_t)pg * IDX_TOPK_PAGE + key0 % IDX_TOPK_PAGE) * (kLatRow * 2);
       f.live = rows > 0 ? ~0u : 0u;
@@ -498,7 +515,8 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   };
   Source next;
   uint32_t live[kFlight + 1];  // of this step's tile and the ones in flight
-  const auto load_first = [&]() __attribute__((always_inline)) {
+  const auto source = [&](int t) __attribute__((always_inline)) { return source_at(t, PAGED ? page_of(t) : 0); };
+  const auto load_first = [&](const auto& source) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < kFlight; ++t) {
       next = source(t);
@@ -509,7 +527,16 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     next = source(kFlight);
   };
   if (tid == 0) s_again = 0;  // before the barriers of the walk
-  if (steps > 0) load_first();
+  if constexpr (MODE == kTree) {
+    if (steps > 0) {
+      int pages[kFlight + 1];  // the first tiles' page ids, asked for together
+#pragma unroll
+      for (int t = 0; t <= kFlight; ++t) pages[t] = page_of(t);
+      load_first([&](int t) __attribute__((always_inline)) { return source_at(t, pages[t]); });
+    }
+  } else {
+    if (steps > 0) load_first(source);
+  }
 
   // Waits for step i's tile, computes its logits x, masked, and starts the
   // loads of a later tile on the way (kMore).
@@ -642,7 +669,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     tile_barrier();  // every tile is read, every load done
     if (attempt > 0 || !__builtin_amdgcn_readfirstlane(s_again)) break;
     st = RowStat{-INFINITY, 0.f};
-    load_first();
+    load_first(source);
     walk([&](auto kMore, int i) __attribute__((always_inline)) {
       w4f x[2];
       logits(kMore, i, x);
@@ -651,7 +678,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     st.m -= T::kFullLift;
     dma_wait<0>();
     tile_barrier();
-    load_first();
+    load_first(source);
   }
   float l = sum_quarters(st.l), m = st.m;
   if (MODE == kTree) {
@@ -725,15 +752,17 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   if (MODE != kTree || !A.parts || s_at.parts) return;
   __syncthreads();  // masks, tiles and state are read
   if (tid == 0) {
-    const TreeSeq t(A, s_at.b, 16 * HG);
+    TreeSeq t(A, s_at.b, 16 * HG);
     const int64_t left = s_at.pages - (t.pages - s_at.first);  // a share that goes on took the block to its end
     int next = left > 0 ? s_at.b : -1, block = s_at.block + 1;
     if (next >= 0 && block >= t.blocks) {
       block = 0;
-      do ++next;
-      while (next < A.B && TreeSeq(A, next, 16 * HG).blocks == 0);
+      do t = TreeSeq(A, ++next, 16 * HG);
+      while (next < A.B && t.blocks == 0);
       if (next >= A.B) next = -1;
     }
+    s_at.nodes = t.nodes;
+    s_at.keys = t.keys;
     s_at.b = next;
     s_at.block = block;
     s_at.first = 0;

@@ -34,15 +34,16 @@ struct MatArgs {
   int64_t out_row;
 };
 
-// Four neighbouring columns of a row; `n` of them are there.
+// Four neighbouring columns of a row, at any address (the memory pipeline takes unaligned accesses); `n` of them are there.
 template <class E>
 __device__ __forceinline__ void store4(E* p, v4f v, int n) {
   typedef E e4 __attribute__((ext_vector_type(4)));
+  typedef E e4u __attribute__((ext_vector_type(4), aligned(2)));
   const e4 y = {(E)v[0], (E)v[1], (E)v[2], (E)v[3]};
-  if (n >= 4 && ((uintptr_t)p & (sizeof(E) * 4 - 1)) == 0) *reinterpret_cast<e4*>(p) = y;
+  if (n >= 4) *reinterpret_cast<e4u*>(p) = y;
   else
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 3; ++j)
       if (j < n) p[j] = y[j];
 }
 
@@ -342,15 +343,37 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_matmul_tiles(MatArgs A) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) acc[NF - 1][j][u] = fmaf(s[0][j], p[j][u], acc[NF - 1][j][u]);
 
+  // the sums are made here, not moved behind the branches below with all they are made of
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) asm volatile("" : "+v"(acc[i][j]));
+  // Two fragments' columns 4g .. 4g + 3 of a row: the lanes of odd g hand those of the first to the lane 16 below
+  // and take its ones of the second, so that each has 8 neighbouring columns of one of them.
+  typedef E e4 __attribute__((ext_vector_type(4)));
+  typedef E e8 __attribute__((ext_vector_type(8)));
+  typedef E e8u __attribute__((ext_vector_type(8), aligned(2)));
 #pragma unroll
   for (int j = 0; j < MF; ++j) {
     const int m = m0 + 16 * MF * wm + 16 * j + r;
-    if (m >= A.M) continue;
     E* const row = static_cast<E*>(A.out) + (int64_t)m * A.out_row;
 #pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      const int n = n0 + 16 * NF * wn + 16 * i + 4 * g;
-      store4(row + n, acc[i][j], A.N - n);
+    for (int i = 0; i < NF; i += 2) {
+      const v4f a = acc[i][j], c = acc[i + 1][j];
+      const uint2 u = __builtin_bit_cast(uint2, e4{(E)a[0], (E)a[1], (E)a[2], (E)a[3]});
+      const uint2 v = __builtin_bit_cast(uint2, e4{(E)c[0], (E)c[1], (E)c[2], (E)c[3]});
+      const auto x = __builtin_amdgcn_permlane16_swap(u.x, v.x, false, false);
+      const auto y = __builtin_amdgcn_permlane16_swap(u.y, v.y, false, false);
+      const e8 z = __builtin_bit_cast(e8, make_uint4(x[0], y[0], x[1], y[1]));
+      const int n = n0 + 16 * NF * wn + 16 * (i + (g & 1)) + 8 * (g >> 1);
+      if (m >= A.M) continue;
+      if (n + 8 <= A.N) {
+        *reinterpret_cast<e8u*>(row + n) = z;  // at any address: the memory pipeline takes them
+      } else {
+#pragma unroll
+        for (int k = 0; k < 7; ++k)
+          if (n + k < A.N) row[n + k] = z[k];
+      }
     }
   }
 }
@@ -372,9 +395,10 @@ static void launch_tiles(const MatArgs& A, hipStream_t stream) {
 }
 
 // Up to 32 rows the weights are streamed: as many columns a workgroup as leave one to a unit.  Beyond that the tile is
-// the one whose rounds over the chip take the least: a block of a round takes about 0.28 us of a unit with 64 x 64,
-// 0.64 with 128 x 128 and 2.0 with 256 x 256 (1024 x 4096 x 5120: 57, 31 and 68 us; 777 x 768 x 5120: 16, 27 and 65;
-// 4096 x 12288 x 5120: 660, 302 and 254).
+// the one whose rounds over the chip take the least: a block of a round takes about 0.25 us with 64 x 64, 0.63 with
+// 128 x 128 and 1.9 with 256 x 256 (1024 x 4096 x 5120: 57, 30 and 68 us; 777 x 768 x 5120: 15, 27 and 65;
+// 4096 x 12288 x 5120: 660, 302 and 231).  48 columns instead of 64 where that is one round too: 13.3 against 14.7 us for
+// 777 x 768 x 5120.
 template <class E>
 static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   const auto tiles = [&](int64_t n, int64_t m) { return ((A.N + n - 1) / n) * ((A.M + m - 1) / m); };
@@ -387,9 +411,10 @@ static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   } else if (A.M <= 32) {
     if (A.N <= 32 * kUnits) launch_few<E, 2, 2, 8, 2>(A, stream);
     else launch_few<E, 4, 2, 4, 3>(A, stream);
-  } else if (cost(64, 28) <= cost(128, 64)) {
-    launch_few<E, 4, 4, 4, 2>(A, stream);
-  } else if (cost(128, 64) <= cost(256, 200)) {
+  } else if (cost(64, 25) <= cost(128, 63)) {
+    if (tiles(48, 64) <= kUnits) launch_few<E, 3, 4, 8, 1>(A, stream);
+    else launch_few<E, 4, 4, 8, 1>(A, stream);
+  } else if (cost(128, 63) <= cost(256, 190)) {
     launch_tiles<E, 4, 4, 2, 2>(A, stream);
   } else {
     launch_tiles<E, 8, 4, 2, 4>(A, stream);
