@@ -396,13 +396,16 @@ static void launch_tiles(const MatArgs& A, hipStream_t stream) {
 
 // Up to 32 rows the weights are streamed: as many columns a workgroup as leave one to a unit.  Beyond that the tile is
 // the one whose rounds over the chip take the least: a block of a round takes about 0.25 us with 64 x 64, 0.63 with
-// 128 x 128 and 1.9 with 256 x 256 (1024 x 4096 x 5120: 57, 30 and 68 us; 777 x 768 x 5120: 15, 27 and 65;
-// 4096 x 12288 x 5120: 660, 302 and 231).  48 columns instead of 64 where that is one round too: 13.3 against 14.7 us for
+// 128 x 128 (two of which share a unit, so that beyond the first round each half one counts for itself) and 1.9 with
+// 256 x 256.  Measured, in us with the three tiles: 777 x 768 x 5120 15, 27 and 65; 300 x 12288 x 5120 58, 48 and 74; 1024 x 4096 x 5120 57, 28 and 68;
+// 4096 x 12288 x 5120 660, 302 and 231.  48 columns instead of 64 where that is one round too: 13.3 against 14.7 us for
 // 777 x 768 x 5120.
 template <class E>
 static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   const auto tiles = [&](int64_t n, int64_t m) { return ((A.N + n - 1) / n) * ((A.M + m - 1) / m); };
-  const auto cost = [&](int64_t size, int64_t of_round) { return (tiles(size, size) + kUnits - 1) / kUnits * of_round; };
+  const auto rounds = [&](int64_t size, int64_t units) { return (tiles(size, size) + units - 1) / units; };
+  const int64_t half = rounds(128, kUnits / 2);
+  const int64_t c64 = 50 * rounds(64, kUnits), c128 = 63 * (half < 2 ? 2 : half), c256 = 380 * rounds(256, kUnits);
   if (tiles(16, 16) > 0x7fffff) return IDX_EUNSUPPORTED;  // a launch dimension takes fewer than 2^32 threads
   if (A.M <= 16) {
     if (A.N <= 16 * kUnits) launch_few<E, 1, 1, 8, 4>(A, stream);
@@ -411,10 +414,10 @@ static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   } else if (A.M <= 32) {
     if (A.N <= 32 * kUnits) launch_few<E, 2, 2, 8, 2>(A, stream);
     else launch_few<E, 4, 2, 4, 3>(A, stream);
-  } else if (cost(64, 25) <= cost(128, 63)) {
+  } else if (c64 <= c128 && c64 <= c256) {
     if (tiles(48, 64) <= kUnits) launch_few<E, 3, 4, 8, 1>(A, stream);
     else launch_few<E, 4, 4, 8, 1>(A, stream);
-  } else if (cost(128, 63) <= cost(256, 190)) {
+  } else if (c128 <= c256) {
     launch_tiles<E, 4, 4, 2, 2>(A, stream);
   } else {
     launch_tiles<E, 8, 4, 2, 4>(A, stream);

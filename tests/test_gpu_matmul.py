@@ -39,7 +39,7 @@ def _check(out, x, xs, w, ws, where):
 SIZES = [(1, 1, 16), (1, 7, 128), (2, 130, 48), (3, 64, 144), (5, 257, 1040), (16, 576, 512), (17, 1000, 256), (31, 33, 2064), (1, 4097, 640),
          (33, 128, 4096), (64, 768, 1280), (65, 100, 384), (130, 129, 272), (200, 513, 1024), (257, 255, 2000), (300, 1030, 528),
          (513, 300, 640), (1025, 520, 128), (1501, 1500, 272), (1500, 1537, 2000), (1537, 1408, 128), (3601, 3590, 400), (3333, 3845, 1152),
-         (3840, 3584, 16), (3, 8337, 1168), (16, 12288, 256)]
+         (1000, 1003, 528), (3840, 3584, 16), (3, 8337, 1168), (16, 12288, 256)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -110,7 +110,7 @@ def test_matmul_exact_integers():
     """Small whole numbers whose sums the output holds: the exact product at every size of step."""
     import scoring_exact_top_amd as lib
     g = torch.Generator().manual_seed(13)
-    for M, N, K in ((1, 64, 5120), (16, 128, 16384), (2, 8300, 1280), (30, 8300, 1280), (70, 300, 2176), (512, 512, 1024), (1600, 1500, 2048),
+    for M, N, K in ((1, 64, 5120), (16, 128, 16384), (2, 8300, 1280), (30, 8300, 1280), (70, 300, 2176), (512, 512, 1024), (1000, 1000, 1024), (1600, 1500, 2048),
                     (3600, 3600, 1024)):
         # one number in 16 is not zero: about K / 256 products of at most 4 2^2, multiples of 1/4 (scales 2^-1 .. 2)
         x, w = (torch.randint(-2, 3, (n, K), generator=g).float() * (torch.rand(n, K, generator=g) < 1 / 8) for n in (M, N))
