@@ -189,3 +189,71 @@ def test_tree_views_streams_and_given_buffers():
     got = _call(wide.cuda()[:, :, 1:1 + H, 64:], cache, table, prefix, counts, masks, out=out, lse=lse, workspace=ws, stream=s)
     s.synchronize()
     assert got[0] is out and got[1] is lse and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_tree_stream_of_ragged_blocks():
+    """More blocks than workgroups, of trees and sequences of all sizes: workgroups that end one block, do others
+    whole and begin the next; blocks that many share."""
+    g = torch.Generator().manual_seed(8)
+    B, S, H = 30, 16, 128
+    prefix = [int(n) for n in torch.randint(0, 700, (B,), generator=g)]
+    counts = [int(n) for n in torch.randint(0, S + 1, (B,), generator=g)]
+    prefix[3], counts[3], prefix[4], counts[4] = 15000, 16, 0, 16
+    q, cache, table, masks = _case(prefix, counts, S, H, torch.bfloat16, 9)
+    log("tree stream", prefix, counts)
+    out, lse = _call(q, cache, table, prefix, counts, masks)
+    _check(out, lse, q, cache, table, prefix, counts, masks, nodes=(0, 1, 7, 8, 14, 15), where="stream")
+    again, again_lse = _call(q, cache, table, prefix, counts, masks)
+    assert torch.equal(out, again) and torch.equal(lse, again_lse)
+
+
+def test_tree_many_sequences():
+    """Batches past the one that is shared out: a workgroup a block, padding rows written by it."""
+    g = torch.Generator().manual_seed(10)
+    B, S, H = 1100, 3, 48
+    prefix = [int(n) for n in torch.randint(0, 90, (B,), generator=g)]
+    counts = [int(n) for n in torch.randint(0, S + 1, (B,), generator=g)]
+    q, cache, table, masks = _case(prefix, counts, S, H, torch.bfloat16, 11)
+    log("tree direct", B, S, H)
+    out, lse = _call(q, cache, table, prefix, counts, masks, out=torch.full((B, S, H, 512), 7.0, dtype=torch.bfloat16, device="cuda"))
+    some = list(range(0, B, 37)) + [B - 1]
+    pick = lambda t: [t[b] for b in some]  # noqa: E731
+    _check(out[some], lse[some], q[some], cache, table[some], pick(prefix), pick(counts), pick(masks), where="direct")
+    n = torch.tensor(counts)[:, None]
+    gone = (torch.arange(S)[None] >= n).cuda()
+    assert (out[gone] == 0).all() and (lse[gone] == -math.inf).all()
+    assert torch.isfinite(lse[~gone]).all()
+
+
+def test_tree_of_a_long_cache():
+    """A sequence of four million keys of a cache past 2^32 bytes, its shares counted in 64 bits.  The table names
+    three runs of pages over and over, so that the plain form has a few thousand keys with a count each."""
+    import scoring_exact_top_amd as lib
+    S, H, pages, P = 64, 128, 65538, 60000
+    g = torch.Generator().manual_seed(12)
+    log("tree long", S, H, pages)
+    own = torch.tensor([5, 59001, 30000, 58300, 59999, 17])
+    rows = torch.randn(len(own), 64, 576, generator=g).bfloat16()
+    cache = torch.zeros(P, 64, 576, dtype=torch.bfloat16, device="cuda")
+    cache[own.cuda()] = rows.cuda()
+    of = torch.cat([torch.randint(0, 2, (20000,), generator=g), torch.randint(2, 4, (25000,), generator=g), torch.full((pages - 45001,), 4), torch.tensor([5])])
+    prefix, masks = (pages - 1) * 64, _tree(S, g)
+    q = torch.randn(1, S, H, 576, generator=g).bfloat16()
+    i32 = lambda n: torch.tensor(n, dtype=torch.int32).cuda()  # noqa: E731
+    out, lse = lib.latent_tree(q.cuda(), cache, own[of].int()[None].cuda(), i32([prefix]), None,
+                               torch.tensor([_signed(v) for v in masks]).cuda(), SCALE)
+    out, lse = out.cpu(), lse.cpu()
+    times = torch.bincount(of, minlength=len(own)).double().repeat_interleave(64)
+    k = rows.view(-1, 576).double()
+    for j in (0, 1, 31, 62, 63):
+        for h in (0, 64, 127):
+            n = times.clone()
+            n[-64:] = torch.tensor([masks[j] >> i & 1 for i in range(64)]).double()
+            qd = q[0, j, h].double()
+            x = k @ qd * SCALE + n.log()
+            want = torch.logsumexp(x, 0)
+            w = torch.exp(x - want)
+            # a quarter of the keys (a row's block is shared by four workgroups), four in a lane's sum at a time
+            _, _, _, dl = attend(qd, k, k[:, :512], SCALE)
+            check_row(out[0, j, h], lse[0, j, h], (w @ k[:, :512], float(want), w @ k[:, :512].abs(), dl), prefix // 16, q.dtype,
+                      "long: node %d head %d" % (j, h))
