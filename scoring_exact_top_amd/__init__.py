@@ -756,11 +756,13 @@ def _angles(positions, table, T: int, dev):
     """Addresses of the positions and the table of angles, and the table's rows."""
     if positions.shape != (T,):
         raise ValueError("expected positions of shape [%d], got %s" % (T, list(positions.shape)))
-    if table.dim() != 2 or table.shape[1] != ROPE:
-        raise ValueError("expected a table [positions,%d], got %s" % (ROPE, list(table.shape)))
-    if table.shape[0] >> 31:
-        _int32(table.shape[0])
-    return _at(positions, torch.int32, dev), _at(table, torch.float32, dev), table.shape[0]
+    shape = table.shape
+    if len(shape) != 2 or shape[1] != ROPE:
+        raise ValueError("expected a table [positions,%d], got %s" % (ROPE, list(shape)))
+    P = shape[0]
+    if P >> 31:
+        _int32(P)
+    return _at(positions, torch.int32, dev), _at(table, torch.float32, dev), P
 
 
 def _head_rows(x, rope_at: int):
@@ -787,11 +789,13 @@ def norm_rotate(x, positions, table, rope_at: int, interleaved: bool = False, no
     dt, dev, dtype, T, H, D, x_at, x_strides = _head_rows(x, rope_at)
     if out is None:
         out = _empty((T, H, D), dtype, dev, stream)
-    out_at = _rows_at(out, dtype, dev, (T, H, D))
+        out_at, out_strides = out.data_ptr(), (H * D, D)
+    else:
+        out_at, out_strides = _rows_at(out, dtype, dev, (T, H, D)), _strides(out)
     pos_at, table_at, P = _angles(positions, table, T, dev)
     _check(_lib.idx_topk_norm_rotate(x_at, *x_strides, _norm(norm), _vector(weight, D, dtype, dev), _vector(bias, D, dtype, dev), eps,
-                                     pos_at, table_at, P, rope_at, 1 if interleaved else 0, T, H, D, dt, out_at, *_strides(out), None,
-                                     None, _on(stream, dev)))
+                                     pos_at, table_at, P, rope_at, 1 if interleaved else 0, T, H, D, dt, out_at, *out_strides, None, None,
+                                     _on(stream, dev)))
     return out
 
 
@@ -884,9 +888,12 @@ def matmul_e4m3(x, x_scale, w, w_scale, dtype=torch.bfloat16, out=None, stream=N
         raise ValueError("expected an output of bfloat16 or float16, got %s" % dtype)
     if out is None:
         out = _empty((M, N), dtype, dev, stream)
-    x_at, out_at = _rows_at(x, x.dtype, dev, (M, K)), _rows_at(out, dtype, dev, (M, N))
+        out_at, out_row = out.data_ptr(), N
+    else:
+        out_at, (out_row,) = _rows_at(out, dtype, dev, (M, N)), _strides(out)
+    x_at = _rows_at(x, x.dtype, dev, (M, K))
     _check(_lib.idx_topk_matmul_e4m3(x_at, *_strides(x), _at(x_scale, torch.float32, dev), 128 if x_scale.shape[1] == blocks else 0,
-                                     _at(w, w.dtype, dev), _at(w_scale, torch.float32, dev), M, N, K, kind, out_at, *_strides(out),
+                                     _at(w, w.dtype, dev), _at(w_scale, torch.float32, dev), M, N, K, kind, out_at, out_row,
                                      _on(stream, dev)))
     return out
 
