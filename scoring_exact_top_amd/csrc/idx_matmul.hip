@@ -11,6 +11,13 @@
 // 16x16x32 form does the same.  The weights' rows are the rows of A and the activations' those of B, so that a lane
 // holds four neighbouring columns n of one row m: one scale a lane, and outputs that are stored
 // together.  Both operands are laid out alike (lane l has bytes 32 (l / 16) .. + 32 of row l % 16).
+//
+// Measured, and what bounds it (rows x columns x k; a call in a loop, the kernel alone in brackets):
+//   1 x 7680 x 5120          8.7 us (8.2)   memory, 4.8 TB/s, and the launch
+//   16 x 12288 x 5120       11.7 us (12.3)  memory, 5.4 TB/s
+//   777 x 768 x 5120        12.5 us (13.2)  a block's way into LDS (64 bytes a clock), 208 of 256 units with one tile each
+//   4096 x 12288 x 5120      223 us         2315 TFLOP/s; matrix cores 60% busy: the additions of scaled sums take issue
+//                                           slots beside them (without: 77%), LDS reads and loads about as many clocks
 #include <type_traits>
 #include "idx_attn.hpp"
 #include "idx_common.hpp"
@@ -179,7 +186,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void k_matmul_few(MatArgs A) {
 // Two barriers a step.  At the first (before the second half of w's fragments) every wave has read x and the first
 // half of w: that part of the image takes the block after the next.  At the second (before the last fragment's
 // products) every wave has read the rest, and the next block's first part is there: its fragments are read beside
-// the last products.  So a load has a step and a half to arrive with two images (a step, with one barrier: 13% more time).
+// the last products.  So a load has a step and a half to arrive with two images (a step, with one barrier: a tenth more time).
 constexpr int kScaleSteps = 4;  // steps whose scales of x are loaded together
 
 template <class E, int NF, int MF, int WN, int WM>
@@ -397,9 +404,9 @@ static void launch_tiles(const MatArgs& A, hipStream_t stream) {
 // Up to 32 rows the weights are streamed: as many columns a workgroup as leave one to a unit.  Beyond that the tile is
 // the one whose rounds over the chip take the least: a block of a round takes about 0.25 us with 64 x 64, 0.63 with
 // 128 x 128 (two of which share a unit, so that beyond the first round each half one counts for itself) and 1.9 with
-// 256 x 256.  Measured, in us with the three tiles: 777 x 768 x 5120 15, 27 and 65; 300 x 12288 x 5120 58, 48 and 74; 1024 x 4096 x 5120 57, 28 and 68;
-// 4096 x 12288 x 5120 660, 302 and 231.  48 columns instead of 64 where that is one round too: 13.3 against 14.7 us for
-// 777 x 768 x 5120.
+// 256 x 256.  Measured, in us with the three tiles: 777 x 768 x 5120 15, 27 and 65; 300 x 12288 x 5120 58, 48 and 74;
+// 1024 x 4096 x 5120 57, 28 and 68; 4096 x 12288 x 5120 660, 302 and 223.  48 columns instead of 64 where that is one
+// round too: 13.3 against 14.7 us for 777 x 768 x 5120.
 template <class E>
 static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   const auto tiles = [&](int64_t n, int64_t m) { return ((A.N + n - 1) / n) * ((A.M + m - 1) / m); };

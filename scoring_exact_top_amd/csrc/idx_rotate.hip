@@ -12,6 +12,13 @@
 // (interleaved) or p, p + 32 (halves).  The angles' cosines and sines come from a table in
 // FP32, which the caller computes in 64 bits: in FP32 the angle itself would be off by 2^-8 at
 // position 65536.
+//
+// Measured (a call in a loop, the kernel alone in brackets):
+//   4096 tokens x 64 heads of 128 to codes    24.0 us (25.5)  103 MB at 4.3 TB/s
+//   3001 tokens x 40 heads of 128, normed     17.7 us (19.0)  62 MB at 3.5 TB/s
+//   16 tokens x 128 heads of 192               8.1 us (3.5)   the host's work for a launch
+//   append of 30000 tokens, rows returned     27.1 us (27.7)  123 MB at 4.5 TB/s
+//   append of 16 tokens                       10.6 us (3.5)   the host's work for a launch
 #include "idx_attn.hpp"
 #include "idx_latent.hpp"
 #include "idx_quant.hpp"
