@@ -97,13 +97,30 @@ struct Part {
 };
 constexpr int kMinPages = 2;
 
-__device__ __forceinline__ int wave_incl_scan(int x, int lane) {
+// Inclusive running sum over the wave, all lanes active, by moves between lanes: within rows of 16, then a row's last
+// lane to the rows behind it.
+__device__ __forceinline__ int wave_incl_scan(int x) {
+  constexpr int kShr = 0x110, kBroadcast15 = 0x142, kBroadcast31 = 0x143;
+  x += __builtin_amdgcn_update_dpp(0, x, kShr + 1, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, kShr + 2, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, kShr + 4, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, kShr + 8, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, kBroadcast15, 0xa, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, kBroadcast31, 0xc, 0xf, false);
+  return x;
+}
+__device__ __forceinline__ int64_t wave_incl_scan(int64_t x) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d, 64);
-    if (lane >= d) x += y;
+    const int64_t y = __shfl_up((long long)x, d, 64);
+    if ((int)(threadIdx.x & 63) >= d) x += y;
   }
   return x;
+}
+// A lane's number in all of them.
+__device__ __forceinline__ int of_lane(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
+__device__ __forceinline__ int64_t of_lane(int64_t x, int l) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), l) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)x, l));
 }
 
 // Drafted tokens of a tree's sequence (0 for a sequence that is not one).
@@ -122,7 +139,7 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
   int64_t total = 0;
   for (int b0 = 0; b0 < A.B; b0 += 64) {
     const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
-    total += __shfl(wave_incl_scan(n, lane), 63, 64);
+    total += of_lane(wave_incl_scan(n), 63);
   }
   // sum of max(1, ceil(n / unit)) <= total / unit + B <= parts
   int unit = (int)((total + (A.parts - A.B) - 1) / (A.parts - A.B));
@@ -132,7 +149,7 @@ __device__ __forceinline__ Part plan_part(const LatArgs& A, int wg, int lane) {
     const int n = b0 + lane < A.B ? (seq_len(A, b0 + lane) + IDX_TOPK_PAGE - 1) / IDX_TOPK_PAGE : 0;
     const int parts = b0 + lane < A.B ? max(1, (n + unit - 1) / unit) : 0;
     const int both = parts > 1 ? parts << 16 | parts : parts;
-    const int end = base + wave_incl_scan(both, lane);
+    const int end = base + wave_incl_scan(both);
     const int last = end & 0xFFFF;
     const uint64_t mine = __ballot(wg >= last - parts && wg < last);
     if (mine) {
@@ -179,33 +196,20 @@ struct TreeStart {
   int shares, wg, nodes, keys;  // of the sequence
 };
 
-template <class N>
-__device__ __forceinline__ N wave_sum_before(N x, int lane) {  // inclusive
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const N y = __shfl_up((std::conditional_t<sizeof(N) == 8, long long, int>)x, d, 64);
-    if (lane >= d) x += y;
-  }
-  return x;
-}
-
-// N: 32 bits where the work is below 2^22 pages (a plan takes a workgroup 2 us then, in 64 bits 5).
+// N: 32 bits where the work is below 2^22 pages.  `head`: the first 64 sequences, read once.
 template <int HG, class N>
-__device__ __forceinline__ TreeStart plan_tree_in(const LatArgs& A, int wg, int lane, N total, N blocks) {
+__device__ __forceinline__ TreeStart plan_tree_in(const LatArgs& A, const TreeSeq& head, int wg, int lane, N total, N blocks) {
   TreeStart at{-1, 0, 0, 0, 0, 0, (int64_t)total, 1, wg, 0, 0};
-  const N shares = A.parts;
-  // sum of ceil(pages / unit) <= total / unit + blocks <= parts
+  constexpr N shares = kUnits;
+  // sum of ceil(pages / unit) <= total / unit + blocks <= shares
   N unit = blocks < shares ? quotient(total + shares - blocks - 1, shares - blocks) : total + kBegin + 1;
   const bool cut = unit <= quotient(total, shares) + kBegin;
   unit = unit < kMinPages ? kMinPages : unit;
   if (cut && A.B <= 64) {
     // that bound is for lengths that just pass a multiple of the unit; a smaller one often fits
-    const TreeSeq t(A, lane, 16 * HG);
     N u = quotient(total + shares - 1, shares);
-    for (u = u < kMinPages ? kMinPages : u; u < unit; ++u) {
-      const N all = wave_sum_before((N)t.blocks * quotient((N)t.pages + u - 1, u), lane);
-      if (__shfl((std::conditional_t<sizeof(N) == 8, long long, int>)all, 63, 64) <= shares) unit = u;
-    }
+    for (u = u < kMinPages ? kMinPages : u; u < unit; ++u)
+      if (of_lane(wave_incl_scan((N)head.blocks * quotient((N)head.pages + u - 1, u)), 63) <= shares) unit = u;
   }
   N from = wg;
   if (!cut) {
@@ -216,19 +220,18 @@ __device__ __forceinline__ TreeStart plan_tree_in(const LatArgs& A, int wg, int 
     at.pages = at.end - from;
   }
   N base = 0;
+  TreeSeq t = head;
 #pragma nounroll
-  for (int b0 = 0; b0 < A.B; b0 += 64) {
-    const TreeSeq t(A, b0 + lane, 16 * HG);
+  for (int b0 = 0;;) {
     const N parts = cut ? quotient((N)t.pages + unit - 1, unit) : t.pages;
-    const N w = (N)t.blocks * parts, end = base + wave_sum_before(w, lane), begin = end - w;
+    const N w = (N)t.blocks * parts, end = base + wave_incl_scan(w), begin = end - w;
     const uint64_t found = __ballot(from >= begin && from < end);
     if (found) {
-      const int l = __ffsll((unsigned long long)found) - 1;
-      const auto of = [&](N x) { return (N)__shfl((std::conditional_t<sizeof(N) == 8, long long, int>)x, l, 64); };
-      const N into = from - of(begin), n = of(parts), pages = of(t.pages), block = quotient(into, n), part = into - block * n;
+      const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)found) - 1);
+      const N into = from - of_lane(begin, l), n = of_lane(parts, l), pages = of_lane(t.pages, l), block = quotient(into, n), part = into - block * n;
       at.b = b0 + l;
-      at.nodes = __shfl(t.nodes, l, 64);
-      at.keys = __shfl(t.keys, l, 64);
+      at.nodes = of_lane(t.nodes, l);
+      at.keys = of_lane(t.keys, l);
       at.block = (int)block;
       at.first = (int)part;
       if (cut) {
@@ -239,7 +242,10 @@ __device__ __forceinline__ TreeStart plan_tree_in(const LatArgs& A, int wg, int 
       }
       break;
     }
-    base = (N)__shfl((std::conditional_t<sizeof(N) == 8, long long, int>)end, 63, 64);
+    base = of_lane(end, 63);
+    b0 += 64;
+    if (b0 >= A.B) break;
+    t = TreeSeq(A, b0 + lane, 16 * HG);
   }
   return at;
 }
@@ -248,26 +254,19 @@ template <int HG>
 __device__ __forceinline__ TreeStart plan_tree(const LatArgs& A, int wg, int lane) {
   int64_t total = 0;
   int blocks = 0;
+  const TreeSeq head(A, lane, 16 * HG);
+  TreeSeq t = head;
 #pragma nounroll
-  for (int b0 = 0; b0 < A.B; b0 += 64) {
-    const TreeSeq t(A, b0 + lane, 16 * HG);
-    int64_t w = (int64_t)t.blocks * t.pages;
-    int n = t.blocks;
-    if (A.B == 1) {
-      w = __shfl((long long)w, 0, 64);
-      n = __shfl(n, 0, 64);
-    } else {
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) {
-        w += __shfl_xor((long long)w, d, 64);
-        n += __shfl_xor(n, d, 64);
-      }
-    }
-    total += w;
-    blocks += n;
+  for (int b0 = 0;;) {
+    const int64_t w = (int64_t)t.blocks * t.pages;
+    blocks += of_lane(wave_incl_scan(t.blocks), 63);
+    total += __any(w >= 1 << 22) ? of_lane(wave_incl_scan(w), 63) : of_lane(wave_incl_scan((int)w), 63);
+    b0 += 64;
+    if (b0 >= A.B) break;
+    t = TreeSeq(A, b0 + lane, 16 * HG);
   }
-  if (total < 1 << 22) return plan_tree_in<HG, int32_t>(A, wg, lane, (int32_t)total, blocks);
-  return plan_tree_in<HG, int64_t>(A, wg, lane, total, blocks);
+  if (total < 1 << 22) return plan_tree_in<HG, int32_t>(A, head, wg, lane, (int32_t)total, blocks);
+  return plan_tree_in<HG, int64_t>(A, head, wg, lane, total, blocks);
 }
 
 // HG row groups of 16 (one wave each) x KG key groups: wave (kg, hg) walks
@@ -380,7 +379,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   const int b = part.b;
   int row = (rb * HG + hg) * kRowsWave + col;
   bool have = row < A.S * A.H;
-  int step = have ? row / A.H : 0, head = have ? row % A.H : 0;
+  int step = have ? quotient(row, A.H) : 0, head = have ? row - step * A.H : 0;
   int limit = MODE == kPaged ? len - A.S + 1 + step : len;  // this lane's row sees keys below
   int limit_min = MODE == kPaged ? len - A.S + 1 : len;     // every row does
   int q_step = step, nodes = 0;
@@ -390,12 +389,19 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
     limit_min = len - nodes;
     q_step = step < nodes ? step : 0;  // a row of no drafted token repeats the first one's, and is dropped
     // a row's mask, its bits behind the last drafted token cleared
-    if (tid < HG * kRowsWave) {
-      const int r = rb * HG * kRowsWave + tid, node = r < A.S * A.H ? r / A.H : A.S;
-      mask = node < nodes ? A.masks[b * A.mask_seq + node] & (~0ull >> (64 - nodes)) : 0;
-    }
+    if (kg == 0 && lane < kRowsWave && have && step < nodes) mask = A.masks[b * A.mask_seq + step] & (~0ull >> (64 - nodes));
     if (rb * HG * kRowsWave >= nodes * A.H) tile1 = tile0;  // no row of this workgroup is one
   }
+  const int mine = __builtin_amdgcn_readfirstlane(tile0) + kg;  // this key group's first tile
+  // the same for all key groups: barriers
+  const int steps = __builtin_amdgcn_readfirstlane(tile1 > tile0 ? (tile1 - tile0 + KG - 1) / KG : 0);
+  // A tile's page id; page 0 of the table stands in for tiles past the end.  A scalar load: vector loads would queue
+  // behind the tile loads.
+  const auto page_of = [&](int t) __attribute__((always_inline)) {
+    const auto* table = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)A.list) + (int64_t)b * A.K;
+    const int key0 = (mine + t * KG) * kTileKeys;
+    return table[t < steps && key0 < len ? key0 / IDX_TOPK_PAGE : 0];
+  };
 
   // The first memory the wave waits for: this range's slots (-1 for what is not
   // to be read) go to LDS behind q's loads, which are under way meanwhile.
@@ -412,7 +418,6 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const typename T::v8*>(p + 32 * s);
   }
-  if (MODE == kTree && tid < HG * kRowsWave) s_mask[tid] = mask;  // before the barriers of the walk
   if (!PAGED) {
     for (int i = tid; i < n_list; i += 64 * HG * KG) {
       s_list[i] = slot >= 0 && slot < A.num_slots ? slot : -1;
@@ -440,10 +445,6 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   };
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)s_tile;
 
-  const int mine = __builtin_amdgcn_readfirstlane(tile0) + kg;  // this key group's first tile
-  // the same for all key groups: barriers
-  const int steps = __builtin_amdgcn_readfirstlane(tile1 > tile0 ? (tile1 - tile0 + KG - 1) / KG : 0);
-
   // This wave's share of a tile, in kLoads loads: lane j < kRows has the address
   // of load j's row, each lane its own of the rotary parts'.  Keys that are not
   // there (bit clear in `live`) come from the zero row; so does a whole tile
@@ -453,13 +454,6 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   struct Source {
     uint32_t dst, live;
     uint32_t lo, hi, rlo[kRope4], rhi[kRope4];
-  };
-  // A tile's page id; page 0 of the table stands in for tiles past the end.  A scalar load: vector loads would queue
-  // behind the tile loads.
-  const auto page_of = [&](int t) __attribute__((always_inline)) {
-    const auto* table = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>((uintptr_t)A.list) + (int64_t)b * A.K;
-    const int key0 = (mine + t * KG) * kTileKeys;
-    return table[t < steps && key0 < len ? key0 / IDX_TOPK_PAGE : 0];
   };
   const auto source_at = [&](int t, int pg) __attribute__((always_inline)) {
     Source f;
@@ -628,6 +622,7 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   // 15 octaves; bfloat16's 64 octaves take a standard deviation of 14 to be passed.
   const float lift = T::first_lift(steps);
   __builtin_amdgcn_s_waitcnt(0x0F70);  // q is there: the waits below count tile loads only
+  if (MODE == kTree && kg == 0 && lane < kRowsWave) s_mask[hg * kRowsWave + lane] = mask;  // before the walk's barriers
   for (int attempt = 0;; ++attempt) {
 #pragma unroll
     for (int d = 0; d < kCols; ++d) o[d] = w4f{};
@@ -688,8 +683,8 @@ __global__ __launch_bounds__(64 * HG * KG, HG * KG == 8 ? 2 : 1) void k_latent(L
   if (MODE == kTree) {
     // worked out again, not kept over the walk
     row = (__builtin_amdgcn_readfirstlane(s_at.block) * HG + hg) * kRowsWave + (own_lane() & 15);
-    step = row / A.H;
-    head = row % A.H;
+    step = quotient(row, A.H);
+    head = row - step * A.H;
     have = step < (A.parts ? nodes : A.S);
     if (step >= nodes) {
       // without a plan there is no second kernel that writes the zeros of rows of no drafted token
