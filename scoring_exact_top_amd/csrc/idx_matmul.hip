@@ -13,10 +13,10 @@
 // together.  Both operands are laid out alike (lane l has bytes 32 (l / 16) .. + 32 of row l % 16).
 //
 // Measured, and what bounds it (rows x columns x k; a call in a loop, the kernel alone in brackets):
-//   1 x 7680 x 5120          8.7 us (8.2)   memory, 4.8 TB/s, and the launch
+//   1 x 7680 x 5120          8.5 us (8.1)   memory, 4.8 TB/s, and the launch
 //   16 x 12288 x 5120       11.7 us (12.3)  memory, 5.4 TB/s
-//   777 x 768 x 5120        12.5 us (13.2)  a block's way into LDS (64 bytes a clock), 208 of 256 units with one tile each
-//   4096 x 12288 x 5120      223 us         2315 TFLOP/s; matrix cores 60% busy: the additions of scaled sums take issue
+//   777 x 768 x 5120        11.7 us (12.6)  a block's way into LDS (64 bytes a clock), 208 of 256 units with one tile each
+//   4096 x 12288 x 5120  223-229 us         2280 TFLOP/s; matrix cores 60% busy: the additions of scaled sums take issue
 //                                           slots beside them (without: 77%), LDS reads and loads about as many clocks
 #include <type_traits>
 #include "idx_attn.hpp"
@@ -420,7 +420,7 @@ static void launch_tiles(const MatArgs& A, hipStream_t stream) {
 // 128 x 128 (two of which share a unit, so that beyond the first round each half one counts for itself) and 1.9 with
 // 256 x 256.  Measured, in us with the three tiles: 777 x 768 x 5120 15, 27 and 65; 300 x 12288 x 5120 58, 48 and 74;
 // 1024 x 4096 x 5120 57, 28 and 68; 4096 x 12288 x 5120 660, 302 and 223.  48 columns instead of 64 where that is one
-// round too: 13.3 against 14.7 us for 777 x 768 x 5120.
+// round too: 13.3 against 14.7 us for 777 x 768 x 5120 (neither folded).
 template <class E>
 static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   const auto tiles = [&](int64_t n, int64_t m) { return ((A.N + n - 1) / n) * ((A.M + m - 1) / m); };
