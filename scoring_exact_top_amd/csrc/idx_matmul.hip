@@ -86,7 +86,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void k_matmul_few(MatArgs A) {
   const int total = gridDim.x, per = total >> 3, extra = total & 7, x8 = blockIdx.x & 7, i8 = blockIdx.x >> 3;
   const int work = x8 * per + min(x8, extra) + i8;
   int n0 = work / tiles_m * (16 * NF), m0 = work % tiles_m * (16 * MF);
-  if (MF == 4 && A.fold) {
+  if (MF > 1 && A.fold) {
     const int half = (tiles_m + 1) / 2, quarter = ((A.N + 16 * NF - 1) / (16 * NF) + 3) / 4;
     const int m = x8 / 4 * half + i8 % half;
     n0 = (x8 % 4 * quarter + i8 / half) * (16 * NF);
@@ -403,7 +403,7 @@ template <class E, int NF, int MF, int W, int D>
 static void launch_few(MatArgs A, hipStream_t stream) {
   const int64_t tm = (A.M + 16 * MF - 1) / (16 * MF), tn = (A.N + 16 * NF - 1) / (16 * NF);
   const int64_t half = (tm + 1) / 2, quarter = (tn + 3) / 4;
-  A.fold = MF == 4 && half * MF + quarter * NF < tm * MF + (tn + 7) / 8 * NF &&
+  A.fold = MF > 1 && half * MF + quarter * NF < tm * MF + (tn + 7) / 8 * NF &&
            half * quarter <= (tm * tn + kUnits - 1) / kUnits * (kUnits / 8);
   const int64_t grid = A.fold ? 8 * half * quarter : tm * tn;
   k_matmul_few<E, NF, MF, W, D><<<dim3((uint32_t)grid), dim3(64 * W), 0, stream>>>(A);
@@ -415,7 +415,8 @@ static void launch_tiles(const MatArgs& A, hipStream_t stream) {
   k_matmul_tiles<E, NF, MF, WN, WM><<<dim3((uint32_t)grid), dim3(64 * WN * WM), 0, stream>>>(A);
 }
 
-// Up to 32 rows the weights are streamed: as many columns a workgroup as leave one to a unit.  Beyond that the tile is
+// Up to 32 rows the weights are streamed: as many columns a workgroup as leave one to a unit.  More rows take tiles of
+// 32 x 32 too where those are one to a unit (128 x 1536 x 7168: 9.4 us, with 64 x 64 14.8).  Beyond that the tile is
 // the one whose rounds over the chip take the least: a block of a round takes about 0.25 us with 64 x 64, 0.63 with
 // 128 x 128 (two of which share a unit, so that beyond the first round each half one counts for itself) and 1.9 with
 // 256 x 256.  Measured, in us with the three tiles: 777 x 768 x 5120 15, 27 and 65; 300 x 12288 x 5120 58, 48 and 74;
@@ -432,9 +433,10 @@ static int launch_matmul(const MatArgs& A, hipStream_t stream) {
     if (A.N <= 16 * kUnits) launch_few<E, 1, 1, 8, 4>(A, stream);
     else if (A.N <= 32 * kUnits) launch_few<E, 2, 1, 8, 3>(A, stream);
     else launch_few<E, 3, 1, 4, 4>(A, stream);
+  } else if (tiles(32, 32) <= kUnits) {
+    launch_few<E, 2, 2, 8, 2>(A, stream);
   } else if (A.M <= 32) {
-    if (A.N <= 32 * kUnits) launch_few<E, 2, 2, 8, 2>(A, stream);
-    else launch_few<E, 4, 2, 4, 3>(A, stream);
+    launch_few<E, 4, 2, 4, 3>(A, stream);
   } else if (c64 <= c128 && c64 <= c256) {
     if (tiles(48, 64) <= kUnits) launch_few<E, 3, 4, 8, 1>(A, stream);
     else launch_few<E, 4, 4, 8, 1>(A, stream);
