@@ -596,7 +596,8 @@ int idx_topk_cache_append_rotary(const void *latents, int64_t latent_token, int3
  * bfloat16's rounding).  It is scaled and added to the others in FP32 and the result is rounded
  * once; sums that leave the output's type are infinities.  NaN codes
  * (those of idx_topk_norm_quant for a row with a NaN) make the outputs they enter NaN, and no others.
- * The result does not depend on timing.  Calls of 2^23 tiles of 16 x 16 and more are IDX_EUNSUPPORTED.  No workspace.
+ * The result does not depend on timing.  Calls of 2^23 tiles of 128 x 128 (M up to 32: of 16 x 16) and more are
+ * IDX_EUNSUPPORTED.  No workspace.
  */
 int idx_topk_matmul_e4m3(const uint8_t *x, int64_t x_row, const float *x_scale, int32_t x_group,
                          const uint8_t *w, const float *w_scale, int32_t M, int32_t N, int32_t K,

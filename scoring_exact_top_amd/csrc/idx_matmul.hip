@@ -428,7 +428,8 @@ static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   const auto rounds = [&](int64_t size, int64_t units) { return (tiles(size, size) + units - 1) / units; };
   const int64_t half = rounds(128, kUnits / 2);
   const int64_t c64 = 50 * rounds(64, kUnits), c128 = 63 * (half < 2 ? 2 : half), c256 = 380 * rounds(256, kUnits);
-  if (tiles(16, 16) > 0x7fffff) return IDX_EUNSUPPORTED;  // a launch dimension takes fewer than 2^32 threads
+  // a launch dimension takes fewer than 2^32 threads: the tiles that large calls take, 16 columns of few rows at least
+  if ((A.M <= 32 ? tiles(16, 16) : tiles(128, 128)) > 0x7fffff) return IDX_EUNSUPPORTED;
   if (A.M <= 16) {
     if (A.N <= 16 * kUnits) launch_few<E, 1, 1, 8, 4>(A, stream);
     else if (A.N <= 32 * kUnits) launch_few<E, 2, 1, 8, 3>(A, stream);

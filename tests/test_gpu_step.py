@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from gpu_util import log
-from step_util import table_of
+from step_util import U, product, table_of
 
 pytestmark = pytest.mark.gpu
 
@@ -182,3 +182,63 @@ def test_refusals():
         with pytest.raises(lib.IdxTopkError):
             f()
             print("not refused: %d" % i, flush=True)
+
+
+def test_product_past_32_bits():
+    """Weights, strided activations and outputs of more than 2^32 bytes, in the kernels for few rows and for many."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator("cuda").manual_seed(3)
+    N, K = 40000, 131072
+    w = torch.randint(0, 100, (N, K), generator=g, dtype=torch.uint8, device="cuda")
+    ws = torch.rand(-(-N // 128), K // 128, generator=g, device="cuda")
+    e4m3 = lambda t: t.cpu().view(torch.float8_e4m3fn)  # noqa: E731
+
+    def check(got, x, xs, w, ws, where):
+        want, off = product(e4m3(x), xs.cpu(), e4m3(w), ws.cpu())
+        over = (got.double().cpu() - want).abs() - (off + U[got.dtype] * (want.abs() + off))
+        assert float(over.max()) <= 0, where
+
+    for M in (3, 30, 600):
+        log("product past 32 bits", M, N, K)
+        x = torch.randint(0, 100, (M, K), generator=g, dtype=torch.uint8, device="cuda")
+        xs = torch.rand(M, K // 128, generator=g, device="cuda")
+        out = lib.matmul_e4m3(x, xs, w, ws)
+        for n in (0, 32768, 39936):
+            rows = [0, M // 2, M - 1]
+            check(out[rows][:, n:n + 64], x[rows], xs[rows], w[n:n + 64], ws[n // 128:n // 128 + 1], "weights %d, columns from %d" % (M, n))
+    few, fs = torch.randint(0, 100, (200, 256), generator=g, dtype=torch.uint8, device="cuda"), torch.rand(2, 2, generator=g, device="cuda")
+    xs = torch.rand(N, 1, generator=g, device="cuda")
+    log("strided past 32 bits")
+    out = lib.matmul_e4m3(w[:, 512:768], xs, few, fs)
+    check(out[-70:], w[-70:, 512:768], xs[-70:], few, fs, "activations")
+    log("output past 32 bits")
+    x, xs = torch.randint(0, 100, (70000, 128), generator=g, dtype=torch.uint8, device="cuda"), torch.rand(70000, 1, generator=g, device="cuda")
+    out = lib.matmul_e4m3(x, xs, w.view(-1, 128)[:32768], torch.ones(256, 1, device="cuda"))
+    rows = [0, 40000, 65535, 65536, 69999]
+    check(out[rows], x[rows], xs[rows], w.view(-1, 128)[:32768], torch.ones(256, 1), "outputs")
+
+
+def test_rows_past_32_bits():
+    """Heads of a wider tensor and cache slots behind 2^32 bytes."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator("cuda").manual_seed(4)
+    T, width, P = 40000, 65536, 60000
+    wide = torch.zeros(T, width, dtype=torch.bfloat16, device="cuda")
+    table = table_of(5000).cuda()
+    wide[:, :768] = torch.randn(T, 768, generator=g, device="cuda").bfloat16()
+    x = wide[:, :192].unsqueeze(1)
+    pos = torch.randint(0, 5000, (T,), generator=g, device="cuda", dtype=torch.int32)
+    log("rotate past 32 bits")
+    for call in (lib.norm_rotate, lib.norm_rotate_quant):
+        got, want = call(x, pos, table, 128, norm="rms"), call(x.contiguous(), pos, table, 128, norm="rms")
+        for a, b in zip(got, want) if isinstance(got, tuple) else ((got, want),):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    log("append past 32 bits")
+    cache, kc = torch.zeros(P, 64, 576, dtype=torch.bfloat16, device="cuda"), torch.zeros(P, 64, 128, dtype=torch.uint8, device="cuda")
+    ks = torch.zeros(P, 64, device="cuda")
+    small = tuple(torch.zeros_like(t[:625]) for t in (cache, kc, ks))
+    there = torch.randperm(T, generator=torch.Generator().manual_seed(1)).int().cuda()
+    lib.cache_append_rotary(wide[:, :576], wide[:, 576:704], there + (P * 64 - T), pos, table, cache, kc, ks)
+    lib.cache_append_rotary(wide[:, :576].contiguous(), wide[:, 576:704].contiguous(), there, pos, table, *small)
+    for a, b in zip((cache, kc, ks), small):
+        assert torch.equal(a[P - 625:], b) and not a[:P - 625].any()
