@@ -767,13 +767,16 @@ def _angles(positions, table, T: int, dev):
 
 def _head_rows(x, rope_at: int):
     """What norm_rotate and norm_rotate_quant take of x [T,H,D]."""
-    dt, dev, dtype = _dtype16(x), x.get_device(), x.dtype
-    if x.dim() != 3:
-        raise ValueError("expected x [T,H,D], got %s" % list(x.shape))
-    T, H, D = shape = x.shape
+    dt, dev, dtype, shape = _dtype16(x), x.get_device(), x.dtype, x.shape
+    if len(shape) != 3:
+        raise ValueError("expected x [T,H,D], got %s" % list(shape))
+    T, H, D = shape
     if (T | H | D | rope_at) >> 31:
         _int32(T | H | D | rope_at)
-    return dt, dev, dtype, T, H, D, _rows_at(x, dtype, dev, shape), _strides(x)
+    token, head, unit = x.stride()
+    if unit != 1 and D > 1:
+        raise ValueError("expected unit stride along the last dimension")
+    return dt, dev, dtype, T, H, D, x.data_ptr(), (token if T > 1 else 0, head if H > 1 else 0)
 
 
 def norm_rotate(x, positions, table, rope_at: int, interleaved: bool = False, norm: str = "none", weight=None, bias=None,
@@ -839,13 +842,13 @@ def cache_append_rotary(latents, index_keys, slots, positions, table, latent_cac
     num = n = None
     if latents is not None:
         lat_at = _rows_at(latents, dtype, dev, (T, LATENT_ROW))
-        lat_stride, = _strides(latents)
+        lat_stride = latents.stride(0) if T > 1 else 0
         cache_at, num = _cache_at(latent_cache, LATENT_ROW, dtype, dev)
     if latents_out is not None:
         _, out_at = _out(latents_out, (T, LATENT_ROW), dtype, dev, stream)
     if index_keys is not None:
         key_at = _rows_at(index_keys, dtype, dev, (T, DIM))
-        key_stride, = _strides(index_keys)
+        key_stride = index_keys.stride(0) if T > 1 else 0
         kc_at, n = _cache_at(k_cache, DIM, torch.float8_e4m3fn if k_cache.dtype == torch.float8_e4m3fn else torch.uint8, dev)
         ks_at = _at(k_scale, torch.float32, dev)
         if k_scale.numel() != n or (num is not None and num != n):
@@ -858,6 +861,9 @@ def cache_append_rotary(latents, index_keys, slots, positions, table, latent_cac
                                              P, T, dt, cache_at, kc_at, ks_at, n if num is None else num, out_at, _on(stream, dev)))
 
 
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
 def matmul_e4m3(x, x_scale, w, w_scale, dtype=torch.bfloat16, out=None, stream=None):
     """Product x @ w.T of e4m3 operands with block scales; see idx_topk_matmul_e4m3.
 
@@ -868,32 +874,34 @@ def matmul_e4m3(x, x_scale, w, w_scale, dtype=torch.bfloat16, out=None, stream=N
     """
     if not x.is_cuda:
         raise ValueError("expected a device tensor")
-    dev = x.get_device()
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-        raise ValueError("expected x [M,K] and w [N,K], got %s and %s" % (list(x.shape), list(w.shape)))
-    M, K = x.shape
-    N = w.shape[0]
+    dev, shape, w_shape = x.get_device(), x.shape, w.shape
+    if len(shape) != 2 or len(w_shape) != 2 or shape[1] != w_shape[1]:
+        raise ValueError("expected x [M,K] and w [N,K], got %s and %s" % (list(shape), list(w_shape)))
+    (M, K), N = shape, w_shape[0]
     if (M | N | K) >> 31:
         _int32(M | N | K)
-    for t in (x, w):
-        if t.dtype != torch.float8_e4m3fn and t.dtype != torch.uint8:
-            raise ValueError("expected float8_e4m3fn or uint8, got %s" % t.dtype)
+    x_type, w_type = x.dtype, w.dtype
+    if x_type not in _CODES or w_type not in _CODES:
+        raise ValueError("expected float8_e4m3fn or uint8, got %s and %s" % (x_type, w_type))
     blocks = (K + 127) // 128
-    if x_scale.shape != (M, blocks) and x_scale.shape != (M, 1):
-        raise ValueError("expected x_scale [%d,%d] or [%d,1], got %s" % (M, blocks, M, list(x_scale.shape)))
+    groups = x_scale.shape
+    if groups != (M, blocks) and groups != (M, 1):
+        raise ValueError("expected x_scale [%d,%d] or [%d,1], got %s" % (M, blocks, M, list(groups)))
     if w_scale.shape != ((N + 127) // 128, blocks):
         raise ValueError("expected w_scale [%d,%d], got %s" % ((N + 127) // 128, blocks, list(w_scale.shape)))
     kind = _DTYPES.get(dtype)
     if kind is None:
         raise ValueError("expected an output of bfloat16 or float16, got %s" % dtype)
+    x_row, unit = x.stride()
+    if unit != 1 and K > 1:
+        raise ValueError("expected unit stride along the last dimension")
     if out is None:
         out = _empty((M, N), dtype, dev, stream)
         out_at, out_row = out.data_ptr(), N
     else:
         out_at, (out_row,) = _rows_at(out, dtype, dev, (M, N)), _strides(out)
-    x_at = _rows_at(x, x.dtype, dev, (M, K))
-    _check(_lib.idx_topk_matmul_e4m3(x_at, *_strides(x), _at(x_scale, torch.float32, dev), 128 if x_scale.shape[1] == blocks else 0,
-                                     _at(w, w.dtype, dev), _at(w_scale, torch.float32, dev), M, N, K, kind, out_at, out_row,
+    _check(_lib.idx_topk_matmul_e4m3(x.data_ptr(), x_row if M > 1 else 0, _at(x_scale, torch.float32, dev), 128 if groups[1] == blocks else 0,
+                                     _at(w, w_type, dev), _at(w_scale, torch.float32, dev), M, N, K, kind, out_at, out_row,
                                      _on(stream, dev)))
     return out
 

@@ -13,7 +13,7 @@
 // together.  Both operands are laid out alike (lane l has bytes 32 (l / 16) .. + 32 of row l % 16).
 //
 // Measured, and what bounds it (rows x columns x k; a call in a loop, the kernel alone in brackets):
-//   1 x 7680 x 5120          8.5 us (8.1)   memory, 4.8 TB/s, and the launch
+//   1 x 7680 x 5120          7.6 us (8.1)   memory, 5.2 TB/s, and the host's work for a launch
 //   16 x 12288 x 5120       11.7 us (12.3)  memory, 5.4 TB/s
 //   777 x 768 x 5120        11.7 us (12.6)  a block's way into LDS (64 bytes a clock), 208 of 256 units with one tile each
 //   4096 x 12288 x 5120  223-229 us         2280 TFLOP/s; matrix cores 60% busy: the additions of scaled sums take issue
