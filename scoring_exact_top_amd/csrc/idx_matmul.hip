@@ -397,22 +397,29 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_matmul_tiles(MatArgs A) {
 
 static inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+// Workgroups of `waves` waves go into a launch dimension up to 2^32 - 1 threads; a larger one wraps, without an error.
+static inline bool fits(int64_t groups, int waves) { return groups * (64 * waves) <= 0xffffffffLL; }
+
 // Folded where a chiplet then reads fewer rows of x and w for its tiles and has no more rounds of them (777 x 768 x 5120,
 // 208 tiles: 11.9 instead of 12.9 us; 200 x 4096 x 7168, where it would read more: 17.1 instead of 15.7).
 template <class E, int NF, int MF, int W, int D>
-static void launch_few(MatArgs A, hipStream_t stream) {
+static int launch_few(MatArgs A, hipStream_t stream) {
   const int64_t tm = (A.M + 16 * MF - 1) / (16 * MF), tn = (A.N + 16 * NF - 1) / (16 * NF);
   const int64_t half = (tm + 1) / 2, quarter = (tn + 3) / 4;
   A.fold = MF > 1 && half * MF + quarter * NF < tm * MF + (tn + 7) / 8 * NF &&
            half * quarter <= (tm * tn + kUnits - 1) / kUnits * (kUnits / 8);
   const int64_t grid = A.fold ? 8 * half * quarter : tm * tn;
+  if (!fits(grid, W)) return IDX_EUNSUPPORTED;
   k_matmul_few<E, NF, MF, W, D><<<dim3((uint32_t)grid), dim3(64 * W), 0, stream>>>(A);
+  return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
 template <class E, int NF, int MF, int WN, int WM>
-static void launch_tiles(const MatArgs& A, hipStream_t stream) {
+static int launch_tiles(const MatArgs& A, hipStream_t stream) {
   constexpr int TN = 16 * NF * WN, TM = 16 * MF * WM;
   const int64_t grid = (int64_t)((A.N + TN - 1) / TN) * ((A.M + TM - 1) / TM);
+  if (!fits(grid, WN * WM)) return IDX_EUNSUPPORTED;
   k_matmul_tiles<E, NF, MF, WN, WM><<<dim3((uint32_t)grid), dim3(64 * WN * WM), 0, stream>>>(A);
+  return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
 }
 
 // Up to 32 rows the weights are streamed: as many columns a workgroup as leave one to a unit.  More rows take tiles of
@@ -428,25 +435,22 @@ static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   const auto rounds = [&](int64_t size, int64_t units) { return (tiles(size, size) + units - 1) / units; };
   const int64_t half = rounds(128, kUnits / 2);
   const int64_t c64 = 50 * rounds(64, kUnits), c128 = 63 * (half < 2 ? 2 : half), c256 = 380 * rounds(256, kUnits);
-  // a launch dimension takes fewer than 2^32 threads: the tiles that large calls take, 16 columns of few rows at least
+  // larger calls are refused: rows and columns stay so far below 2^31 that a tile's end is one too
   if ((A.M <= 32 ? tiles(16, 16) : tiles(128, 128)) > 0x7fffff) return IDX_EUNSUPPORTED;
   if (A.M <= 16) {
-    if (A.N <= 16 * kUnits) launch_few<E, 1, 1, 8, 4>(A, stream);
-    else if (A.N <= 32 * kUnits) launch_few<E, 2, 1, 8, 3>(A, stream);
-    else launch_few<E, 3, 1, 4, 4>(A, stream);
-  } else if (tiles(32, 32) <= kUnits) {
-    launch_few<E, 2, 2, 8, 2>(A, stream);
-  } else if (A.M <= 32) {
-    launch_few<E, 4, 2, 4, 3>(A, stream);
-  } else if (c64 <= c128 && c64 <= c256) {
-    if (tiles(48, 64) <= kUnits) launch_few<E, 3, 4, 8, 1>(A, stream);
-    else launch_few<E, 4, 4, 8, 1>(A, stream);
-  } else if (c128 <= c256) {
-    launch_tiles<E, 4, 4, 2, 2>(A, stream);
-  } else {
-    launch_tiles<E, 8, 4, 2, 4>(A, stream);
+    if (A.N <= 16 * kUnits) return launch_few<E, 1, 1, 8, 4>(A, stream);
+    if (A.N <= 32 * kUnits) return launch_few<E, 2, 1, 8, 3>(A, stream);
+    return launch_few<E, 3, 1, 4, 4>(A, stream);
   }
-  return hipGetLastError() == hipSuccess ? IDX_OK : IDX_EHIP;
+  if (tiles(32, 32) <= kUnits) return launch_few<E, 2, 2, 8, 2>(A, stream);
+  if (A.M <= 32) return launch_few<E, 4, 2, 4, 3>(A, stream);
+  // one row or column of tiles 64 wide has half the workgroups with 128 x 128, and half the threads in each
+  if (c64 <= c128 && c64 <= c256 && fits(tiles(64, 64), 8)) {
+    if (tiles(48, 64) <= kUnits) return launch_few<E, 3, 4, 8, 1>(A, stream);
+    return launch_few<E, 4, 4, 8, 1>(A, stream);
+  }
+  if (c128 <= c256) return launch_tiles<E, 4, 4, 2, 2>(A, stream);
+  return launch_tiles<E, 8, 4, 2, 4>(A, stream);
 }
 
 int matmul_e4m3(const uint8_t* x, int64_t x_row, const float* x_scale, int32_t x_group, const uint8_t* w,

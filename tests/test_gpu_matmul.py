@@ -134,3 +134,28 @@ def test_matmul_overflow_and_empty():
     # 448 * 448 * 128 = 49 * 2^19; bfloat16 holds it
     assert (lib.matmul_e4m3(x, one, w, one[:1]) == 448.0 * 448 * 128).all()
     assert lib.matmul_e4m3(x[:0], one[:0], w, one[:1]).shape == (0, 3)
+
+
+def test_matmul_of_one_row_or_column_of_tiles():
+    """Half a thousand million rows, or columns, next to few of the other: past what 64 x 64 tiles can be launched for.
+    Ones with a scale of their own: every output is known."""
+    import scoring_exact_top_amd as lib
+    big, one = 1 << 29, 0x38
+    scale = (torch.arange(big, device="cuda", dtype=torch.int32) % 251 + 1).float()
+    wide = torch.full((big + 70, 16), one, dtype=torch.uint8, device="cuda")
+    few, unit = torch.full((70, 16), one, dtype=torch.uint8, device="cuda"), torch.ones(1, 1, device="cuda")
+    for M, N in ((big, 1), (big + 70, 3)):
+        log("matmul rows", M, N)
+        xs = torch.cat([scale, scale[:M - big]]).view(-1, 1)
+        out = lib.matmul_e4m3(wide[:M], xs, few[:N], unit, out=torch.full((M, N), -1.0, dtype=torch.bfloat16, device="cuda"))
+        for n in range(N):
+            assert torch.equal(out[:, n], (16 * xs[:, 0]).bfloat16()), (M, N, n)
+        del out
+    for M, N in ((33, big), (64, big + 70)):
+        log("matmul columns", M, N)
+        ws = scale[:-(-N // 128)].view(-1, 1)
+        out = lib.matmul_e4m3(few[:M], unit.expand(M, 1).contiguous(), wide[:N], ws, out=torch.full((M, N), -1.0, dtype=torch.bfloat16, device="cuda"))
+        want = (16 * ws[:, 0]).bfloat16().repeat_interleave(128)[:N]
+        for m in range(M):
+            assert torch.equal(out[m], want), (M, N, m)
+        del out, want
