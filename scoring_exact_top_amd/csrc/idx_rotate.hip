@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256) void k_norm_rotate(RotArgs A) {
   typedef E v8 __attribute__((ext_vector_type(8)));
   const int tid = threadIdx.x, at = tid % LPR;
   const int64_t unit = workgroup() * (256 / LPR) + tid / LPR;
-  const uint32_t per = (uint32_t)(A.H + HP - 1) / HP;  // units of a token
+  const uint32_t per = ((uint32_t)A.H + (HP - 1)) / HP;  // units of a token
   const bool in = unit < A.units;
   const uint32_t t = in ? (uint32_t)unit / per : 0, head0 = in ? (uint32_t)unit % per * HP : 0;
   const int chunks = A.D >> 3, r0 = A.rope_at >> 3;
@@ -255,7 +255,7 @@ template <class E, bool QUANT>
 static void launch_rotate(RotArgs A, hipStream_t stream) {
   const int chunks = A.D >> 3;
   const bool many = (int64_t)A.T * A.H >= kManyRows && A.H >= 4;
-  A.units = (int64_t)A.T * (many && chunks <= 24 ? (A.H + 3) / 4 : A.H);
+  A.units = A.T * (many && chunks <= 24 ? ((int64_t)A.H + 3) / 4 : (int64_t)A.H);
   const auto grid = [&](int lpr) { return grid_of((A.units * lpr + 255) / 256); };
   if (chunks <= 8) {
     if (many) k_norm_rotate<E, 8, 1, 4, QUANT><<<grid(8), dim3(256), 0, stream>>>(A);

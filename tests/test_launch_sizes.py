@@ -95,3 +95,18 @@ def test_matmul_launches(tmp_path):
         tiles = -(-m // 128) * -(-n // 128) if m > 32 else -(-m // 16) * -(-n // 16)
         assert (g[0] == 0) == (tiles < 1 << 23), (m, n, g)
     assert all(g[0] == 0 for g in got[:served])
+
+
+def test_rotate_and_append_launches(tmp_path):
+    """Heads and tokens up to 2^31 - 1 of them: a wave of 64 lanes takes 8 x 4 heads of 64 numbers at most, or a token's rows."""
+    rng = random.Random(2)
+    most = (1 << 31) - 1
+    calls = [("rotate", 1, most - i, d) for i in range(5) for d in (64, 128, 192, 200, 1024)]
+    calls += [("rotate", most, 1, 128), ("rotate", most // 4, 4, 64), ("rotate", most // 5, 5, 192), ("rotate", most // 7, 7, 1000)]
+    for _ in range(200):
+        t = int(2 ** rng.uniform(0, 31))
+        calls.append(("rotate", t, max(1, int(2 ** rng.uniform(0, 31)) // t), 8 * rng.randint(8, 128)))
+    calls += [("append", t) for t in (1, 1000, 1 << 24, 1 << 30, most)]
+    for call, got in zip(calls, _launches(tmp_path, calls)):
+        assert got[0] == 0, call
+        _check(call, *got, least=call[1] * 64 if call[0] == "append" else call[1] * call[2] * 2)
