@@ -79,6 +79,14 @@ __device__ __forceinline__ uint32_t max_lanes(uint32_t x) {
   return x;
 }
 
+// sum / n rounded once, from 1 / n: the product, corrected by its own remainder.  A row of one number has that number as its
+// mean then (n of it sum exactly, 16-bit numbers and n up to 1024), and no spread; the product alone may be a step
+// beside it for an n that is no power of two, which without eps, or with large numbers, is all that is normed.
+__device__ __forceinline__ float mean_of(float sum, float n, float inv_n) {
+  const float q = sum * inv_n;
+  return fmaf(fmaf(-q, n, sum), inv_n, q);
+}
+
 // A row's norm: y = (x - mean) * (rstd * weight) + bias.
 struct Norm {
   float mean, rstd;
@@ -176,7 +184,7 @@ __global__ __launch_bounds__(256) void k_norm_rotate(RotArgs A) {
         for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int j = 0; j < 8; ++j) sum += h[c][j];
-        mean = sum_lanes<LPR>(sum) * A.inv_d;
+        mean = mean_of(sum_lanes<LPR>(sum), (float)A.D, A.inv_d);
       }
       sum = 0.f;
 #pragma unroll

@@ -128,6 +128,24 @@ def test_rotate_edges(norm):
         check_codes(codes[good], scales[good], y[good], off[good], norm)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_layer_norm_of_constant_heads(dtype):
+    """A head of one number throughout has no spread, at every width: zeros, with eps and without, and the bias where there is one."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator().manual_seed(6)
+    table = table_of(3)
+    for D in list(range(64, 265, 8)) + [384, 392, 576, 600, 648, 1000, 1016, 1024]:
+        log("constant heads", D, dtype)
+        x = (torch.randn(16, 4, 1, generator=g) * torch.exp2(torch.arange(16.0) - 8)[:, None, None]).to(dtype).expand(16, 4, D).contiguous()
+        pos = torch.zeros(16, dtype=torch.int32)
+        b = torch.randn(D, generator=g).to(dtype)
+        for eps in (0.0, 1e-6):
+            out = lib.norm_rotate(x.cuda(), pos.cuda(), table.cuda(), 0, norm="layer", eps=eps)
+            assert (out == 0).all(), (D, eps)
+            out = lib.norm_rotate(x.cuda(), pos.cuda(), table.cuda(), 0, norm="layer", weight=_cuda(b), bias=_cuda(b), eps=eps)
+            assert (out == b.cuda()).all(), (D, eps)
+
+
 def test_rotate_empty():
     import scoring_exact_top_amd as lib
     t = table_of(10).cuda()
