@@ -372,8 +372,8 @@ int idx_topk_decode_paged_noalloc(const uint8_t *q, const float *q_scale, const 
  *   RMS    x / sqrt(mean(x^2) + eps) * weight + bias
  *   LAYER  (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * weight + bias
  * weight NULL: ones, bias NULL: zeros; both NULL and eps not looked at with NONE.  A row that is zero
- * (after the mean's subtraction) with eps = 0 counts as normed.  A NaN or an infinity in a row, or
- * squares that leave FP32, make its numbers NaN. */
+ * (after the mean's subtraction) with eps = 0 counts as normed.  Rows whose squares leave FP32 on
+ * either side are normed as any other.  A NaN or an infinity in a row makes its numbers NaN. */
 #define IDX_TOPK_NORM_NONE 0
 #define IDX_TOPK_NORM_RMS 1
 #define IDX_TOPK_NORM_LAYER 2

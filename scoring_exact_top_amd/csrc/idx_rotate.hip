@@ -87,20 +87,67 @@ __device__ __forceinline__ float mean_of(float sum, float n, float inv_n) {
   return fmaf(fmaf(-q, n, sum), inv_n, q);
 }
 
-// A row's norm: y = (x - mean) * (rstd * weight) + bias.
+// A row's norm: y = (x 2^shift - mean) * (rstd * weight) + bias, the row's numbers scaled already where it is made.
 struct Norm {
   float mean, rstd;
-  // rstd from the mean square: NaN for a row with a NaN or an infinity, or whose squares leave FP32.  The
-  // instruction is within one unit of the last place and takes no subnormal numbers.
-  __device__ __forceinline__ Norm(float mean, float ms)
-      : mean(mean), rstd(ms < INFINITY ? (ms > 0x1p-100f ? __builtin_amdgcn_rsqf(ms) : 1.f / sqrtf(ms)) : NAN) {}
-  // Mean square 0 (without eps): zeros stay zeros, and numbers whose squares are lost have no norm.
-  __device__ __forceinline__ float operator()(float x, float w, float b) const {
-    x -= mean;
-    const float y = fmaf(x, rstd * w, b);
-    return rstd < INFINITY || rstd != rstd ? y : fmaf(x == 0.f ? 0.f : INFINITY, w, b);
-  }
+  int shift;
+  // The instruction is within one unit of the last place and takes no subnormal numbers.  Below them is only a row without
+  // spread, where rstd does not count and must not be infinite.
+  __device__ __forceinline__ Norm(float mean, float ms, int shift = 0)
+      : mean(mean), rstd(ms < INFINITY ? (ms >= 0x1p-126f ? __builtin_amdgcn_rsqf(ms) : 1.f) : NAN), shift(shift) {}
+  __device__ __forceinline__ float operator()(float x, float w, float b) const { return fmaf(x - mean, rstd * w, b); }
 };
+
+// Mean (0 without `layer`) and sum of squares of a row of d numbers (inv_d = 1 / d), NC x W of them in each of L lanes,
+// of which those count whose first index `there` takes (the others are zero).
+template <int L, int NC, int W, class F>
+__device__ __forceinline__ void moments(const float (&h)[NC][W], const F& there, bool layer, float d, float inv_d, float& mean, float& squares) {
+  float sum = 0.f;
+  mean = 0.f;
+  if (layer) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int j = 0; j < W; ++j) sum += h[c][j];
+    mean = mean_of(sum_lanes<L>(sum), d, inv_d);
+  }
+  sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float x = there(c) ? h[c][j] - mean : 0.f;
+      sum = fmaf(x, x, sum);
+    }
+  squares = sum_lanes<L>(sum);
+}
+
+// The norm of a row.  bfloat16's numbers go from 2^-133 to 2^128, and so their squares leave FP32 on both sides: where
+// the mean square is so small that FP32 may have lost numbers of it (the smallest square to keep all bits is 2^-126), or has
+// passed its end, the row is scaled by the power of two that brings its largest number, or the root of eps, to about 1.
+// NaN for a row with a NaN or an infinity.
+template <int L, int NC, int W, class F>
+__device__ __forceinline__ Norm norm_of(float (&h)[NC][W], const F& there, bool layer, float d, float inv_d, float eps) {
+  float mean, squares;
+  moments<L>(h, there, layer, d, inv_d, mean, squares);
+  const float ms = fmaf(squares, inv_d, eps);
+  if (ms > 0x1p-100f && ms < INFINITY) return Norm(mean, ms);
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < W; ++j) top = max(top, magnitude(h[c][j]));
+  top = max_lanes<L>(top);
+  if (!finite(top)) return Norm(0.f, NAN);
+  const int of_row = __builtin_amdgcn_frexp_expf(__uint_as_float(top)), of_eps = (__builtin_amdgcn_frexp_expf(eps) + 1) >> 1;
+  const int shift = top == 0 ? (eps > 0.f ? -of_eps : 0) : -(eps > 0.f ? max(of_row, of_eps) : of_row);
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+#pragma unroll
+    for (int j = 0; j < W; ++j) h[c][j] = __builtin_amdgcn_ldexpf(h[c][j], shift);
+  moments<L>(h, there, layer, d, inv_d, mean, squares);
+  return Norm(mean, fmaf(squares, inv_d, __builtin_amdgcn_ldexpf(eps, 2 * shift)), shift);
+}
 
 // Rows (a head of a token) in chunks of 8 numbers, one 16-byte load each: LPR lanes a row, NC
 // chunks a lane, HP heads of one token one after another, which share position and angles.  At
@@ -178,23 +225,7 @@ __global__ __launch_bounds__(256) void k_norm_rotate(RotArgs A) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = (float)pv[k][j];
     if (A.norm != IDX_TOPK_NORM_NONE) {
-      float sum = 0.f, mean = 0.f;
-      if (A.norm == IDX_TOPK_NORM_LAYER) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sum += h[c][j];
-        mean = mean_of(sum_lanes<LPR>(sum), (float)A.D, A.inv_d);
-      }
-      sum = 0.f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = at + c * LPR < chunks ? h[c][j] - mean : 0.f;
-          sum = fmaf(d, d, sum);
-        }
-      const Norm norm(mean, fmaf(sum_lanes<LPR>(sum), A.inv_d, A.eps));
+      const Norm norm = norm_of<LPR>(h, [&](int c) { return at + c * LPR < chunks; }, A.norm == IDX_TOPK_NORM_LAYER, (float)A.D, A.inv_d, A.eps);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int i = at + c * LPR;
@@ -202,6 +233,9 @@ __global__ __launch_bounds__(256) void k_norm_rotate(RotArgs A) {
         for (int j = 0; j < 8; ++j) h[c][j] = i < chunks ? norm(h[c][j], (float)wv[c][j], (float)bv[c][j]) : 0.f;
       }
       if (turns && halves) {
+        if (norm.shift != 0)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) p[j] = __builtin_amdgcn_ldexpf(p[j], norm.shift);
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[j] = norm(p[j], (float)pw[j], (float)pb[j]);
       }
@@ -359,12 +393,12 @@ __global__ __launch_bounds__(256) void k_append_rotary(AppendRotArgs A) {
       if (out) out[64 + lane] = y;
     }
     if (A.latent_norm != IDX_TOPK_NORM_NONE) {
-      float sum = 0.f;
+      float h[1][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf((float)xv[j], (float)xv[j], sum);
-      const Norm norm(0.f, fmaf(sum_lanes<64>(sum), 1.f / kLatent, A.latent_eps));
+      for (int j = 0; j < 8; ++j) h[0][j] = (float)xv[j];
+      const Norm norm = norm_of<64>(h, [](int) { return true; }, false, kLatent, 1.f / kLatent, A.latent_eps);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xv[j] = (E)norm((float)xv[j], A.latent_weight ? (float)wv[j] : 1.f, 0.f);
+      for (int j = 0; j < 8; ++j) xv[j] = (E)norm(h[0][j], A.latent_weight ? (float)wv[j] : 1.f, 0.f);
     }
     dst[lane] = xv;
     if (out) out[lane] = xv;
@@ -372,10 +406,10 @@ __global__ __launch_bounds__(256) void k_append_rotary(AppendRotArgs A) {
   if (A.k_cache) {
     float a = (float)kv[0], b = (float)kv[1];
     if (A.key_norm != IDX_TOPK_NORM_NONE) {
-      const float mean = A.key_norm == IDX_TOPK_NORM_LAYER ? sum_lanes<64>(a + b) * (1.f / kD) : 0.f;
-      const Norm norm(mean, fmaf(sum_lanes<64>(fmaf(a - mean, a - mean, (b - mean) * (b - mean))), 1.f / kD, A.key_eps));
-      a = norm(a, A.key_weight ? (float)kw[0] : 1.f, (float)kb[0]);
-      b = norm(b, A.key_weight ? (float)kw[1] : 1.f, (float)kb[1]);
+      float h[1][2] = {{a, b}};
+      const Norm norm = norm_of<64>(h, [](int) { return true; }, A.key_norm == IDX_TOPK_NORM_LAYER, kD, 1.f / kD, A.key_eps);
+      a = norm(h[0][0], A.key_weight ? (float)kw[0] : 1.f, (float)kb[0]);
+      b = norm(h[0][1], A.key_weight ? (float)kw[1] : 1.f, (float)kb[1]);
     }
     const int c = lane - A.key_rope_at / 2;  // this lane's two numbers of the rotary part
     const bool turns = c >= 0 && c < kRope / 2;

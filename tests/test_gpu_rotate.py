@@ -146,6 +146,48 @@ def test_layer_norm_of_constant_heads(dtype):
             assert (out == b.cuda()).all(), (D, eps)
 
 
+# Numbers of a head: their size, or the powers of two they are spread over.  bfloat16's smallest number is 2^-133; the
+# squares of the first rows are below FP32's numbers, those of the last ones above.
+SIZES = [2.0 ** -132, 2.0 ** -126, 1e-30, 3e-23, 1e-21, 2.0 ** -60, 2.0 ** -50, 2.0 ** -49, 1e-12, 1.0, 2.0 ** 60, 1e19, 1e25, 1e38]
+
+
+def _sized(g, shape):
+    """Rows [len(SIZES) + 4, *shape] of these sizes, both signs and zeros among them; constant ones; one number beside zeros; a
+    spread over all of bfloat16."""
+    x = torch.randn(len(SIZES) + 4, *shape, generator=g, dtype=torch.double).clamp(-3, 3)
+    x[:, ..., 3] = 0
+    for i, size in enumerate(SIZES):
+        x[i] *= size
+    x[-4], x[-3] = 1000, 3e-23
+    x[-2] = 0
+    x[-2, ..., 5] = -2.0 ** -133
+    x[-1] = torch.sign(x[-1]) * torch.exp2(torch.randint(-133, -60, x[-1].shape, generator=g).double())
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("H,D,at", [(5, 64, 0), (3, 128, 32), (2, 200, 136), (1, 1000, 8)])
+def test_rotate_of_any_size(H, D, at, norm):
+    """The norm's own numbers for rows whose squares FP32 does not hold, with eps = 0 and beside a small or large eps."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator().manual_seed(D)
+    x = _sized(g, (H, D))
+    table = table_of(100)
+    pos = torch.randint(0, 100, (len(x),), generator=g).to(torch.int32)
+    for eps in (0.0, 1e-42, 1e-36, 1e-6):
+        for ww, bb in (_vectors(g, D, norm, torch.bfloat16), (None, None)):
+            log("rotate sizes", H, D, at, norm, eps, ww is not None)
+            for interleaved in (False, True):
+                held = torch.tensor(eps, dtype=torch.float32).double().item()   # what the call takes: FP32
+                # a constant row has no spread, and no norm without eps: zeros
+                y, off = rotated(*(t.nan_to_num(0, 0, 0) for t in normed(x.double(), norm, ww, bb, max(held, 1e-300))), at, interleaved, table[pos.long()])
+                args = (x.cuda(), pos.cuda(), table.cuda(), at)
+                more = dict(interleaved=interleaved, norm=norm, weight=_cuda(ww), bias=_cuda(bb), eps=eps)
+                check_rounded(lib.norm_rotate(*args, **more), y, off, "%s %s %g" % (norm, interleaved, eps))
+                # scales below FP32's normal numbers are rounded to multiples of 2^-149
+                check_codes(*lib.norm_rotate_quant(*args, **more), y, off + 448 * 2.0 ** -150, "%s %s %g codes" % (norm, interleaved, eps))
+
+
 def test_rotate_empty():
     import scoring_exact_top_amd as lib
     t = table_of(10).cuda()
@@ -264,3 +306,28 @@ def test_append_rotary_not_finite():
         assert torch.isnan(codes[bad]).all() and torch.isfinite(codes[~bad]).all() and (ks[0, :8][bad] == 1).all()
         rows = torch.isfinite(cache[0, :8])
         assert rows[[0, 2, 3, 4, 5, 7]].all() and rows[1, 512:].all() and not rows[1, :512].all() and rows[6, :512].all() and not rows[6, 512:].all()
+
+
+def test_append_rotary_of_any_size():
+    """Latents and keys whose squares FP32 does not hold, with eps = 0 and without."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator().manual_seed(10)
+    lat, key = _sized(g, (576,)), _sized(g, (128,))
+    lat[:, 512:] = torch.randn(len(lat), 64, generator=g).to(torch.bfloat16)
+    T = len(lat)
+    table, pos, slots = table_of(100), torch.randint(0, 100, (T,), generator=g).to(torch.int32), torch.randperm(64, generator=g)[:T].to(torch.int32)
+    lw = (1 + 0.3 * torch.randn(512, generator=g)).to(torch.bfloat16)
+    for key_norm in ("rms", "layer"):
+        kw, kb = _vectors(g, 128, key_norm, torch.bfloat16)
+        for eps in (0.0, 1e-42, 1e-6):
+            log("append sizes", key_norm, eps)
+            held = max(torch.tensor(eps, dtype=torch.float32).double().item(), 1e-300)
+            cache, kc, ks = torch.zeros(1, 64, 576, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 64, 128, dtype=torch.uint8, device="cuda"), torch.zeros(1, 64, device="cuda")
+            lib.cache_append_rotary(lat.cuda(), key.cuda(), slots.cuda(), pos.cuda(), table.cuda(), cache, kc, ks, latent_weight=lw.cuda(), latent_eps=eps,
+                                    key_norm=key_norm, key_weight=kw.cuda(), key_bias=kb.cuda(), key_eps=eps, key_rope_at=40)
+            to, angles, x = slots.long().cuda(), table[pos.long()], lat.double()
+            y, off = normed(x[:, :512], "rms", lw, None, held)
+            y, off = rotated(torch.cat([y, x[:, 512:]], 1), torch.cat([off, torch.zeros(T, 64)], 1), 512, True, angles)
+            check_rounded(cache[0][to], y, off, "rows %g" % eps)
+            y, off = rotated(*(t.nan_to_num(0, 0, 0) for t in normed(key.double(), key_norm, kw, kb, held)), 40, False, angles)
+            check_codes(kc[0][to].view(torch.float8_e4m3fn), ks[0][to], y, off + 448 * 2.0 ** -150, "keys %g" % eps)
