@@ -188,6 +188,51 @@ def test_rotate_of_any_size(H, D, at, norm):
                 check_codes(*lib.norm_rotate_quant(*args, **more), y, off + 448 * 2.0 ** -150, "%s %s %g codes" % (norm, interleaved, eps))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("H,D,at", [(4, 64, 0), (5, 128, 64), (6, 192, 128), (7, 72, 8), (13, 136, 40), (40, 128, 0), (4, 184, 120), (9, 64, 0)])
+def test_rotate_of_many_heads(H, D, at, dtype):
+    """Enough heads that a lane group takes four of them, the last of a token fewer: against the definition, and bit for bit
+    what fewer tokens at a time give; strided, in place, to codes; padded tokens and what lies between are left alone."""
+    import scoring_exact_top_amd as lib
+    T = (1 << 14) // H + 5
+    half = T // 2
+    assert T * H >= 1 << 14 > max(half, T - half) * H
+    g = torch.Generator().manual_seed(H * D)
+    table = table_of(1000)
+    pos = torch.randint(0, 1000, (T,), generator=g).to(torch.int32)
+    pos[::97], pos[1::97], pos[T - 1] = -1, 1000, -2 ** 31
+    there = (pos >= 0) & (pos < 1000)
+    wide = torch.randn(T, H + 1, 2, D, generator=g).to(dtype)
+    wide[::3, 1] *= 30
+    x = wide[:, 1:, 1]                                        # strides (H + 1) 2 D and 2 D
+    there_c, pos_c, table_c, wide_c = there.cuda(), pos.cuda(), table.cuda(), wide.cuda()
+    for norm in ("none", "rms", "layer"):
+        w, b = _vectors(g, D, norm, dtype)
+        for interleaved in (False, True):
+            log("many heads", T, H, D, at, dtype, norm, interleaved)
+            y, off = rotated(*normed(x.double(), norm, w, b, 1e-5), at, interleaved, table[pos.clamp(0, 999).long()])
+            more = dict(interleaved=interleaved, norm=norm, weight=_cuda(w), bias=_cuda(b), eps=1e-5)
+            target = torch.full((T, H, D + 24), 7.0, dtype=dtype, device="cuda")
+            lib.norm_rotate(wide_c[:, 1:, 1], pos_c, table_c, at, out=target[..., 8:8 + D], **more)
+            got = target[..., 8:8 + D]
+            check_rounded(got[there_c], y[there], off[there], "%s %s" % (norm, interleaved))
+            assert (target[~there_c] == 7).all() and (target[..., :8] == 7).all() and (target[..., 8 + D:] == 7).all()
+            place = wide_c.clone()
+            lib.norm_rotate(place[:, 1:, 1], pos_c, table_c, at, out=place[:, 1:, 1], **more)
+            assert torch.equal(place[:, 1:, 1][there_c], got[there_c]) and torch.equal(place[~there_c], wide_c[~there_c])
+            assert torch.equal(place[:, 0], wide_c[:, 0]) and torch.equal(place[:, :, 0], wide_c[:, :, 0])
+            codes, scales = torch.full((T, H, D), 3.0, device="cuda").to(torch.float8_e4m3fn), torch.full((T, H), -7.0, device="cuda")
+            lib.norm_rotate_quant(wide_c[:, 1:, 1], pos_c, table_c, at, codes=codes, scales=scales, **more)
+            check_codes(codes[there_c], scales[there_c], y[there], off[there], "%s %s codes" % (norm, interleaved))
+            assert (codes[~there_c].float() == 3).all() and (scales[~there_c] == -7).all()
+            for part in (slice(0, half), slice(half, T)):
+                live = there_c[part]
+                few = lib.norm_rotate(wide_c[part, 1:, 1], pos_c[part], table_c, at, **more)
+                assert torch.equal(few[live], got[part][live])
+                few, few_scales = lib.norm_rotate_quant(wide_c[part, 1:, 1], pos_c[part], table_c, at, **more)
+                assert torch.equal(few[live].view(torch.uint8), codes[part][live].view(torch.uint8)) and torch.equal(few_scales[live], scales[part][live])
+
+
 def test_rotate_empty():
     import scoring_exact_top_amd as lib
     t = table_of(10).cuda()
