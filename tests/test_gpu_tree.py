@@ -207,6 +207,53 @@ def test_tree_stream_of_ragged_blocks():
     assert torch.equal(out, again) and torch.equal(lse, again_lse)
 
 
+# Batches that are shared out in several passes of 64 sequences: sequences, nodes, heads, long ones, runs without drafts
+PLANNED = [
+    # few blocks in all: each cut into parts of its own
+    (65, 1, 16, (63, 64), [(3, 20)]),
+    (65, 2, 5, (64,), [(0, 60)]),
+    (128, 1, 16, (63, 64, 127), [(10, 30), (65, 80)]),
+    (128, 3, 4, (127,), [(0, 127)]),
+    (200, 1, 16, (63, 128, 199), [(50, 60), (70, 100)]),
+    (200, 2, 8, (0, 64, 198), [(180, 192)]),
+    (1024, 2, 8, (64, 700, 1023), [(0, 60), (66, 640), (705, 950)]),
+    # many, or few beside long ones: a stream of pages, whose shares go on from one sequence to the next, over runs without drafts too
+    (65, 64, 32, (63, 64), [(30, 60)]),
+    (128, 16, 128, (64,), [(40, 62), (66, 126)]),
+    (200, 16, 64, (63, 128, 199), [(60, 63), (64, 128), (150, 199)]),
+    (200, 16, 32, (199,), [(0, 3)]),
+    (1024, 4, 64, (63, 64, 1023), [(100, 300), (301, 1000)]),
+    (1024, 2, 128, (0, 512), [(513, 1024)]),
+    (1024, 3, 64, (), []),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n", range(len(PLANNED)))
+def test_tree_plan_of_many_sequences(n, dtype):
+    B, S, H, long, runs = PLANNED[n]
+    g = torch.Generator().manual_seed(20 + n)
+    prefix = [int(v) for v in torch.randint(0, 150, (B,), generator=g)]
+    counts = [int(v) if b % 11 else 0 for b, v in enumerate(torch.randint(1, S + 1, (B,), generator=g))]
+    for first, last in runs:
+        counts[first:last] = [0] * (last - first)
+    for b in long:
+        prefix[b], counts[b] = 2500 + 64 * (b % 5) + b % 64, S
+    log("tree plan", B, S, H, long, runs, dtype)
+    q, cache, table, masks = _case(prefix, counts, S, H, dtype, 30 + n)
+    out, lse = torch.full((B, S, H, 512), 7.0, dtype=dtype, device="cuda"), torch.full((B, S, H), 7.0, device="cuda")
+    _call(q, cache, table, prefix, counts, masks, out=out, lse=lse)
+    edges = {e + d for e in [0, B - 1, *range(64, B, 64)] for d in (-2, -1, 0, 1)} | set(long) | {b for r in runs for b in (r[0] - 1, r[0], r[1] - 1, r[1])}
+    some = sorted({b for b in edges if 0 <= b < B} | set(range(0, B, 29)))
+    pick = lambda t: [t[b] for b in some]  # noqa: E731
+    _check(out[some], lse[some], q[some], cache, table[some], pick(prefix), pick(counts), pick(masks), nodes=sorted({0, S // 2, S - 1}), where="plan %d" % n)
+    gone = (torch.arange(S)[None] >= torch.tensor(counts)[:, None]).cuda()
+    assert (out[gone] == 0).all() and (lse[gone] == -math.inf).all()
+    assert torch.isfinite(lse[~gone]).all() and (lse[~gone] != 7).all() and (out[~gone] != 7).any(-1).all()
+    again, again_lse = _call(q, cache, table, prefix, counts, masks)
+    assert torch.equal(out, again) and torch.equal(lse, again_lse)
+
+
 def test_tree_many_sequences():
     """Batches past the one that is shared out: a workgroup a block, padding rows written by it."""
     g = torch.Generator().manual_seed(10)
