@@ -593,8 +593,10 @@ int idx_topk_cache_append_rotary(const void *latents, int64_t latent_token, int3
  * x, w and out 16-byte aligned; K at most 2^24.  A block's sum is the matrix cores': FP32 over groups of
  * eight neighbouring columns, in which each product is cut off 13 binary places below the leading
  * one of the largest (measured; for random numbers 1.5e-5 of the result, a hundredth of
- * bfloat16's rounding).  It is scaled and added to the others in FP32 and the result is rounded
- * once; sums that leave the output's type are infinities.  NaN codes
+ * bfloat16's rounding).  A group is so off by up to 2^-10 of its largest product: where that one is
+ * cancelled by another group's, small products beside it are lost.  A block's sum is scaled by
+ * x_scale * w_scale (in FP32, which has to hold it) and added to the others in FP32, and the result is
+ * rounded once; sums that leave the output's type are infinities.  NaN codes
  * (those of idx_topk_norm_quant for a row with a NaN) make the outputs they enter NaN, and no others.
  * The result does not depend on timing.  Calls of 2^23 tiles of 128 x 128 (M up to 32: of 16 x 16) and more are
  * IDX_EUNSUPPORTED.  No workspace.

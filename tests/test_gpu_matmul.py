@@ -124,6 +124,27 @@ def test_matmul_exact_integers():
         assert torch.equal(out.double().cpu(), want.half().double()), (M, N, K)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_matmul_of_cancelling_products(dtype):
+    """One product far above the others in each group of eight, which the next group takes away again: what is left is the sum of
+    small ones, each cut off against its group's largest, and within the stated bound; groups without a large one keep theirs."""
+    import scoring_exact_top_amd as lib
+    g = torch.Generator().manual_seed(14)
+    for M, N, K in ((3, 70, 272), (25, 9000, 272), (150, 200, 400), (1520, 1500, 656), (3601, 3590, 256)):
+        log("matmul cancelling", M, N, K, dtype)
+        x, w = (torch.randn(n, K, generator=g) * torch.exp2(torch.randint(-8, 1, (n, K), generator=g).float()) for n in (M, N))
+        k = torch.arange(0, K - 15, 32)                       # two groups of every four
+        x[:, k + 3], x[:, k + 8 + 5] = 448.0, 448.0
+        w[:, k + 3], w[:, k + 8 + 5] = 448.0, -448.0
+        x, w = x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+        B = -(-K // 128)
+        xs, ws = torch.exp(torch.randn(M, B, generator=g)), torch.exp(torch.randn(-(-N // 128), B, generator=g))
+        _check(lib.matmul_e4m3(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), dtype=dtype), x, xs, w, ws, "%d %d %d" % (M, N, K))
+        # without the large ones the same small products are kept to a step of the output's type
+        x[:, k + 3] = x[:, k + 8 + 5] = torch.zeros(1).to(torch.float8_e4m3fn)
+        _check(lib.matmul_e4m3(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), dtype=dtype), x, xs, w, ws, "%d %d %d without" % (M, N, K))
+
+
 def test_matmul_overflow_and_empty():
     import scoring_exact_top_amd as lib
     x = torch.full((2, 128), 448.0).to(torch.float8_e4m3fn).cuda()
