@@ -24,8 +24,8 @@
 //                                                  power leaves; 3.4 TB/s, 820 TFLOP/s; join 13
 //   16 tokens x 64 heads x 2048 of 262144 rows      24 us  walk 18, join 6: latency, partial results
 //   one token, 128 heads, 2048 rows                 15 us  walk 11, join 3: latency
-//   trees of 20 nodes, 16 sequences to 32768 keys,  768 us  833 TFLOP/s; walk 752 at least: LDS traffic as above;
-//   128 heads (741 on another card)                        join 31
+//   trees of 20 nodes, 16 sequences to 32768 keys,  742 to 768 us by the card, 833 TFLOP/s and more; walk 752 at least
+//   128 heads                                              alone: LDS traffic as above; join 31
 //   a tree of 12 nodes, 4000 keys, 64 heads         32 us  walk 26, join 6: latency of the plan, q, the first tiles
 //   40 trees of 7 nodes, 1500 keys, 20 heads        32 us  walk 25, join 8: the same
 #include <type_traits>

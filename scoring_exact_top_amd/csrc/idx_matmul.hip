@@ -13,11 +13,12 @@
 // together.  Both operands are laid out alike (lane l has bytes 32 (l / 16) .. + 32 of row l % 16).
 //
 // Measured, and what bounds it (rows x columns x k; a call in a loop, the kernel alone in brackets):
-//   1 x 7680 x 5120          7.6 us (8.1)   memory, 5.2 TB/s, and the host's work for a launch
-//   16 x 12288 x 5120       11.7 us (12.3)  memory, 5.4 TB/s
-//   777 x 768 x 5120        11.7 us (12.6)  a block's way into LDS (64 bytes a clock), 208 of 256 units with one tile each
-//   4096 x 12288 x 5120  223-229 us         2280 TFLOP/s; matrix cores 60% busy: the additions of scaled sums take issue
-//                                           slots beside them (without: 77%), LDS reads and loads about as many clocks
+//   1 x 7680 x 5120          7.6 us (8.2)   memory, 5.2 TB/s, and the host's work for a launch
+//   16 x 12288 x 5120       11.7 us (12.2)  memory, 5.4 TB/s
+//   777 x 768 x 5120        11.7 us (12.5)  a third a block's way into LDS (64 bytes a clock; 208 of 256 units have one tile
+//                                           each), the rest its latency: a wave has one block on its way
+//   4096 x 12288 x 5120  221-229 us         2280 TFLOP/s; matrix cores 61% busy; without the additions of scaled sums, which
+//                                           take issue slots beside them, 199 us and 64%: LDS reads and loads as many clocks
 #include <type_traits>
 #include "idx_attn.hpp"
 #include "idx_common.hpp"
@@ -423,12 +424,14 @@ static int launch_tiles(const MatArgs& A, hipStream_t stream) {
 }
 
 // Up to 32 rows the weights are streamed: as many columns a workgroup as leave one to a unit.  More rows take tiles of
-// 32 x 32 too where those are one to a unit (128 x 1536 x 7168: 9.4 us, with 64 x 64 14.8).  Beyond that the tile is
+// 32 x 32 too where those are one to a unit (128 x 1536 x 7168: 9.3 us, with 48 x 64 14.5).  Beyond that the tile is
 // the one whose rounds over the chip take the least: a block of a round takes about 0.25 us with 64 x 64, 0.63 with
 // 128 x 128 (two of which share a unit, so that beyond the first round each half one counts for itself) and 1.9 with
-// 256 x 256.  Measured, in us with the three tiles: 777 x 768 x 5120 15, 27 and 65; 300 x 12288 x 5120 58, 48 and 74;
-// 1024 x 4096 x 5120 57, 28 and 68; 4096 x 12288 x 5120 660, 302 and 223.  48 columns instead of 64 where that is one
-// round too: 13.3 against 14.7 us for 777 x 768 x 5120 (neither folded).
+// 256 x 256.  Measured, in us with the three tiles: 777 x 768 x 5120 13.4, 27 and 55; 300 x 12288 x 5120 56, 47 and 60;
+// 1024 x 4096 x 7168 63, 38 and 73; 4096 x 12288 x 5120 660, 302 and 223.  48 columns instead of 64 where that is one
+// round too: 12.5 against 13.4 us for 777 x 768 x 5120, 15.0 against 16.2 for 400 x 1536 x 7168 (as folded as the rule
+// has them).  Of 77 sizes with 33 to 1024 rows the rule is within 5% of the best of the five tiles in 63, and furthest
+// behind where k is short and few rows meet many columns (64 x 24576 x 1536: 14.6 us, 11.8 with 128 x 128).
 template <class E>
 static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   const auto tiles = [&](int64_t n, int64_t m) { return ((A.N + n - 1) / n) * ((A.M + m - 1) / m); };

@@ -14,11 +14,11 @@
 // position 65536.
 //
 // Measured (a call in a loop, the kernel alone in brackets):
-//   4096 tokens x 64 heads of 128 to codes    24.3 us (25.5)  103 MB at 4.2 TB/s
-//   3001 tokens x 40 heads of 128, normed     17.7 us (19.0)  62 MB at 3.5 TB/s
-//   16 tokens x 128 heads of 192               7.4 us (3.5)   the host's work for a launch
-//   append of 30000 tokens, rows returned     27.2 us (27.6)  123 MB at 4.5 TB/s
-//   append of 16 tokens                       10.3 us (3.5)   the host's work for a launch
+//   4096 tokens x 64 heads of 128 to codes    23.8 us (25.8)  103 MB at 4.3 TB/s
+//   3001 tokens x 40 heads of 128, normed     15.7 us (16.7)  62 MB at 4.0 TB/s
+//   16 tokens x 128 heads of 192               7.4 us (3.4)   the host's work for a launch
+//   append of 30000 tokens, rows returned     25.5 us (26.0)  123 MB at 4.8 TB/s
+//   append of 16 tokens                       10.5 us (3.4)   the host's work for a launch
 #include "idx_attn.hpp"
 #include "idx_latent.hpp"
 #include "idx_quant.hpp"
