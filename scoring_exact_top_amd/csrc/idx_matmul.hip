@@ -438,7 +438,7 @@ static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   const auto rounds = [&](int64_t size, int64_t units) { return (tiles(size, size) + units - 1) / units; };
   const int64_t half = rounds(128, kUnits / 2);
   const int64_t c64 = 50 * rounds(64, kUnits), c128 = 63 * (half < 2 ? 2 : half), c256 = 380 * rounds(256, kUnits);
-  // larger calls are refused: rows and columns stay so far below 2^31 that a tile's end is one too
+  // larger calls are refused: what is left has rows, columns and the ends of their tiles in 32 bits
   if ((A.M <= 32 ? tiles(16, 16) : tiles(128, 128)) > 0x7fffff) return IDX_EUNSUPPORTED;
   if (A.M <= 16) {
     if (A.N <= 16 * kUnits) return launch_few<E, 1, 1, 8, 4>(A, stream);
@@ -447,7 +447,7 @@ static int launch_matmul(const MatArgs& A, hipStream_t stream) {
   }
   if (tiles(32, 32) <= kUnits) return launch_few<E, 2, 2, 8, 2>(A, stream);
   if (A.M <= 32) return launch_few<E, 4, 2, 4, 3>(A, stream);
-  // one row or column of tiles 64 wide has half the workgroups with 128 x 128, and half the threads in each
+  // one row or column of tiles can be too long for a launch of 64 x 64 ones: 128 x 128 take half as many workgroups of half the threads
   if (c64 <= c128 && c64 <= c256 && fits(tiles(64, 64), 8)) {
     if (tiles(48, 64) <= kUnits) return launch_few<E, 3, 4, 8, 1>(A, stream);
     return launch_few<E, 4, 4, 8, 1>(A, stream);
